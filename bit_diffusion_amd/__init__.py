@@ -12,8 +12,8 @@ import os
 from . import _abi
 from ._abi import (SVDQ_OK, SVDQ_ERR_INVALID_ARG, SVDQ_ERR_UNSUPPORTED_DEVICE,  # noqa: F401
                    SVDQ_ERR_UNSUPPORTED_CONFIG, SVDQ_ERR_LAUNCH, SVDQ_PREC_INT4, SVDQ_PREC_NVFP4,
-                   SVDQ_DT_F32, SVDQ_DT_BF16, SVDQ_ACT_NONE, SVDQ_ACT_GELU_TANH, LayerCfg,
-                   SvdqError, lib, LIB_PATH)
+                   SVDQ_DT_F32, SVDQ_DT_BF16, SVDQ_ACT_NONE, SVDQ_ACT_GELU_TANH,
+                   SVDQ_ACT_SILU, LayerCfg, SvdqError, lib, LIB_PATH)
 
 __all__ = [
     "svdq_quantize_act", "svdq_gemm_w4a4", "awq_gemm_w4a16", "svdq_check_device",
@@ -25,7 +25,8 @@ __all__ = [
     "svdq_gemm_w4a4_packed_workspace_bytes", "svdq_gemm_w4a4_packed_ws",
     "svdq_quantize_next_workspace_bytes", "svdq_peak_mfma", "svdq_peak_copy",
     "svdq_gemm_w4a4_packed_noalloc", "svdq_peak_read",
-    "svdq_check_arch", "svdq_status_string", "svdq_last_error", "svdq_version", "LayerCfg",
+    "svdq_lora_batch_workspace_bytes", "svdq_lora_batch", "svdq_group_norm_workspace_bytes",
+    "svdq_group_norm", "svdq_check_arch", "svdq_status_string", "svdq_last_error", "svdq_version", "LayerCfg",
     "SvdqError", "lib", "LIB_PATH",
 ]
 
@@ -36,6 +37,21 @@ def _ptr(t):
         return None
     if isinstance(t, int):
         return t
+    return t.data_ptr()
+
+
+def _dev_ptr(t, name):
+    """As _ptr, for a buffer that a kernel reads or writes: a tensor elsewhere than on the
+    current device is refused before its address reaches one."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise SvdqError(SVDQ_ERR_INVALID_ARG, f"{name} is on {t.device}, not on a GPU")
+    import torch
+    if t.device.index != torch.cuda.current_device():
+        raise SvdqError(SVDQ_ERR_INVALID_ARG,
+                        f"{name} is on {t.device}, not on the current device "
+                        f"cuda:{torch.cuda.current_device()}")
     return t.data_ptr()
 
 
@@ -203,6 +219,43 @@ def svdq_lowrank_factors(cfg, w, smooth_inv, omega, block, iters, l1, l2, sigma,
     return _check(lib().svdq_lowrank_factors(ctypes.byref(cfg), _ptr(w), _ptr(smooth_inv),
                                              _ptr(omega), int(block), int(iters), _ptr(l1), _ptr(l2),
                                              _ptr(sigma), _ptr(workspace), _stream(stream)))
+
+
+def svdq_lora_batch_workspace_bytes(M, K, N, max_rank, n_segments):
+    n = ctypes.c_int64(0)
+    _check(lib().svdq_lora_batch_workspace_bytes(int(M), int(K), int(N), int(max_rank),
+                                                 int(n_segments), ctypes.byref(n)))
+    return n.value
+
+
+def svdq_lora_batch(M, K, N, max_rank, n_adapters, n_segments, x, x_stride, lora_down, lora_up, alphas,
+                    ranks, seg_start, seg_adapter, base, base_stride, act, out_dtype, out, out_stride,
+                    workspace, workspace_bytes, stream=None):
+    return _check(lib().svdq_lora_batch(
+        int(M), int(K), int(N), int(max_rank), int(n_adapters), int(n_segments), _dev_ptr(x, "x"),
+        int(x_stride), _dev_ptr(lora_down, "lora_down"), _dev_ptr(lora_up, "lora_up"),
+        _dev_ptr(alphas, "alphas"), _dev_ptr(ranks, "ranks"), _dev_ptr(seg_start, "seg_start"),
+        _dev_ptr(seg_adapter, "seg_adapter"), _dev_ptr(base, "base"), int(base_stride), int(act),
+        int(out_dtype), _dev_ptr(out, "out"), int(out_stride), _dev_ptr(workspace, "workspace"),
+        int(workspace_bytes), _stream(stream)))
+
+
+def svdq_group_norm_workspace_bytes(B, rows, C, groups):
+    n = ctypes.c_int64(0)
+    _check(lib().svdq_group_norm_workspace_bytes(int(B), int(rows), int(C), int(groups),
+                                                 ctypes.byref(n)))
+    return n.value
+
+
+def svdq_group_norm(B, rows, C, groups, eps, x_dtype, x, x_stride, weight, bias, mod_dtype, mod_scale,
+                    mod_shift, mod_stride, act, out_dtype, out, out_stride, workspace, workspace_bytes,
+                    stream=None):
+    return _check(lib().svdq_group_norm(
+        int(B), int(rows), int(C), int(groups), float(eps), int(x_dtype), _dev_ptr(x, "x"),
+        int(x_stride), _dev_ptr(weight, "weight"), _dev_ptr(bias, "bias"), int(mod_dtype),
+        _dev_ptr(mod_scale, "mod_scale"), _dev_ptr(mod_shift, "mod_shift"), int(mod_stride), int(act),
+        int(out_dtype), _dev_ptr(out, "out"), int(out_stride), _dev_ptr(workspace, "workspace"),
+        int(workspace_bytes), _stream(stream)))
 
 
 def svdq_peak_mfma(kind, iters, out, stream=None):

@@ -20,6 +20,7 @@ SVDQ_DT_F32 = 0
 SVDQ_DT_BF16 = 1
 SVDQ_ACT_NONE = 0
 SVDQ_ACT_GELU_TANH = 1
+SVDQ_ACT_SILU = 2
 
 # Every symbol include/*.h declares.
 EXPORTS = ("svdq_quantize_act", "svdq_gemm_w4a4", "awq_gemm_w4a16", "svdq_check_device",
@@ -31,7 +32,8 @@ EXPORTS = ("svdq_quantize_act", "svdq_gemm_w4a4", "awq_gemm_w4a16", "svdq_check_
            "svdq_quantize_residual", "svdq_lowrank_workspace_bytes", "svdq_lowrank_factors",
            "svdq_gemm_w4a4_packed_workspace_bytes", "svdq_gemm_w4a4_packed_ws",
            "svdq_quantize_next_workspace_bytes", "svdq_peak_mfma", "svdq_peak_copy",
-           "svdq_gemm_w4a4_packed_noalloc", "svdq_peak_read")
+           "svdq_gemm_w4a4_packed_noalloc", "svdq_peak_read", "svdq_lora_batch_workspace_bytes",
+           "svdq_lora_batch", "svdq_group_norm_workspace_bytes", "svdq_group_norm")
 
 
 class LayerCfg(ctypes.Structure):
@@ -97,6 +99,14 @@ def lib():
         L.svdq_peak_mfma.argtypes = [I32, I32, P, ctypes.POINTER(ctypes.c_int64), P]
         L.svdq_peak_copy.argtypes = [P, P, I64, P]
         L.svdq_peak_read.argtypes = [P, I64, P, P]
+        L.svdq_lora_batch_workspace_bytes.argtypes = [I64, I32, I32, I32, I32,
+                                                      ctypes.POINTER(ctypes.c_int64)]
+        L.svdq_lora_batch.argtypes = [I64, I32, I32, I32, I32, I32, P, I64, P, P, P, P, P, P, P, I64,
+                                      I32, I32, P, I64, P, I64, P]
+        L.svdq_group_norm_workspace_bytes.argtypes = [I64, I64, I32, I32,
+                                                      ctypes.POINTER(ctypes.c_int64)]
+        L.svdq_group_norm.argtypes = [I64, I64, I32, I32, F, I32, P, I64, P, P, I32, P, P, I64, I32,
+                                      I32, P, I64, P, I64, P]
         L.svdq_check_device.argtypes = [ctypes.c_int]
         L.svdq_check_arch.argtypes = [ctypes.c_char_p]
         L.svdq_status_string.argtypes = [ctypes.c_int]
@@ -113,7 +123,9 @@ def lib():
                      "svdq_lowrank_workspace_bytes", "svdq_lowrank_factors",
                      "svdq_gemm_w4a4_packed_workspace_bytes", "svdq_gemm_w4a4_packed_ws",
                      "svdq_quantize_next_workspace_bytes", "svdq_peak_mfma", "svdq_peak_copy",
-                     "svdq_gemm_w4a4_packed_noalloc", "svdq_peak_read"):
+                     "svdq_gemm_w4a4_packed_noalloc", "svdq_peak_read",
+                     "svdq_lora_batch_workspace_bytes", "svdq_lora_batch",
+                     "svdq_group_norm_workspace_bytes", "svdq_group_norm"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib

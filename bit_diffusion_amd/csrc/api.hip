@@ -110,6 +110,61 @@ svdq_status check_global_scale(float s, const char* name) {
     return SVDQ_OK;
 }
 
+svdq_status check_dtype(int32_t dt, const char* name) {
+    if (dt != SVDQ_DT_F32 && dt != SVDQ_DT_BF16)
+        return fail(SVDQ_ERR_INVALID_ARG, "%s %d is not a svdq_dtype value", name, dt);
+    return SVDQ_OK;
+}
+
+svdq_status check_act(int32_t act) {
+    if (act != SVDQ_ACT_NONE && act != SVDQ_ACT_GELU_TANH && act != SVDQ_ACT_SILU)
+        return fail(SVDQ_ERR_INVALID_ARG, "act %d is not a svdq_act value", act);
+    return SVDQ_OK;
+}
+
+svdq_status check_stride(int64_t stride, int64_t least, const char* name) {
+    if (stride < least)
+        return fail(SVDQ_ERR_INVALID_ARG, "%s = %lld is less than the row's %lld elements", name,
+                    (long long)stride, (long long)least);
+    return SVDQ_OK;
+}
+
+svdq_status check_workspace(const void* ws, int64_t bytes, int64_t need) {
+    if (ws != nullptr && !aligned(ws, 16)) return fail(SVDQ_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+    if (need > 0 && (ws == nullptr || bytes < need))
+        return fail(SVDQ_ERR_INVALID_ARG, "workspace of %lld bytes: %lld are needed",
+                    (long long)(ws == nullptr ? 0 : bytes), (long long)need);
+    return SVDQ_OK;
+}
+
+svdq_status check_lora_batch(int64_t M, int32_t K, int32_t N, int32_t max_rank, int32_t n_segments) {
+    if (M < 0) return fail(SVDQ_ERR_INVALID_ARG, "M = %lld is negative", (long long)M);
+    if (K <= 0 || K % 64 != 0) return fail(SVDQ_ERR_INVALID_ARG, "K %d must be a positive multiple of 64", K);
+    if (N <= 0) return fail(SVDQ_ERR_INVALID_ARG, "N %d must be positive", N);
+    if (max_rank <= 0 || max_rank % 16 != 0)
+        return fail(SVDQ_ERR_INVALID_ARG, "max_rank %d must be a positive multiple of 16", max_rank);
+    if (max_rank > 128)
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "max_rank %d exceeds the supported maximum 128", max_rank);
+    if (n_segments < 0) return fail(SVDQ_ERR_INVALID_ARG, "n_segments = %d is negative", n_segments);
+    if (n_segments > 1 << 20)
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "n_segments = %d exceeds the supported maximum 2^20", n_segments);
+    if (M > (int64_t)1 << 26 || N > 1 << 23)
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "M = %lld, N = %d too large for one launch", (long long)M, N);
+    return SVDQ_OK;
+}
+
+svdq_status check_group_norm(int64_t B, int64_t rows, int32_t C, int32_t groups) {
+    if (B < 0) return fail(SVDQ_ERR_INVALID_ARG, "B = %lld is negative", (long long)B);
+    if (rows < 0) return fail(SVDQ_ERR_INVALID_ARG, "rows = %lld is negative", (long long)rows);
+    if (groups <= 0 || C <= 0 || C % groups != 0)
+        return fail(SVDQ_ERR_INVALID_ARG, "C %d must be a positive multiple of groups %d", C, groups);
+    if (C > 65536) return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "C %d exceeds the supported maximum 65536", C);
+    if (B > 65535 || rows > (int64_t)1 << 30)
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "B = %lld, rows = %lld too large for one launch", (long long)B,
+                    (long long)rows);
+    return SVDQ_OK;
+}
+
 svdq_status after_launch(const char* what) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(SVDQ_ERR_LAUNCH, "%s launch failed: %s", what, hipGetErrorString(e));
@@ -595,6 +650,120 @@ svdq_status svdq_lowrank_factors(const svdq_layer_cfg* cfg, const float* w, cons
     svdq::launch_lowrank_factors(cfg->out_features, cfg->in_features, r, block, iters, w, smooth_inv, omega,
                                  l1, l2, sigma, workspace, reinterpret_cast<hipStream_t>(stream));
     return after_launch("svdq_lowrank_factors");
+}
+
+svdq_status svdq_lora_batch_workspace_bytes(int64_t M, int32_t K, int32_t N, int32_t max_rank,
+                                            int32_t n_segments, int64_t* bytes) {
+    SVDQ_TRY(check_lora_batch(M, K, N, max_rank, n_segments));
+    if (bytes == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = svdq::lora_batch_workspace_bytes(M, K, max_rank, n_segments);
+    return SVDQ_OK;
+}
+
+svdq_status svdq_lora_batch(int64_t M, int32_t K, int32_t N, int32_t max_rank, int32_t n_adapters,
+                            int32_t n_segments, const void* x, int64_t x_stride,
+                            const void* lora_down, const void* lora_up, const float* alphas,
+                            const int32_t* ranks, const int32_t* seg_start,
+                            const int32_t* seg_adapter, const void* base, int64_t base_stride,
+                            int32_t act, int32_t out_dtype, void* out, int64_t out_stride,
+                            void* workspace, int64_t workspace_bytes, svdq_stream_t stream) {
+    SVDQ_TRY(check_lora_batch(M, K, N, max_rank, n_segments));
+    if (n_adapters <= 0) return fail(SVDQ_ERR_INVALID_ARG, "n_adapters = %d must be positive", n_adapters);
+    SVDQ_TRY(check_act(act));
+    SVDQ_TRY(check_dtype(out_dtype, "out_dtype"));
+    const int64_t esz = out_dtype == SVDQ_DT_BF16 ? 2 : 4;
+    SVDQ_TRY(check_ptr(x, "x", 16));
+    SVDQ_TRY(check_stride(x_stride, K, "x_stride"));
+    if (x_stride % 8 != 0)
+        return fail(SVDQ_ERR_INVALID_ARG, "x_stride = %lld must be a multiple of 8", (long long)x_stride);
+    SVDQ_TRY(check_ptr(lora_down, "lora_down", 16));
+    SVDQ_TRY(check_ptr(lora_up, "lora_up", 16));
+    SVDQ_TRY(check_ptr(alphas, "alphas", 4));
+    if (ranks != nullptr && !aligned(ranks, 4)) return fail(SVDQ_ERR_INVALID_ARG, "ranks is not 4-byte aligned");
+    SVDQ_TRY(check_ptr(seg_start, "seg_start", 4));
+    SVDQ_TRY(check_ptr(seg_adapter, "seg_adapter", 4));
+    SVDQ_TRY(check_ptr(out, "out", esz));
+    SVDQ_TRY(check_stride(out_stride, N, "out_stride"));
+    if (base != nullptr) {
+        SVDQ_TRY(check_ptr(base, "base", esz));
+        SVDQ_TRY(check_stride(base_stride, N, "base_stride"));
+        if (base == out && base_stride != out_stride)
+            return fail(SVDQ_ERR_INVALID_ARG, "base is out but base_stride = %lld is not out_stride = %lld",
+                        (long long)base_stride, (long long)out_stride);
+    }
+    SVDQ_TRY(check_workspace(workspace, workspace_bytes,
+                             svdq::lora_batch_workspace_bytes(M, K, max_rank, n_segments)));
+    SVDQ_TRY(check_current_device());
+    if (M == 0 || n_segments == 0) return SVDQ_OK;
+    svdq::LoraBatchArgs a{};
+    a.M = M; a.K = K; a.N = N; a.R = max_rank;
+    a.n_adapters = n_adapters; a.n_segments = n_segments;
+    a.x = x; a.x_stride = x_stride;
+    a.down = lora_down; a.up = lora_up; a.alphas = alphas; a.ranks = ranks;
+    a.starts = seg_start; a.ids = seg_adapter;
+    a.base = base; a.base_stride = base_stride;
+    a.act = act; a.bf16 = out_dtype == SVDQ_DT_BF16 ? 1 : 0;
+    a.out = out; a.out_stride = out_stride;
+    a.work = static_cast<float*>(workspace);
+    a.vec = aligned(out, 16) && out_stride * esz % 16 == 0 &&
+            (base == nullptr || (aligned(base, 16) && base_stride * esz % 16 == 0));
+    svdq::launch_lora_batch(a, reinterpret_cast<hipStream_t>(stream));
+    return after_launch("svdq_lora_batch");
+}
+
+svdq_status svdq_group_norm_workspace_bytes(int64_t B, int64_t rows, int32_t C, int32_t groups,
+                                            int64_t* bytes) {
+    SVDQ_TRY(check_group_norm(B, rows, C, groups));
+    if (bytes == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = svdq::group_norm_workspace_bytes(B, rows, C, groups);
+    return SVDQ_OK;
+}
+
+svdq_status svdq_group_norm(int64_t B, int64_t rows, int32_t C, int32_t groups, float eps,
+                            int32_t x_dtype, const void* x, int64_t x_stride, const void* weight,
+                            const void* bias, int32_t mod_dtype, const void* mod_scale,
+                            const void* mod_shift, int64_t mod_stride, int32_t act,
+                            int32_t out_dtype, void* out, int64_t out_stride, void* workspace,
+                            int64_t workspace_bytes, svdq_stream_t stream) {
+    SVDQ_TRY(check_group_norm(B, rows, C, groups));
+    if (!(std::isfinite(eps) && eps > 0.0f))
+        return fail(SVDQ_ERR_INVALID_ARG, "eps = %g must be finite and positive", (double)eps);
+    SVDQ_TRY(check_dtype(x_dtype, "x_dtype"));
+    SVDQ_TRY(check_dtype(mod_dtype, "mod_dtype"));
+    SVDQ_TRY(check_dtype(out_dtype, "out_dtype"));
+    SVDQ_TRY(check_act(act));
+    const int64_t xsz = x_dtype == SVDQ_DT_BF16 ? 2 : 4, osz = out_dtype == SVDQ_DT_BF16 ? 2 : 4;
+    const size_t msz = mod_dtype == SVDQ_DT_BF16 ? 2 : 4;
+    SVDQ_TRY(check_ptr(x, "x", xsz));
+    SVDQ_TRY(check_stride(x_stride, C, "x_stride"));
+    if (weight != nullptr && !aligned(weight, 2)) return fail(SVDQ_ERR_INVALID_ARG, "weight is not 2-byte aligned");
+    if (bias != nullptr && !aligned(bias, 2)) return fail(SVDQ_ERR_INVALID_ARG, "bias is not 2-byte aligned");
+    if (mod_scale != nullptr || mod_shift != nullptr) {
+        if (mod_scale != nullptr) SVDQ_TRY(check_ptr(mod_scale, "mod_scale", msz));
+        if (mod_shift != nullptr) SVDQ_TRY(check_ptr(mod_shift, "mod_shift", msz));
+        SVDQ_TRY(check_stride(mod_stride, C, "mod_stride"));
+    }
+    SVDQ_TRY(check_ptr(out, "out", osz));
+    SVDQ_TRY(check_stride(out_stride, C, "out_stride"));
+    if (x == out && (x_dtype != out_dtype || x_stride != out_stride))
+        return fail(SVDQ_ERR_INVALID_ARG, "x is out but their types or strides differ");
+    SVDQ_TRY(check_workspace(workspace, workspace_bytes, svdq::group_norm_workspace_bytes(B, rows, C, groups)));
+    SVDQ_TRY(check_current_device());
+    if (B == 0 || rows == 0) return SVDQ_OK;
+    svdq::GroupNormArgs a{};
+    a.B = B; a.rows = rows; a.C = C; a.groups = groups; a.eps = eps;
+    a.x_bf16 = x_dtype == SVDQ_DT_BF16 ? 1 : 0;
+    a.x = x; a.x_stride = x_stride;
+    a.weight = weight; a.bias = bias;
+    a.mod_bf16 = mod_dtype == SVDQ_DT_BF16 ? 1 : 0;
+    a.mod_scale = mod_scale; a.mod_shift = mod_shift; a.mod_stride = mod_stride;
+    a.act = act;
+    a.out_bf16 = out_dtype == SVDQ_DT_BF16 ? 1 : 0;
+    a.out = out; a.out_stride = out_stride;
+    a.work = workspace;
+    a.vec = aligned(x, 16) && aligned(out, 16) && x_stride * xsz % 16 == 0 && out_stride * osz % 16 == 0;
+    svdq::launch_group_norm(a, reinterpret_cast<hipStream_t>(stream));
+    return after_launch("svdq_group_norm");
 }
 
 svdq_status svdq_peak_mfma(int32_t kind, int32_t iters, float* out, int64_t* ops,

@@ -47,4 +47,16 @@ __device__ __forceinline__ float gelu_tanh(float y) {
     return y * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
+// SiLU: y / (1 + exp(-y)), on the hardware's exp2 and reciprocal as above.
+__device__ __forceinline__ float silu(float y) {
+    return y * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * y));
+}
+
+// The activation of a svdq_act value.
+__device__ __forceinline__ float activate(float y, int act) {
+    if (act == 1) return gelu_tanh(y);
+    if (act == 2) return silu(y);
+    return y;
+}
+
 }  // namespace svdq

@@ -78,6 +78,50 @@ struct PackedGemmArgs {
     int64_t split_ws_bytes;
 };
 
+struct LoraBatchArgs {
+    int64_t M;
+    int K, N, R;             // R: the pool's ranks, a multiple of 16 up to 128
+    int n_adapters, n_segments;
+    const void* x;           // bf16 [M, K]
+    int64_t x_stride;
+    const void* down;        // bf16 [n_adapters, R, K]
+    const void* up;          // bf16 [n_adapters, N, R]
+    const float* alphas;     // [n_adapters]
+    const int* ranks;        // [n_adapters] or NULL (all R)
+    const int* starts;       // [n_segments + 1]
+    const int* ids;          // [n_segments]
+    const void* base;        // [M, N] or NULL
+    int64_t base_stride;
+    int act;
+    int bf16;                // type of base and out: 0 fp32, 1 bf16
+    void* out;
+    int64_t out_stride;
+    float* work;             // partial t, fp32 [splits][M][R]
+    int vec;                 // base and out take 16-byte accesses
+    int splits;              // set by the launcher
+};
+
+struct GroupNormArgs {
+    int64_t B, rows;
+    int C, groups;
+    float eps;
+    int x_bf16;              // 0 fp32, 1 bf16
+    const void* x;           // [B rows, C]
+    int64_t x_stride;
+    const void* weight;      // bf16 [C] or NULL
+    const void* bias;
+    int mod_bf16;
+    const void* mod_scale;   // [B, C] or NULL
+    const void* mod_shift;
+    int64_t mod_stride;
+    int act;
+    int out_bf16;
+    void* out;
+    int64_t out_stride;
+    void* work;
+    int vec;                 // x and out take 16-byte accesses
+};
+
 // Largest workspace the K split of svdq_gemm_w4a4_packed uses (its split count is capped so
 // that the partial tiles fit).
 constexpr int64_t kSplitWorkspaceMax = (int64_t)64 << 20;
@@ -108,6 +152,14 @@ int64_t launch_mfma_peak(int kind, int iters, float* out, hipStream_t st);
 void launch_copy(const void* src, void* dst, int64_t bytes, hipStream_t st);
 void launch_read(const void* src, int64_t bytes, void* out, hipStream_t st);
 int64_t quantize_next_workspace_bytes(int64_t M, int N, int next_r);
+
+// adapters of many requests (lora_batch.hip)
+int64_t lora_batch_workspace_bytes(int64_t M, int K, int R, int n_segments);
+void launch_lora_batch(const LoraBatchArgs& a, hipStream_t st);
+
+// group normalisation of channels-last images (group_norm.hip)
+int64_t group_norm_workspace_bytes(int64_t B, int64_t rows, int C, int groups);
+void launch_group_norm(const GroupNormArgs& a, hipStream_t st);
 
 // offline weight quantization (weights.hip)
 void launch_calib_absmax(int64_t M, int K, const void* x, float* absmax, hipStream_t st);

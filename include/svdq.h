@@ -20,7 +20,9 @@
  *                       lora_act = x . L1^T (bf16), in one pass over x;
  *   svdq_gemm_w4a4    : y = dequant(codes_x) . dequant(codes_w)^T + lora_act . L2^T + b
  *                       (optionally GELU-tanh), fp32 or bf16 output.
- * and the modulation layers as one call, awq_gemm_w4a16.
+ * and the modulation layers as one call, awq_gemm_w4a16.  Beside a linear stand the adapters
+ * of a batch's requests (svdq_lora_batch), before it the group norm of channels-last images
+ * (svdq_group_norm).
  *
  * Conventions shared by every entry point
  *   - Ownership: the caller allocates and owns every buffer (device memory unless stated).
@@ -58,7 +60,8 @@ typedef enum {
 
 typedef enum { SVDQ_PREC_INT4 = 0, SVDQ_PREC_NVFP4 = 1 } svdq_precision;
 typedef enum { SVDQ_DT_F32 = 0, SVDQ_DT_BF16 = 1 } svdq_dtype;
-typedef enum { SVDQ_ACT_NONE = 0, SVDQ_ACT_GELU_TANH = 1 } svdq_act;
+/* SVDQ_ACT_SILU is taken by svdq_lora_batch and svdq_group_norm only. */
+typedef enum { SVDQ_ACT_NONE = 0, SVDQ_ACT_GELU_TANH = 1, SVDQ_ACT_SILU = 2 } svdq_act;
 
 /* The quantization fields a checkpoint's config.json records for one layer
  * ([ainews] paragraph 2: method, precision, group size, low-rank rank). */
@@ -346,6 +349,86 @@ int32_t svdq_merged_rank(int32_t rank, int32_t r_lora);
 svdq_status svdq_merge_lora(const svdq_layer_cfg* cfg, int32_t r_lora, const void* l1,
                             const void* l2, const void* lora_down, const void* lora_up,
                             float alpha, void* l1_out, void* l2_out, svdq_stream_t stream);
+
+/* Adapters of many requests beside one shared linear: where svdq_merge_lora gives every row
+ * the same adapter, here the rows of a batch belong to different requests and each request
+ * brings its own adapter, or none.  The linear runs once for all rows (svdq_gemm_w4a4_packed,
+ * svdq_gemm_w4a4, awq_gemm_w4a16, without activation); this call then adds to its output
+ *
+ *   out[m, n] = act(base[m, n] + alphas[s] sum_{j < rank_s} (sum_k x[m, k] lora_down[s, j, k])
+ *                                                           lora_up[s, n, j])
+ *
+ * for every row m of segment i, s = seg_adapter[i].  All sums are fp32; the down-projection is
+ * not rounded to 16 bits in between; the result is rounded once.
+ *
+ *   x          [M, K] bf16, the linear's input (for an SVDQ layer the raw x, not smoothed),
+ *              rows x_stride elements apart (x_stride >= K, a multiple of 8).
+ *   lora_down  [n_adapters, max_rank, K] bf16 and lora_up [n_adapters, N, max_rank] bf16: the
+ *              pool, each adapter's A and B in the layout svdq_merge_lora takes.  Rows of A
+ *              and columns of B at and past the adapter's rank are not used, whatever they hold.
+ *   alphas     [n_adapters] fp32: the adapter's scale.
+ *   ranks      [n_adapters] int32 in [0, max_rank], or NULL: all max_rank.  A value outside is
+ *              clamped; 0 is an adapter that adds nothing.
+ *   seg_start  [n_segments + 1] int32, not decreasing: segment i is rows seg_start[i] to
+ *              seg_start[i + 1] - 1 (none where they are equal).  Rows before seg_start[0] and
+ *              at or past seg_start[n_segments] are not touched.  Values are clamped to
+ *              [0, M]; where they decrease, rows may be written twice, in no set order, or be
+ *              left, but nothing outside the buffers is read or written.
+ *   seg_adapter [n_segments] int32: index into the pool; a negative index, or one past the
+ *              pool, is no adapter: out = act(base) there.
+ *   base       [M, N] of out_dtype, rows base_stride apart (>= N), or NULL: 0.  base == out
+ *              with base_stride == out_stride updates in place; a column range of a wider
+ *              matrix (one of q, k, v in a fused projection) is a pointer and a stride.
+ *              Otherwise no input may overlap out.
+ *   act        svdq_act, applied to the sum.
+ *   out        [M, N] of out_dtype, rows out_stride apart (>= N).
+ *   workspace  svdq_lora_batch_workspace_bytes(M, K, N, max_rank, n_segments) bytes at least,
+ *              16-byte aligned, overwritten; calls that may overlap in time need one each.
+ * K a positive multiple of 64; max_rank a multiple of 16 up to 128; M up to 2^26; n_segments
+ * up to 2^20 (0 is valid and enqueues nothing).  The segments' arrays are read when the work
+ * runs, so a captured graph replays with what they hold then.  x, lora_down and lora_up must
+ * be 16-byte aligned, base and out aligned to their type (16-byte aligned rows are faster).
+ * All buffers are device memory on the current device.  Bit-reproducible from run to run. */
+svdq_status svdq_lora_batch_workspace_bytes(int64_t M, int32_t K, int32_t N, int32_t max_rank,
+                                            int32_t n_segments, int64_t* bytes);
+svdq_status svdq_lora_batch(int64_t M, int32_t K, int32_t N, int32_t max_rank, int32_t n_adapters,
+                            int32_t n_segments, const void* x, int64_t x_stride,
+                            const void* lora_down, const void* lora_up, const float* alphas,
+                            const int32_t* ranks, const int32_t* seg_start,
+                            const int32_t* seg_adapter, const void* base, int64_t base_stride,
+                            int32_t act, int32_t out_dtype, void* out, int64_t out_stride,
+                            void* workspace, int64_t workspace_bytes, svdq_stream_t stream);
+
+/* Group normalisation of channels-last images with an activation: what turns an image
+ * [B, rows, C] (rows = height x width, channels contiguous) into the bf16 rows the activation
+ * kernels take.  Over the rows x C / groups values of each image b and group g
+ *
+ *   mean = sum x / n,  var = sum (x - mean)^2 / n,
+ *   out  = act(((x - mean) / sqrt(var + eps) weight_c + bias_c) (1 + mod_scale[b, c])
+ *              + mod_shift[b, c])
+ *
+ * in fp32, rounded once.
+ *   x          [B rows, C] of x_dtype, rows x_stride elements apart (>= C).
+ *   weight, bias [C] bf16, or NULL: 1 and 0.
+ *   mod_scale, mod_shift  [B, C] of mod_dtype, rows mod_stride apart (>= C), or NULL: 0.  Two
+ *              column ranges of the rows awq_gemm_w4a16 writes for a modulation layer.
+ *   act        svdq_act.
+ *   out        [B rows, C] of out_dtype, rows out_stride apart (>= C).  out == x is allowed
+ *              where types and strides are the same; otherwise no input may overlap out.
+ *   workspace  svdq_group_norm_workspace_bytes(B, rows, C, groups) bytes at least, 16-byte
+ *              aligned, overwritten; calls that may overlap in time need one each.
+ * C a positive multiple of groups, up to 65536; eps positive and finite; B up to 65535; rows
+ * up to 2^30 (B = 0 or rows = 0 enqueues nothing).  Buffers are aligned to their type; x and
+ * out that are 16-byte aligned with strides and C multiples of 8 are faster.  All buffers are
+ * device memory on the current device.  Bit-reproducible from run to run. */
+svdq_status svdq_group_norm_workspace_bytes(int64_t B, int64_t rows, int32_t C, int32_t groups,
+                                            int64_t* bytes);
+svdq_status svdq_group_norm(int64_t B, int64_t rows, int32_t C, int32_t groups, float eps,
+                            int32_t x_dtype, const void* x, int64_t x_stride, const void* weight,
+                            const void* bias, int32_t mod_dtype, const void* mod_scale,
+                            const void* mod_shift, int64_t mod_stride, int32_t act,
+                            int32_t out_dtype, void* out, int64_t out_stride, void* workspace,
+                            int64_t workspace_bytes, svdq_stream_t stream);
 
 /* SVDQ_OK when HIP device `device` is a gfx950 GPU, else SVDQ_ERR_UNSUPPORTED_DEVICE
  * (or SVDQ_ERR_INVALID_ARG for a bad ordinal).  Results are cached per device. */
