@@ -40,19 +40,25 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _dev_ptr(t, name):
-    """As _ptr, for a buffer that a kernel reads or writes: a tensor elsewhere than on the
-    current device is refused before its address reaches one."""
-    if t is None or isinstance(t, int):
-        return t
-    if not t.is_cuda:
-        raise SvdqError(SVDQ_ERR_INVALID_ARG, f"{name} is on {t.device}, not on a GPU")
-    import torch
-    if t.device.index != torch.cuda.current_device():
-        raise SvdqError(SVDQ_ERR_INVALID_ARG,
-                        f"{name} is on {t.device}, not on the current device "
-                        f"cuda:{torch.cuda.current_device()}")
-    return t.data_ptr()
+def _dev_ptrs(names, tensors):
+    """As _ptr for each of the buffers that a kernel reads or writes: a tensor elsewhere than on
+    the current device is refused before its address reaches one."""
+    ptrs, current = [], None
+    for i, t in enumerate(tensors):
+        if t is not None and not isinstance(t, int):
+            dev = t.get_device()
+            if dev != current:
+                if dev < 0:
+                    raise SvdqError(SVDQ_ERR_INVALID_ARG, f"{names[i]} is on {t.device}, not on a GPU")
+                if current is None:
+                    import torch
+                    current = torch.cuda.current_device()
+                if dev != current:
+                    raise SvdqError(SVDQ_ERR_INVALID_ARG, f"{names[i]} is on {t.device}, not on the "
+                                                          f"current device cuda:{current}")
+            t = t.data_ptr()
+        ptrs.append(t)
+    return ptrs
 
 
 def _stream(stream):
@@ -228,16 +234,18 @@ def svdq_lora_batch_workspace_bytes(M, K, N, max_rank, n_segments):
     return n.value
 
 
+_LORA_BATCH = ("x", "lora_down", "lora_up", "alphas", "ranks", "seg_start", "seg_adapter", "base", "out",
+               "workspace")
+
+
 def svdq_lora_batch(M, K, N, max_rank, n_adapters, n_segments, x, x_stride, lora_down, lora_up, alphas,
                     ranks, seg_start, seg_adapter, base, base_stride, act, out_dtype, out, out_stride,
                     workspace, workspace_bytes, stream=None):
-    return _check(lib().svdq_lora_batch(
-        int(M), int(K), int(N), int(max_rank), int(n_adapters), int(n_segments), _dev_ptr(x, "x"),
-        int(x_stride), _dev_ptr(lora_down, "lora_down"), _dev_ptr(lora_up, "lora_up"),
-        _dev_ptr(alphas, "alphas"), _dev_ptr(ranks, "ranks"), _dev_ptr(seg_start, "seg_start"),
-        _dev_ptr(seg_adapter, "seg_adapter"), _dev_ptr(base, "base"), int(base_stride), int(act),
-        int(out_dtype), _dev_ptr(out, "out"), int(out_stride), _dev_ptr(workspace, "workspace"),
-        int(workspace_bytes), _stream(stream)))
+    x, down, up, al, rk, st, ad, ba, ou, ws = _dev_ptrs(
+        _LORA_BATCH, (x, lora_down, lora_up, alphas, ranks, seg_start, seg_adapter, base, out, workspace))
+    return _check(lib().svdq_lora_batch(M, K, N, max_rank, n_adapters, n_segments, x, x_stride, down, up, al,
+                                        rk, st, ad, ba, base_stride, act, out_dtype, ou, out_stride, ws,
+                                        workspace_bytes, _stream(stream)))
 
 
 def svdq_group_norm_workspace_bytes(B, rows, C, groups):
@@ -247,15 +255,16 @@ def svdq_group_norm_workspace_bytes(B, rows, C, groups):
     return n.value
 
 
+_GROUP_NORM = ("x", "weight", "bias", "mod_scale", "mod_shift", "out", "workspace")
+
+
 def svdq_group_norm(B, rows, C, groups, eps, x_dtype, x, x_stride, weight, bias, mod_dtype, mod_scale,
                     mod_shift, mod_stride, act, out_dtype, out, out_stride, workspace, workspace_bytes,
                     stream=None):
-    return _check(lib().svdq_group_norm(
-        int(B), int(rows), int(C), int(groups), float(eps), int(x_dtype), _dev_ptr(x, "x"),
-        int(x_stride), _dev_ptr(weight, "weight"), _dev_ptr(bias, "bias"), int(mod_dtype),
-        _dev_ptr(mod_scale, "mod_scale"), _dev_ptr(mod_shift, "mod_shift"), int(mod_stride), int(act),
-        int(out_dtype), _dev_ptr(out, "out"), int(out_stride), _dev_ptr(workspace, "workspace"),
-        int(workspace_bytes), _stream(stream)))
+    x, w, b, ms, mt, ou, ws = _dev_ptrs(_GROUP_NORM, (x, weight, bias, mod_scale, mod_shift, out, workspace))
+    return _check(lib().svdq_group_norm(B, rows, C, groups, eps, x_dtype, x, x_stride, w, b, mod_dtype, ms, mt,
+                                        mod_stride, act, out_dtype, ou, out_stride, ws, workspace_bytes,
+                                        _stream(stream)))
 
 
 def svdq_peak_mfma(kind, iters, out, stream=None):

@@ -28,8 +28,10 @@ FLAGS = [
 SOURCES = ["api.hip", "quant.hip", "gemm_int4.hip", "gemm_int4_fp6.hip", "gemm_nvfp4.hip",
            "awq.hip", "lora.hip", "lora_batch.hip", "group_norm.hip", "weights.hip", "lowrank.hip",
            "peaks.hip", "noalloc.hip"]
-# per-source extra flags: MFMA results in VGPRs (the fp32 rescale reads them with VALU ops)
-EXTRA = {"gemm_int4_fp6.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# per-source extra flags: MFMA results in VGPRs (the fp32 rescale, the adapters' epilogue read
+# them with VALU ops)
+EXTRA = {"gemm_int4_fp6.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "lora_batch.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _compile(src):

@@ -656,7 +656,7 @@ svdq_status svdq_lora_batch_workspace_bytes(int64_t M, int32_t K, int32_t N, int
                                             int32_t n_segments, int64_t* bytes) {
     SVDQ_TRY(check_lora_batch(M, K, N, max_rank, n_segments));
     if (bytes == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "bytes is NULL");
-    *bytes = svdq::lora_batch_workspace_bytes(M, K, max_rank, n_segments);
+    *bytes = svdq::lora_batch_workspace_bytes(M, max_rank, n_segments);
     return SVDQ_OK;
 }
 
@@ -692,7 +692,7 @@ svdq_status svdq_lora_batch(int64_t M, int32_t K, int32_t N, int32_t max_rank, i
                         (long long)base_stride, (long long)out_stride);
     }
     SVDQ_TRY(check_workspace(workspace, workspace_bytes,
-                             svdq::lora_batch_workspace_bytes(M, K, max_rank, n_segments)));
+                             svdq::lora_batch_workspace_bytes(M, max_rank, n_segments)));
     SVDQ_TRY(check_current_device());
     if (M == 0 || n_segments == 0) return SVDQ_OK;
     svdq::LoraBatchArgs a{};
@@ -704,7 +704,7 @@ svdq_status svdq_lora_batch(int64_t M, int32_t K, int32_t N, int32_t max_rank, i
     a.base = base; a.base_stride = base_stride;
     a.act = act; a.bf16 = out_dtype == SVDQ_DT_BF16 ? 1 : 0;
     a.out = out; a.out_stride = out_stride;
-    a.work = static_cast<float*>(workspace);
+    a.work = workspace;
     a.vec = aligned(out, 16) && out_stride * esz % 16 == 0 &&
             (base == nullptr || (aligned(base, 16) && base_stride * esz % 16 == 0));
     svdq::launch_lora_batch(a, reinterpret_cast<hipStream_t>(stream));

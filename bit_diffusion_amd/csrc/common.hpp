@@ -9,6 +9,8 @@ typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 namespace svdq {
 
@@ -24,6 +26,12 @@ __device__ __forceinline__ uint32_t f32_to_bf16(float f) {
     if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0x7FC0u;
     u += 0x7FFFu + ((u >> 16) & 1u);
     return u >> 16;
+}
+
+// Two fp32 -> two bf16 in one word (the first in the low half), round to nearest even: one
+// v_cvt_pk_bf16_f32.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
 // The 8 bf16 words of a 16-byte register block as an MFMA operand.

@@ -96,9 +96,9 @@ struct LoraBatchArgs {
     int bf16;                // type of base and out: 0 fp32, 1 bf16
     void* out;
     int64_t out_stride;
-    float* work;             // partial t, fp32 [splits][M][R]
+    void* work;              // t as MFMA operands, a set for every block of 16 rows
     int vec;                 // base and out take 16-byte accesses
-    int splits;              // set by the launcher
+    int nb, max_blocks;      // blocks of 32 ranks, and of 16 rows, in work (set by the launcher)
 };
 
 struct GroupNormArgs {
@@ -154,7 +154,7 @@ void launch_read(const void* src, int64_t bytes, void* out, hipStream_t st);
 int64_t quantize_next_workspace_bytes(int64_t M, int N, int next_r);
 
 // adapters of many requests (lora_batch.hip)
-int64_t lora_batch_workspace_bytes(int64_t M, int K, int R, int n_segments);
+int64_t lora_batch_workspace_bytes(int64_t M, int R, int n_segments);
 void launch_lora_batch(const LoraBatchArgs& a, hipStream_t st);
 
 // group normalisation of channels-last images (group_norm.hip)

@@ -4,14 +4,23 @@
 // s = seg_adapter[i] of a pool, or none:
 //   out[m, n] = act(base[m, n] + sum_{j < rank_s} t[m, j] B_s[n, j]),
 //   t[m, j]   = alpha_s sum_k x[m, k] A_s[j, k].
-// Two launches: the down-projection writes t in fp32 to the workspace, the up-projection
-// adds to base.  Both are bound by memory (x once; base and out once): 2 R flops per byte
-// of x, R / 2 per byte of bf16 base and out.
+// Both products are bound by memory (x once; base and out once): 2 R flops per byte of x,
+// R / 2 per byte of bf16 base and out.  Many rows take two launches, the down-projection
+// (t to the workspace) and the up-projection (t, base -> out); few rows take one, in which
+// every workgroup forms its rows' t itself.
 //
 // Tiles.  A workgroup owns rows of one segment only, so its adapter is uniform.  The
 // offsets live in device memory (a captured graph replays with other offsets), so the grid
 // is the most tiles any cut of M rows into n segments can need, and each workgroup finds its
 // tile by a prefix sum of the segments' tile counts, 64 segments per step in one wave.
+//
+// Operands.  In the MFMA's operands neighbouring lanes hold different rows of a row-major
+// matrix.  Loaded like that, each 16 bytes of a wave's load are a cache line of their own, and
+// the line look-ups, not the bytes, set the time (8 bytes per cycle and CU measured).  So
+// every matrix is loaded and stored with neighbouring lanes on neighbouring 16 bytes of a
+// row, and turned into operand order, or back, through LDS private to the wave, its 16-byte
+// slots exclusive-ored with the row so that neither side meets a bank twice.  t itself is
+// kept in operand order in the workspace.
 //
 // t keeps fp32 accuracy through the bf16 MFMA: it is split into bf16 terms h = bf16(t),
 // m = bf16(t - h), l = bf16(t - h - m) which multiply the same operand.  Two terms
@@ -25,339 +34,629 @@
 namespace svdq {
 namespace {
 
-constexpr int kColTile = 256;    // output columns of a workgroup of the up-projection
+constexpr int kColTile = 256;    // output columns of a workgroup
 
 struct Tile {
-    int seg;    // segment index
     int row0;   // first row
     int rows;   // rows of the tile, 1 to the tile height; 0: no tile
+    int id;     // the segment's seg_adapter
+    int block;  // the first of its blocks of 16 rows, counted over the segments in order
 };
 
-// Tile `want` of the segments' tiles of `tm` rows, in order.  Offsets are clamped to [0, M]
+__device__ __forceinline__ int wave_scan(int v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(v, d, 64);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+// Tile `want` of the segments' tiles of 16 TB rows, in order.  Offsets are clamped to [0, M]
 // and a segment whose end lies before its start is empty, so that no offset reaches memory
 // outside the rows.  Every lane of the wave calls it and gets the same answer.
-__device__ __forceinline__ Tile find_tile(const int* __restrict__ starts, int n, int M, int tm,
-                                          int want) {
-    const int lane = threadIdx.x & 63;
-    int before = 0;
+template <int TB>
+__device__ __forceinline__ Tile find_tile(const LoraBatchArgs& a, int want) {
+    const int lane = threadIdx.x & 63, n = a.n_segments, M = (int)a.M;
+    int before = 0, blocks = 0;
     for (int c = 0; c < n; c += 64) {
         const int i = c + lane;
-        int a = 0, len = 0;
+        int r0 = 0, len = 0, id = -1;
         if (i < n) {
-            a = min(max(starts[i], 0), M);
-            len = max(min(max(starts[i + 1], 0), M) - a, 0);
+            id = a.ids[i];
+            r0 = min(max(a.starts[i], 0), M);
+            len = max(min(max(a.starts[i + 1], 0), M) - r0, 0);
         }
-        const int nt = (len + tm - 1) / tm;
-        int sum = nt;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(sum, d, 64);
-            if (lane >= d) sum += o;
-        }
+        const int nt = (len + 16 * TB - 1) / (16 * TB), nb = (len + 15) >> 4;
+        const int sum = wave_scan(nt), bsum = TB == 1 ? sum : wave_scan(nb);
         const unsigned long long past = __ballot(before + sum > want);
         if (past != 0) {
             const int src = __ffsll(past) - 1;
-            const int first = before + __shfl(sum - nt, src, 64);
-            const int off = (want - first) * tm;
-            return Tile{c + src, __shfl(a, src, 64) + off, min(tm, __shfl(len, src, 64) - off)};
+            const int off = want - before - __builtin_amdgcn_readlane(sum - nt, src);
+            return Tile{__builtin_amdgcn_readlane(r0, src) + off * 16 * TB,
+                        min(16 * TB, __builtin_amdgcn_readlane(len, src) - off * 16 * TB),
+                        __builtin_amdgcn_readlane(id, src),
+                        blocks + __builtin_amdgcn_readlane(bsum - nb, src) + off * TB};
         }
-        before += __shfl(sum, 63, 64);
+        before += __builtin_amdgcn_readlane(sum, 63);
+        blocks += __builtin_amdgcn_readlane(bsum, 63);
     }
-    return Tile{0, 0, 0};
+    return Tile{0, 0, -1, 0};
 }
+
+// A tile's adapter, its rank (0: none, as for an index outside the pool) and its scale.
+struct Adapter {
+    int s, rank;
+    float alpha;
+};
+
+__device__ __forceinline__ Adapter adapter_of(const LoraBatchArgs& a, int id) {
+    if (id < 0 || id >= a.n_adapters) return Adapter{0, 0, 0.f};
+    return Adapter{id, a.ranks == nullptr ? a.R : min(max(a.ranks[id], 0), a.R), a.alphas[id]};
+}
+
+// Whether rows without adapter stay as they are: no activation, in place.
+__device__ __forceinline__ bool unchanged(const LoraBatchArgs& a) { return a.act == 0 && a.base == a.out; }
 
 __device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
 }
 
-// Adapter of a segment and its rank; -1 for none (and for an index outside the pool).
-__device__ __forceinline__ int adapter_of(const LoraBatchArgs& a, int seg, int& rank) {
-    const int s = a.ids[seg];
-    if (s < 0 || s >= a.n_adapters) { rank = 0; return -1; }
-    rank = a.ranks == nullptr ? a.R : min(max(a.ranks[s], 0), a.R);
-    return rank == 0 ? -1 : s;
+__device__ __forceinline__ uint4 only_if(bool on, uint4 v) {
+    return make_uint4(on ? v.x : 0u, on ? v.y : 0u, on ? v.z : 0u, on ? v.w : 0u);
 }
 
-// Down-projection of one tile of 16 RBM rows: the W waves take the 64-channel steps of K in
-// turn, each with the whole tile's accumulators, and their sums are added in wave order.
-// With gridDim.y > 1 the steps are dealt over that many workgroups too and each writes its
-// own partial t (the up-projection adds them in order).  A lane's 32 bytes of a step are
-// contiguous (channels 16 q to 16 q + 15 of the step; both operands take the same order, and
-// the sum does not mind), so four lanes cover a row's 128 bytes.
-// RB: rank blocks of 16 in registers.  Blocks past the adapter's rank repeat its last one
-// and are not stored.
-template <int RBM, int RB, int W>
-__global__ __launch_bounds__(W * 64) void lora_down_kernel(LoraBatchArgs a) {
-    __shared__ f32x4 red[W][RBM * RB][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, q = lane >> 4, r16 = lane & 15;
-    const Tile t = find_tile(a.starts, a.n_segments, (int)a.M, RBM * 16, (int)blockIdx.x);
-    if (t.rows == 0) return;
-    int rank;
-    const int s = adapter_of(a, t.seg, rank);
-    if (s < 0) return;
-    const int nrb = (rank + 15) >> 4;
-    const int K = a.K, steps = K >> 6;
+// Between a wave's writes to its LDS and its lanes' reads of one another's: the LDS serves a
+// wave in order, so only the compiler has to keep them so.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
-    const uint16_t* xp[RBM];
+// 16 rows x 128 channels as loaded (v[g]: rows 4 g to 4 g + 3, 16 lanes to a row) to the
+// operands of 4 steps of 32 channels, through 4 KB of LDS.
+__device__ __forceinline__ void to_operands(uint4* buf, const uint4 (&v)[4], uint4 (&op)[4]) {
+    const int lane = threadIdx.x & 63, q = lane >> 4, r16 = lane & 15;
+    wave_sync();
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const int row = g * 4 + q;
+        buf[row * 16 + (r16 ^ row)] = v[g];
+    }
+    wave_sync();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) op[k] = buf[r16 * 16 + ((k * 4 + q) ^ r16)];
+}
+
+// One wave's share of the down-projection: every stride-th step of 128 channels from `first`,
+// 16 RBM rows x rank blocks rb0 to rb0 + RB - 1 (those past the adapter's last repeat it; the
+// caller drops them).  U steps are loaded at a time; channels past K count as zeros.
+// acc[i][j]: lane (q, r16) holds ranks 4 q to 4 q + 3 of block j for row 16 i + r16.
+template <int RBM, int RB, int U>
+__device__ __forceinline__ void down_steps(const LoraBatchArgs& a, const Tile& t, const Adapter& ad, int rb0,
+                                           int first, int stride, uint4* buf, f32x4 (&acc)[RBM][RB]) {
+    const int lane = threadIdx.x & 63, q = lane >> 4, r16 = lane & 15, K = a.K;
+    const uint16_t* xp[RBM][4];
 #pragma unroll
     for (int i = 0; i < RBM; ++i)
-        xp[i] = (const uint16_t*)a.x + (int64_t)(t.row0 + min(i * 16 + r16, t.rows - 1)) * a.x_stride + q * 16;
-    const uint16_t* dp[RB];
 #pragma unroll
-    for (int j = 0; j < RB; ++j)
-        dp[j] = (const uint16_t*)a.down + ((int64_t)s * a.R + min(j, nrb - 1) * 16 + r16) * K + q * 16;
-
-    f32x4 acc[RBM][RB];
+        for (int g = 0; g < 4; ++g)
+            xp[i][g] = (const uint16_t*)a.x + (int64_t)(t.row0 + min(i * 16 + g * 4 + q, t.rows - 1)) * a.x_stride;
+    const uint16_t* dp = (const uint16_t*)a.down + ((int64_t)ad.s * a.R + q) * K;
+    const int last = ((ad.rank + 15) >> 4) - 1;
 #pragma unroll
     for (int i = 0; i < RBM; ++i)
 #pragma unroll
         for (int j = 0; j < RB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const int workers = W * gridDim.y;
-    for (int st = blockIdx.y * W + w; st < steps; st += workers) {
-        const int k = st * 64;
-        uint4 xv[RBM][2], dv[RB][2];
+    const int steps = (K + 127) >> 7;
+    for (int st = first; st < steps; st += U * stride) {
+        uint4 xv[U][RBM][4], dv[U][RB][4];
 #pragma unroll
-        for (int i = 0; i < RBM; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) xv[i][h] = *(const uint4*)(xp[i] + k + h * 8);
-#pragma unroll
-        for (int j = 0; j < RB; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) dv[j][h] = *(const uint4*)(dp[j] + k + h * 8);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int u = 0; u < U; ++u) {
+            const int k = (st + u * stride) * 128 + r16 * 8, kk = min(k, K - 8);
 #pragma unroll
             for (int i = 0; i < RBM; ++i)
 #pragma unroll
-                for (int j = 0; j < RB; ++j) acc[i][j] = mfma16(dv[j][h], xv[i][h], acc[i][j]);
+                for (int g = 0; g < 4; ++g) xv[u][i][g] = *(const uint4*)(xp[i][g] + kk);
+#pragma unroll
+            for (int j = 0; j < RB; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    dv[u][j][g] = *(const uint4*)(dp + (int64_t)(min(rb0 + j, last) * 16 + g * 4) * K + kk);
+            if (k != kk) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+#pragma unroll
+                    for (int i = 0; i < RBM; ++i) xv[u][i][g] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < RB; ++j) dv[u][j][g] = make_uint4(0, 0, 0, 0);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            uint4 xo[RBM][4];
+#pragma unroll
+            for (int i = 0; i < RBM; ++i) to_operands(buf, xv[u][i], xo[i]);
+#pragma unroll
+            for (int j = 0; j < RB; ++j) {
+                uint4 d[4];
+                to_operands(buf, dv[u][j], d);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int i = 0; i < RBM; ++i) acc[i][j] = mfma16(d[k], xo[i][k], acc[i][j]);
+            }
+        }
     }
-    // D: lane (q, r16) holds ranks 4 q to 4 q + 3 of row r16
-#pragma unroll
-    for (int i = 0; i < RBM; ++i)
-#pragma unroll
-        for (int j = 0; j < RB; ++j) red[w][i * RB + j][lane] = acc[i][j];
-    __syncthreads();
-    float* out = a.work + (int64_t)blockIdx.y * a.M * a.R;
-    for (int b = w; b < RBM * RB; b += W) {
-        f32x4 v = red[0][b][lane];
-#pragma unroll
-        for (int o = 1; o < W; ++o) v += red[o][b][lane];
-        const int row = b / RB * 16 + r16, rb = b % RB;
-        if (row < t.rows && rb < nrb)
-            *(f32x4*)(out + (int64_t)(t.row0 + row) * a.R + rb * 16 + q * 4) = v;
-    }
-}
-
-// The words of 8 consecutive bf16 with elements at and past `live` cleared.
-__device__ __forceinline__ uint4 keep_first(uint4 v, int live) {
-    if (live >= 8) return v;
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = live >= 2 * i + 2 ? w[i] : live == 2 * i + 1 ? (w[i] & 0xFFFFu) : 0u;
-    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // bf16 terms of v: the first is v rounded (to the largest finite value where rounding would
 // overflow), the next ones the rests; an infinity or NaN stands in the first term alone.
-template <int NT>
-__device__ __forceinline__ void split_terms(float v, uint32_t (&t)[NT]) {
+__device__ __forceinline__ void split_terms(float v, uint32_t (&t)[3]) {
     uint32_t h = f32_to_bf16(v);
     const bool finite = (__float_as_uint(v) & 0x7F800000u) != 0x7F800000u;
     if (finite && (h & 0x7FFFu) == 0x7F80u) h -= 1;
     t[0] = h;
     float rest = v - bf16_to_f32(h);
 #pragma unroll
-    for (int i = 1; i < NT; ++i) {
+    for (int i = 1; i < 3; ++i) {
         t[i] = finite ? f32_to_bf16(rest) : 0u;
         rest -= bf16_to_f32(t[i]);
     }
 }
 
-// Up-projection of a tile of 16 RBE rows x 256 columns, 64 columns to a wave, with the
-// adapter's B as the MFMA's row operand, so that a lane ends with consecutive columns of one
-// row: B's rows are dealt so that 16-byte pieces of base and out are loaded and stored, four
-// lanes covering 64 contiguous bytes of a row.
-template <int RBE, bool BF16>
-__global__ __launch_bounds__(256) void lora_up_kernel(LoraBatchArgs a) {
-    constexpr int NT = BF16 ? 2 : 3;
-    extern __shared__ uint4 terms[];   // [NT][kb][RBE][64] operands
+// Ranks of the up-projection go in NB blocks of 32 (16 ranks in all: NB = 0, one half block).
+// Every block of the instantiation is multiplied, with zeros at and past the adapter's rank.
+constexpr int blocks_of(int NB) { return NB == 0 ? 1 : NB; }
+// Operands of a block of 16 rows' t: one for each term; in the half block the first holds the
+// first term in lanes q = 0, 1 and the second in q = 2, 3, the other the third and zeros.
+constexpr int ops_of(int NB, bool bf16) { return NB == 0 ? (bf16 ? 1 : 2) : (bf16 ? 2 : 3); }
+
+// alpha times ranks j0 to j0 + 3 of row r16, `live` of them below the rank, to their places in
+// the operands `to` [ops][blocks][64 lanes] (blocks = 0: the half block).
+__device__ __forceinline__ void put_terms(uint2* to, int blocks, bool bf16, int j0, int r16, f32x4 v, float alpha,
+                                          int live) {
+    uint32_t t[4][3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split_terms(e < live ? alpha * v[e] : 0.f, t[e]);
+    const int at = (((j0 >> 3) & 3) * 16 + r16) * 2 + ((j0 >> 2) & 1);   // lane's half operand
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+        const uint2 w = make_uint2(t[0][n] | (t[1][n] << 16), t[2][n] | (t[3][n] << 16));
+        if (blocks > 0) {
+            if (n < 2 || !bf16) to[(n * blocks + (j0 >> 5)) * 128 + at] = w;
+        } else if (n < 2) {
+            to[n * 64 + at] = w;
+        } else if (!bf16) {
+            to[128 + at] = w;
+            to[192 + at] = make_uint2(0, 0);
+        }
+    }
+}
+
+// The words of 8 consecutive bf16 with elements at and past `live` cleared.
+__device__ __forceinline__ uint4 keep_first(uint4 v, int live) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = live >= 2 * i + 2 ? w[i] : live == 2 * i + 1 ? (w[i] & 0xFFFFu) : 0u;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Workgroup `id` of a grid of tiles x inner: consecutive workgroups go to the 8 XCDs in turn,
+// so with per > 0 XCD x takes tiles x per to (x + 1) per - 1, each with all its inner parts:
+// rows of one segment, hence its adapter, stay in one XCD's L2.  per = 0: tiles in order.
+__device__ __forceinline__ void tile_of(int id, int per, int inner, int& tile, int& part) {
+    const int l = per > 0 ? id >> 3 : id;
+    tile = l / inner;
+    part = l - tile * inner;
+    if (per > 0) tile += (id & 7) * per;
+}
+
+// Down-projection of a tile of 16 RBM rows, RB rank blocks: the W waves take the steps of K
+// in turn and their sums are added in wave order through LDS.
+template <int RBM, int RB, int W, int U>
+__global__ __launch_bounds__(W * 64) void lora_down_kernel(LoraBatchArgs a, int per, int inner) {
+    constexpr int kSums = W * RBM * RB * 64, kStage = W * 256;
+    static_assert(kSums * 16 <= 65536 && kStage * 16 <= 65536, "64 KB of LDS");
+    __shared__ uint4 lds[kSums > kStage ? kSums : kStage];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, q = lane >> 4, r16 = lane & 15;
-    const Tile t = find_tile(a.starts, a.n_segments, (int)a.M, RBE * 16, (int)blockIdx.x);
+    int tile, part;
+    tile_of(blockIdx.x, per, inner, tile, part);
+    const Tile t = find_tile<RBM>(a, tile);
     if (t.rows == 0) return;
-    int rank;
-    const int s = adapter_of(a, t.seg, rank);
-    if (s < 0 && a.act == 0 && a.base == a.out && a.base_stride == a.out_stride) return;
-    const int nkb = (rank + 31) >> 5;
+    const Adapter ad = adapter_of(a, t.id);
+    if (ad.rank == 0) return;
+    const int rb0 = part * RB;
+    const bool some = rb0 * 16 < ad.rank;   // uniform over the workgroup
+    f32x4* red = (f32x4*)lds;
+    if (some) {
+        f32x4 acc[RBM][RB];
+        down_steps<RBM, RB, U>(a, t, ad, rb0, w, W, lds + w * 256, acc);
+        __syncthreads();                    // the sums take the operands' place
+#pragma unroll
+        for (int i = 0; i < RBM; ++i)
+#pragma unroll
+            for (int j = 0; j < RB; ++j) red[(w * RBM * RB + i * RB + j) * 64 + lane] = acc[i][j];
+        __syncthreads();
+    }
+    const int ranks = a.nb == 0 ? 16 : a.nb * 32, ops = a.nb == 0 ? 2 : 3;
+    for (int b = w; b < RBM * RB; b += W) {
+        const int i = b / RB, j0 = (rb0 + b % RB) * 16 + q * 4;
+        // offsets that break the rules may make more blocks than there is room for
+        if (i * 16 >= t.rows || j0 >= ranks || t.block + i >= a.max_blocks) continue;
+        f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (some) {
+#pragma unroll
+            for (int o = 0; o < W; ++o) v += red[(o * RBM * RB + b) * 64 + lane];
+        }
+        put_terms((uint2*)a.work + (int64_t)(t.block + i) * ops * blocks_of(a.nb) * 128, a.nb, a.bf16 != 0, j0, r16, v,
+                  ad.alpha, ad.rank - j0);
+    }
+}
 
-    if (s >= 0) {
-        const float alpha = a.alphas[s];
-        const int octets = nkb * 4;
-        for (int idx = threadIdx.x; idx < RBE * 16 * octets; idx += 256) {
-            const int r = idx / octets, o = idx - r * octets;
-            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (r < t.rows && o * 8 < rank) {
-                const float* p = a.work + (int64_t)(t.row0 + r) * a.R + o * 8;
-                for (int ks = 0; ks < a.splits; ++ks, p += a.M * a.R) {
-                    const f32x4 lo = *(const f32x4*)p, hi = *(const f32x4*)(p + 4);
+// A wave's 16 RBE rows x 16 CB columns of out.
+template <int RBE, int CB, int NB, bool BF16>
+struct UpTile {
+    static constexpr int kOps = ops_of(NB, BF16), kBlocks = blocks_of(NB);
+    static constexpr int kPer = BF16 ? 8 : 4;                 // columns of a 16-byte piece
+    static constexpr int kLanes = 16 * CB / kPer;             // pieces, and lanes, of a row
+    static constexpr int kPieces = RBE * 16 * kLanes / 64;    // a lane's pieces
+    static constexpr int kChunks = NB == 0 ? 2 : NB * 4;      // 16-byte chunks of a row of B
+    static constexpr int kUp = CB * 16 * kChunks / 64;        // a lane's chunks
+    static constexpr int kLds = (CB * 16 * kChunks > RBE * 64 * CB ? CB * 16 * kChunks : RBE * 64 * CB);   // uint4 a wave
+    uint4 base[kPieces];
+    uint4 up[kUp];
+
+    static __device__ __forceinline__ int piece_row(int p) { return (p * 64 + (threadIdx.x & 63)) / kLanes; }
+    static __device__ __forceinline__ int piece_col() { return (threadIdx.x & 63) % kLanes * kPer; }
+
+    __device__ __forceinline__ void load_base(const LoraBatchArgs& a, const Tile& t, int c0) {
+        const int c = c0 + piece_col();
+        const bool on = a.vec && a.base != nullptr && c + kPer <= a.N;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) { v[e] += lo[e]; v[4 + e] += hi[e]; }
-                }
-            }
-            uint32_t wd[NT][4];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                uint32_t tv[NT];
-                split_terms<NT>(o * 8 + e < rank ? alpha * v[e] : 0.f, tv);
-#pragma unroll
-                for (int i = 0; i < NT; ++i) wd[i][e >> 1] = (e & 1) ? wd[i][e >> 1] | (tv[i] << 16) : tv[i];
-            }
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-                terms[((i * nkb + (o >> 2)) * RBE + (r >> 4)) * 64 + (o & 3) * 16 + (r & 15)] =
-                    make_uint4(wd[i][0], wd[i][1], wd[i][2], wd[i][3]);
+        for (int p = 0; p < kPieces; ++p) {
+            base[p] = make_uint4(0, 0, 0, 0);
+            if (on && piece_row(p) < t.rows)
+                base[p] = *(const uint4*)((const char*)a.base +
+                                          ((int64_t)(t.row0 + piece_row(p)) * a.base_stride + c) * (BF16 ? 2 : 4));
         }
     }
-    __syncthreads();
 
-    const int c0 = blockIdx.y * kColTile + w * 64;
-    if (c0 >= a.N) return;
-    f32x4 acc[RBE][4];
+    // B's rows c0 to c0 + 16 CB - 1 (those past N repeat the last one), zeros at and past the rank
+    __device__ __forceinline__ void load_up(const LoraBatchArgs& a, const Adapter& ad, int c0) {
+        const int lane = threadIdx.x & 63, j = lane % kChunks * 8;
+        const uint16_t* p = (const uint16_t*)a.up + (int64_t)ad.s * a.N * a.R + min(j, a.R - 8);
 #pragma unroll
-    for (int i = 0; i < RBE; ++i)
+        for (int i = 0; i < kUp; ++i)
+            up[i] = *(const uint4*)(p + (int64_t)min(c0 + (i * 64 + lane) / kChunks, a.N - 1) * a.R);
+        if (ad.rank < kChunks * 8) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[i][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (s >= 0) {
-        const uint16_t* up[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int col = c0 + (BF16 ? (c >> 1) * 32 + (r16 >> 2) * 8 + (c & 1) * 4 + (r16 & 3) : c * 16 + r16);
-            up[c] = (const uint16_t*)a.up + ((int64_t)s * a.N + min(col, a.N - 1)) * a.R;
+            for (int i = 0; i < kUp; ++i) up[i] = keep_first(up[i], ad.rank - j);
         }
-        for (int kb = 0; kb < nkb; ++kb) {
-            const int k = kb * 32 + q * 8;
-            uint4 bv[4];
+    }
+
+    // acc = t B^T, lane (q, r16) with columns 16 c + 4 q to 16 c + 4 q + 3 of row 16 i + r16
+    // (B is the MFMA's row operand)
+    __device__ __forceinline__ void products(uint4* lds, const uint4 (&tm)[RBE][kOps][kBlocks], f32x4 (&acc)[RBE][CB]) {
+        constexpr int kSpread = 16 / kChunks;   // rows of B to 256 bytes of LDS
+        const int lane = threadIdx.x & 63, q = lane >> 4, r16 = lane & 15;
+        wave_sync();
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                bv[c] = k < rank ? keep_first(*(const uint4*)(up[c] + k), rank - k) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kUp; ++i) {
+            const int n = (i * 64 + lane) / kChunks, j = lane % kChunks;
+            lds[n * kChunks + (j ^ (n / kSpread % kChunks))] = up[i];
+        }
+        wave_sync();
 #pragma unroll
-            for (int i = 0; i < RBE; ++i)
-                if (i * 16 < t.rows) {
+        for (int i = 0; i < RBE; ++i)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const uint4 tv = terms[((n * nkb + kb) * RBE + i) * 64 + lane];
+            for (int c = 0; c < CB; ++c) acc[i][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[i][c] = mfma16(bv[c], tv, acc[i][c]);
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int c = 0; c < CB; ++c) {
+                const int n = c * 16 + r16, j = NB == 0 ? q & 1 : b * 4 + q;
+                const uint4 m = lds[n * kChunks + (j ^ (n / kSpread % kChunks))];
+#pragma unroll
+                for (int o = 0; o < kOps; ++o) {
+                    // the half block's zeros must not meet an infinite B
+                    const uint4 mo = only_if(NB > 0 || o == 0 || q < 2, m);
+#pragma unroll
+                    for (int i = 0; i < RBE; ++i) acc[i][c] = mfma16(mo, tm[i][o][b], acc[i][c]);
+                }
+            }
+    }
+
+    static __device__ __forceinline__ int slot(int row, int chunk) {
+        return row * CB * 4 + (chunk ^ (CB == 4 ? row & 15 : (row >> 1) & 7));
+    }
+
+    // acc from lanes that hold 4 columns to pieces of kPer columns
+    __device__ __forceinline__ void turn(uint4* lds, const f32x4 (&acc)[RBE][CB], float (&y)[kPieces][kPer]) {
+        const int lane = threadIdx.x & 63, q = lane >> 4, r16 = lane & 15;
+        static_assert(CB == 4 || CB == 2, "slots of a row");
+        f32x4* buf = (f32x4*)lds;
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < RBE; ++i)
+#pragma unroll
+            for (int c = 0; c < CB; ++c) buf[slot(i * 16 + r16, c * 4 + q)] = acc[i][c];
+        wave_sync();
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+            for (int h = 0; h < kPer / 4; ++h) {
+                const f32x4 v = buf[slot(piece_row(p), piece_col() / 4 + h)];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[p][h * 4 + e] = v[e];
+            }
+    }
+
+    template <int ACT>
+    __device__ __forceinline__ void store_as(const LoraBatchArgs& a, const Tile& t, int c0, const float (&y)[kPieces][kPer]) {
+        const int c = c0 + piece_col();
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+            if (piece_row(p) >= t.rows) continue;
+            const int64_t m = t.row0 + piece_row(p);
+            if (a.vec && c + kPer <= a.N) {
+                const uint32_t bw[4] = {base[p].x, base[p].y, base[p].z, base[p].w};
+                float v[kPer];
+                uint32_t ow[4];
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                    v[e] = activate(y[p][e] + (!BF16 ? __uint_as_float(bw[e & 3])
+                                                     : __uint_as_float((e & 1) ? bw[e >> 1] & 0xFFFF0000u : bw[(e >> 1) & 3] << 16)),
+                                    ACT);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    ow[e] = BF16 ? pack_bf16(v[(2 * e) % kPer], v[(2 * e + 1) % kPer]) : __float_as_uint(v[e]);
+                *(uint4*)((char*)a.out + (m * a.out_stride + c) * (BF16 ? 2 : 4)) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                    if (c + e < a.N) {
+                        float v = y[p][e];
+                        if constexpr (BF16) {
+                            if (a.base != nullptr) v += bf16_to_f32(((const uint16_t*)a.base)[m * a.base_stride + c + e]);
+                            ((uint16_t*)a.out)[m * a.out_stride + c + e] = (uint16_t)f32_to_bf16(activate(v, ACT));
+                        } else {
+                            if (a.base != nullptr) v += ((const float*)a.base)[m * a.base_stride + c + e];
+                            ((float*)a.out)[m * a.out_stride + c + e] = activate(v, ACT);
+                        }
                     }
-                }
+            }
         }
     }
 
+    __device__ __forceinline__ void store(const LoraBatchArgs& a, const Tile& t, int c0, const float (&y)[kPieces][kPer]) {
+        if (a.act == 1) store_as<1>(a, t, c0, y);
+        else if (a.act == 2) store_as<2>(a, t, c0, y);
+        else store_as<0>(a, t, c0, y);
+    }
+
+    // rows without adapter: out = act(base)
+    __device__ __forceinline__ void store_base(const LoraBatchArgs& a, const Tile& t, int c0) {
+        float y[kPieces][kPer];
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) y[p][e] = 0.f;
+        store(a, t, c0, y);
+    }
+};
+
+// A workgroup's rows x `blocks` blocks of 64 CB columns, 16 CB columns to each of 4 waves: t
+// stays in registers, and a block's base and B are loaded while the one before is worked on.
+template <int RBE, int CB, int NB, bool BF16>
+__device__ __forceinline__ void up_blocks(const LoraBatchArgs& a, const Tile& t, const Adapter& ad, int first,
+                                          int blocks, uint4* lds) {
+    using Up = UpTile<RBE, CB, NB, BF16>;
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    auto col = [&](int b) { return ((first + b) * 4 + w) * 16 * CB; };
+    Up u, next;
+    u.load_base(a, t, col(0));
+    u.load_up(a, ad, col(0));
+    uint4 tm[RBE][Up::kOps][Up::kBlocks];
+    const int wb = blocks_of(a.nb), ops = a.nb == 0 ? 2 : 3;
 #pragma unroll
     for (int i = 0; i < RBE; ++i) {
-        const int row = i * 16 + r16;
-        if (row >= t.rows) continue;
-        const int64_t m = t.row0 + row;
-        if constexpr (BF16) {
-            const uint16_t* bp = a.base == nullptr ? nullptr : (const uint16_t*)a.base + m * a.base_stride;
-            uint16_t* op = (uint16_t*)a.out + m * a.out_stride;
+        const uint4* src = (const uint4*)a.work +
+                           (int64_t)min(t.block + (i * 16 < t.rows ? i : 0), a.max_blocks - 1) * ops * wb * 64 + lane;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int c = c0 + h * 32 + q * 8;
-                float y[8];
+        for (int o = 0; o < Up::kOps; ++o)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = acc[i][2 * h + (e >> 2)][e & 3];
-                if (a.vec && c + 8 <= a.N) {
-                    if (bp != nullptr) {
-                        const uint4 b = *(const uint4*)(bp + c);
-                        const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] += bf16_to_f32((bw[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-                    }
-                    uint32_t ow[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        ow[e] = f32_to_bf16(activate(y[2 * e], a.act)) | (f32_to_bf16(activate(y[2 * e + 1], a.act)) << 16);
-                    *(uint4*)(op + c) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (c + e < a.N) {
-                            const float b = bp != nullptr ? bf16_to_f32(bp[c + e]) : 0.f;
-                            op[c + e] = (uint16_t)f32_to_bf16(activate(y[e] + b, a.act));
-                        }
-                }
-            }
-        } else {
-            const float* bp = a.base == nullptr ? nullptr : (const float*)a.base + m * a.base_stride;
-            float* op = (float*)a.out + m * a.out_stride;
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const int c = c0 + h * 16 + q * 4;
-                f32x4 y = acc[i][h];
-                if (a.vec && c + 4 <= a.N) {
-                    if (bp != nullptr) y += *(const f32x4*)(bp + c);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = activate(y[e], a.act);
-                    *(f32x4*)(op + c) = y;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (c + e < a.N) op[c + e] = activate(y[e] + (bp != nullptr ? bp[c + e] : 0.f), a.act);
-                }
-            }
+            for (int b = 0; b < Up::kBlocks; ++b) tm[i][o][b] = src[(o * wb + b) * 64];
+    }
+    for (int b = 0; b < blocks; ++b) {
+        if (b + 1 < blocks) {
+            next.load_base(a, t, col(b + 1));
+            next.load_up(a, ad, col(b + 1));
+        }
+        f32x4 acc[RBE][CB];
+        float y[Up::kPieces][Up::kPer];
+        u.products(lds, tm, acc);
+        u.turn(lds, acc, y);
+        u.store(a, t, col(b), y);
+        u = next;
+    }
+}
+
+// Up-projection of a tile of 16 RBE rows, `span` blocks of columns.
+template <int RBE, int CB, int NB, bool BF16>
+__global__ __launch_bounds__(256) void lora_up_kernel(LoraBatchArgs a, int per, int inner, int span) {
+    using Up = UpTile<RBE, CB, NB, BF16>;
+    __shared__ uint4 lds[4][Up::kLds];
+    int tile, part;
+    tile_of(blockIdx.x, per, inner, tile, part);
+    const Tile t = find_tile<RBE>(a, tile);
+    if (t.rows == 0) return;
+    const int first = part * span, w = threadIdx.x >> 6;
+    const int blocks = min(span, (a.N + 64 * CB - 1) / (64 * CB) - first);
+    const Adapter ad = adapter_of(a, t.id);
+    if (ad.rank == 0) {
+        if (unchanged(a)) return;
+        for (int b = 0; b < blocks; ++b) {
+            UpTile<RBE, CB, 0, BF16> u;
+            const int c0 = ((first + b) * 4 + w) * 16 * CB;
+            u.load_base(a, t, c0);
+            u.store_base(a, t, c0);
+        }
+        return;
+    }
+    if constexpr (NB > 2) {
+        if (ad.rank <= 64) {
+            up_blocks<RBE, CB, 2, BF16>(a, t, ad, first, blocks, lds[w]);
+            return;
         }
     }
+    up_blocks<RBE, CB, NB, BF16>(a, t, ad, first, blocks, lds[w]);
+}
+
+// Both products for a tile of 16 rows x 256 columns, 32 columns to each of 8 waves: the waves
+// share the steps of K, and the rows' t goes through LDS.
+template <int RB, bool BF16, int U>
+__global__ __launch_bounds__(512) void lora_few_rows_kernel(LoraBatchArgs a, int inner) {
+    constexpr int W = 8, NB = RB / 2;
+    using Up = UpTile<1, 2, NB, BF16>;
+    constexpr int kStage = Up::kLds > 256 ? Up::kLds : 256;
+    static_assert(kStage >= RB * 64, "the sums take the operands' place");
+    __shared__ uint4 lds[W][kStage];
+    f32x4* red = (f32x4*)lds;
+    __shared__ uint4 terms[ops_of(NB, BF16)][Up::kBlocks][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, q = lane >> 4, r16 = lane & 15;
+    int tile, part;
+    tile_of(blockIdx.x, 0, inner, tile, part);
+    const Tile t = find_tile<1>(a, tile);
+    if (t.rows == 0) return;
+    const int c0 = part * kColTile + w * 32;
+    Up u;
+    u.load_base(a, t, c0);
+    const Adapter ad = adapter_of(a, t.id);
+    if (ad.rank == 0) {
+        if (!unchanged(a)) u.store_base(a, t, c0);
+        return;
+    }
+    u.load_up(a, ad, c0);
+    f32x4 acc[1][RB];
+    down_steps<1, RB, U>(a, t, ad, 0, w, W, lds[w], acc);
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < RB; ++j) red[(w * RB + j) * 64 + lane] = acc[0][j];
+    __syncthreads();
+    if (w < RB) {
+        const int j0 = w * 16 + q * 4;
+        f32x4 v = red[w * 64 + lane];
+#pragma unroll
+        for (int o = 1; o < W; ++o) v += red[(o * RB + w) * 64 + lane];
+        put_terms((uint2*)&terms[0][0][0], NB, BF16, j0, r16, v, ad.alpha, ad.rank - j0);
+    }
+    __syncthreads();
+    uint4 tm[1][Up::kOps][Up::kBlocks];
+#pragma unroll
+    for (int o = 0; o < Up::kOps; ++o)
+#pragma unroll
+        for (int b = 0; b < Up::kBlocks; ++b) tm[0][o][b] = terms[o][b][lane];
+    f32x4 out[1][2];
+    float y[Up::kPieces][Up::kPer];
+    u.products(lds[w], tm, out);
+    u.turn(lds[w], out, y);
+    u.store(a, t, c0, y);
 }
 
 // Most tiles of `tm` rows that n segments of M rows can need.
 int64_t most_tiles(int64_t M, int n, int tm) { return std::min<int64_t>((M + (int64_t)n * (tm - 1)) / tm, M); }
 
-int down_row_blocks(int64_t M) { return M >= 8192 ? 2 : 1; }
+// Blocks of 32 ranks of the pool (0: 16 ranks).
+int rank_blocks(int R) { return R <= 16 ? 0 : R <= 32 ? 1 : R <= 64 ? 2 : 4; }
 
-template <int RBM, int RB>
-void down(const LoraBatchArgs& a, hipStream_t st) {
-    constexpr int W = RBM * RB * 8 <= 64 ? 8 : 4;   // partial sums of W waves: 64 KB of LDS at most
-    const dim3 grid((unsigned)most_tiles(a.M, a.n_segments, RBM * 16), (unsigned)a.splits);
-    hipLaunchKernelGGL((lora_down_kernel<RBM, RB, W>), grid, dim3(W * 64), 0, st, a);
+// Tiles a XCD takes (tile_of): with few tiles they are dealt over all XCDs instead.
+int per_xcd(int64_t tiles) { return tiles >= 64 ? (int)((tiles + 7) / 8) : 0; }
+unsigned grid_of(int64_t tiles, int inner) {
+    const int per = per_xcd(tiles);
+    return (unsigned)((per > 0 ? 8 * per : tiles) * inner);
 }
 
-template <int RBM>
-void down_rank(const LoraBatchArgs& a, hipStream_t st) {
-    if (a.R <= 16) down<RBM, 1>(a, st);
-    else if (a.R <= 32) down<RBM, 2>(a, st);
-    else if (a.R <= 64) down<RBM, 4>(a, st);
-    else down<RBM, 8>(a, st);
+template <int RBM, int RB, int W, int U>
+void down(const LoraBatchArgs& a, hipStream_t st) {
+    const int64_t tiles = most_tiles(a.M, a.n_segments, RBM * 16);
+    const int inner = ((a.nb == 0 ? 1 : a.nb * 2) + RB - 1) / RB;
+    hipLaunchKernelGGL((lora_down_kernel<RBM, RB, W, U>), dim3(grid_of(tiles, inner)), dim3(W * 64), 0, st, a,
+                       per_xcd(tiles), inner);
+}
+
+void launch_down(const LoraBatchArgs& a, hipStream_t st) {
+    if (a.M >= 8192) {
+        if (a.R <= 16) down<2, 1, 8, 2>(a, st);
+        else if (a.R <= 32) down<2, 2, 8, 1>(a, st);
+        else down<2, 4, 8, 1>(a, st);
+        return;
+    }
+    // rank blocks of a workgroup: as many as leave a workgroup for each of 256 CUs
+    const int64_t tiles = most_tiles(a.M, a.n_segments, 16);
+    const int rb = a.R / 16;
+    auto fills = [&](int per) { return tiles * ((rb + per - 1) / per) >= 256; };
+    if (rb == 1 || !fills(2)) down<1, 1, 16, 2>(a, st);
+    else if (rb == 2 || !fills(4)) down<1, 2, 16, 1>(a, st);
+    else down<1, 4, 16, 1>(a, st);
+}
+
+template <int RBE, int NB, bool BF16>
+void up(const LoraBatchArgs& a, hipStream_t st) {
+    constexpr int CB = NB == 4 ? 2 : 4;
+    const int64_t tiles = most_tiles(a.M, a.n_segments, RBE * 16);
+    const int blocks = (a.N + 64 * CB - 1) / (64 * CB);
+    int span = 1;
+    while (span < 8 && span < blocks && tiles * ((blocks + 2 * span - 1) / (2 * span)) >= 1024) span *= 2;
+    const int inner = (blocks + span - 1) / span;
+    hipLaunchKernelGGL((lora_up_kernel<RBE, CB, NB, BF16>), dim3(grid_of(tiles, inner)), dim3(256), 0, st, a,
+                       per_xcd(tiles), inner, span);
 }
 
 template <int RBE, bool BF16>
-void up(const LoraBatchArgs& a, hipStream_t st) {
-    const size_t lds = (size_t)(BF16 ? 2 : 3) * ((a.R + 31) / 32) * RBE * 64 * 16;
-    const dim3 grid((unsigned)most_tiles(a.M, a.n_segments, RBE * 16), (unsigned)((a.N + kColTile - 1) / kColTile));
-    hipLaunchKernelGGL((lora_up_kernel<RBE, BF16>), grid, dim3(256), lds, st, a);
+void up_rank(const LoraBatchArgs& a, hipStream_t st) {
+    switch (a.nb) {
+        case 0: up<RBE, 0, BF16>(a, st); break;
+        case 1: up<RBE, 1, BF16>(a, st); break;
+        case 2: up<RBE, 2, BF16>(a, st); break;
+        default: up<RBE, 4, BF16>(a, st);
+    }
+}
+
+template <bool BF16>
+void few_rows(const LoraBatchArgs& a, hipStream_t st) {
+    const int inner = (a.N + kColTile - 1) / kColTile;
+    const dim3 grid((unsigned)(most_tiles(a.M, a.n_segments, 16) * inner)), block(512);
+    if (a.R <= 16) hipLaunchKernelGGL((lora_few_rows_kernel<1, BF16, 2>), grid, block, 0, st, a, inner);
+    else if (a.R <= 32) hipLaunchKernelGGL((lora_few_rows_kernel<2, BF16, 1>), grid, block, 0, st, a, inner);
+    else hipLaunchKernelGGL((lora_few_rows_kernel<4, BF16, 1>), grid, block, 0, st, a, inner);
 }
 
 }  // namespace
 
-int lora_batch_splits(int64_t M, int K, int n_segments) {
-    const int64_t tiles = most_tiles(M, n_segments, down_row_blocks(M) * 16);
-    const int64_t want = (512 + tiles - 1) / tiles;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({want, 8, K / 64 / 8}));
-}
-
-int64_t lora_batch_workspace_bytes(int64_t M, int K, int R, int n_segments) {
-    if (M == 0 || n_segments == 0) return 0;
-    return (int64_t)lora_batch_splits(M, K, n_segments) * M * R * 4;
+int64_t lora_batch_workspace_bytes(int64_t M, int R, int n_segments) {
+    // the operands of t for an fp32 output, every block of 16 rows
+    const int nb = rank_blocks(R);
+    return most_tiles(M, n_segments, 16) * ops_of(nb, false) * blocks_of(nb) * 1024;
 }
 
 void launch_lora_batch(const LoraBatchArgs& args, hipStream_t st) {
     LoraBatchArgs a = args;
-    a.splits = lora_batch_splits(a.M, a.K, a.n_segments);
-    if (down_row_blocks(a.M) == 2) down_rank<2>(a, st);
-    else down_rank<1>(a, st);
-    const bool tall = (a.M / 64) * ((a.N + kColTile - 1) / kColTile) >= 512;
-    if (a.bf16) tall ? up<4, true>(a, st) : up<1, true>(a, st);
-    else tall ? up<4, false>(a, st) : up<1, false>(a, st);
+    a.nb = rank_blocks(a.R);
+    a.max_blocks = (int)most_tiles(a.M, a.n_segments, 16);
+    const int64_t inner = (a.N + kColTile - 1) / kColTile;
+    if (a.R <= 64 && a.max_blocks * inner <= 512 && (int64_t)a.R * a.K <= 1 << 18) {
+        a.bf16 ? few_rows<true>(a, st) : few_rows<false>(a, st);
+        return;
+    }
+    launch_down(a, st);
+    const bool tall = (a.M / 32) * inner >= 1024;
+    if (a.bf16) tall ? up_rank<2, true>(a, st) : up_rank<1, true>(a, st);
+    else tall ? up_rank<2, false>(a, st) : up_rank<1, false>(a, st);
 }
 
 }  // namespace svdq
