@@ -115,15 +115,15 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// 16 rows x 128 channels as loaded (v[g]: rows 4 g to 4 g + 3, 16 lanes to a row) to the
-// operands of 4 steps of 32 channels, through 4 KB of LDS.
-__device__ __forceinline__ void to_operands(uint4* buf, const uint4 (&v)[4], uint4 (&op)[4]) {
+// 16 rows x 128 channels as loaded (v[g]: rows 4 g to 4 g + 3, 16 lanes to a row; zeros for a
+// lane that is off) to the operands of 4 steps of 32 channels, through 4 KB of LDS.
+__device__ __forceinline__ void to_operands(uint4* buf, const uint4 (&v)[4], bool on, uint4 (&op)[4]) {
     const int lane = threadIdx.x & 63, q = lane >> 4, r16 = lane & 15;
     wave_sync();
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
         const int row = g * 4 + q;
-        buf[row * 16 + (r16 ^ row)] = v[g];
+        buf[row * 16 + (r16 ^ row)] = only_if(on, v[g]);
     }
     wave_sync();
 #pragma unroll
@@ -166,25 +166,18 @@ __device__ __forceinline__ void down_steps(const LoraBatchArgs& a, const Tile& t
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
                     dv[u][j][g] = *(const uint4*)(dp + (int64_t)(min(rb0 + j, last) * 16 + g * 4) * K + kk);
-            if (k != kk) {
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-#pragma unroll
-                    for (int i = 0; i < RBM; ++i) xv[u][i][g] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int j = 0; j < RB; ++j) dv[u][j][g] = make_uint4(0, 0, 0, 0);
-                }
-            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            // zeroed here and not at the load, which nothing should have to wait for
+            const bool on = (st + u * stride) * 128 + r16 * 8 < K;
             uint4 xo[RBM][4];
 #pragma unroll
-            for (int i = 0; i < RBM; ++i) to_operands(buf, xv[u][i], xo[i]);
+            for (int i = 0; i < RBM; ++i) to_operands(buf, xv[u][i], on, xo[i]);
 #pragma unroll
             for (int j = 0; j < RB; ++j) {
                 uint4 d[4];
-                to_operands(buf, dv[u][j], d);
+                to_operands(buf, dv[u][j], on, d);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -296,6 +289,105 @@ __global__ __launch_bounds__(W * 64) void lora_down_kernel(LoraBatchArgs a, int 
         put_terms((uint2*)a.work + (int64_t)(t.block + i) * ops * blocks_of(a.nb) * 128, a.nb, a.bf16 != 0, j0, r16, v,
                   ad.alpha, ad.rank - j0);
     }
+}
+
+// Down-projection of a tile of 16 TB rows, 16 NRB ranks, for ranks past 32: the rows and the
+// adapter's A are staged once for the workgroup, 128 channels at a time, and each wave has RW
+// row blocks x KW rank blocks over all of K.  D steps are in flight in registers.  OCC waves a
+// SIMD: ragged segments make a few more tiles than fill the CUs evenly, and those must find
+// room beside the others, or they cost a whole round.
+// Steps are counted from another one in each tile, round the end of K: rows of x and A lie K
+// elements apart, a distance that falls on few memory channels, and workgroups that walk K in
+// step would all ask the same ones.
+template <int TB, int NRB, int RW, int KW, int D, int OCC>
+__global__ __launch_bounds__((TB / RW) * (NRB / KW) * 64, OCC) void lora_down_wide_kernel(LoraBatchArgs a, int per,
+                                                                                          int inner) {
+    constexpr int kWaves = (TB / RW) * (NRB / KW), kRows = 16 * (TB + NRB), kSet = kWaves * 4, kLoads = kRows / kSet;
+    static_assert(kRows % kSet == 0 && kSet % 16 == 0, "whole loads");
+    __shared__ uint4 lds[kRows * 16];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, q = lane >> 4, r16 = lane & 15, K = a.K;
+    int tile, part;
+    tile_of(blockIdx.x, per, inner, tile, part);
+    const Tile t = find_tile<TB>(a, tile);
+    if (t.rows == 0) return;
+    const Adapter ad = adapter_of(a, t.id);
+    if (ad.rank == 0) return;
+    const int rb0 = part * NRB;
+    // thread's rows of the staged tile: tid / 16 + kSet i; rows first, then ranks (those past the
+    // adapter's last block repeat its last row)
+    const uint16_t* src[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int r = (tid >> 4) + kSet * i, j = rb0 * 16 + r - 16 * TB;
+        src[i] = r < 16 * TB
+                     ? (const uint16_t*)a.x + (int64_t)(t.row0 + min(r, t.rows - 1)) * a.x_stride
+                     : (const uint16_t*)a.down + ((int64_t)ad.s * a.R + min(j, (ad.rank + 15) / 16 * 16 - 1)) * K;
+    }
+    const int steps = (K + 127) >> 7, turn = (int)((unsigned)tile * 5u % (unsigned)steps);
+    auto channel = [&](int st) {
+        st = min(st, steps - 1) + turn;
+        return (st >= steps ? st - steps : st) * 128 + r16 * 8;
+    };
+    auto load = [&](uint4 (&v)[kLoads], int st) {
+        const int k = min(channel(st), K - 8);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) v[i] = *(const uint4*)(src[i] + k);
+    };
+    auto put = [&](const uint4 (&v)[kLoads], int st) {
+        const int row = tid >> 4;
+        const bool on = channel(st) < K;   // zeroed here and not at the load, which nothing should wait for
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) lds[(row + kSet * i) * 16 + (r16 ^ (row & 15))] = only_if(on, v[i]);
+        __syncthreads();
+    };
+    f32x4 acc[RW][KW];
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int j = 0; j < KW; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int j0 = w % (NRB / KW) * KW, i0 = w / (NRB / KW) * RW;
+    auto work = [&]() {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int c = (k * 4 + q) ^ r16;
+            uint4 x[RW];
+#pragma unroll
+            for (int i = 0; i < RW; ++i) x[i] = lds[((i0 + i) * 16 + r16) * 16 + c];
+#pragma unroll
+            for (int j = 0; j < KW; ++j) {
+                const uint4 d = lds[((TB + j0 + j) * 16 + r16) * 16 + c];
+#pragma unroll
+                for (int i = 0; i < RW; ++i) acc[i][j] = mfma16(d, x[i], acc[i][j]);
+            }
+        }
+    };
+    uint4 v[D][kLoads];
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        load(v[d], d);
+        __builtin_amdgcn_sched_barrier(0);   // in this order, so that the oldest can be waited for alone
+    }
+    for (int st = 0; st < steps; st += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            if (d == 0 || st + d < steps) {
+                put(v[d], st + d);
+                load(v[d], st + d + D);
+                __builtin_amdgcn_sched_barrier(0);
+                work();
+            }
+    }
+    const int ranks = a.nb * 32;
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int j = 0; j < KW; ++j) {
+            const int at = (rb0 + j0 + j) * 16 + q * 4;
+            if ((i0 + i) * 16 < t.rows && at < ranks && t.block + i0 + i < a.max_blocks)
+                put_terms((uint2*)a.work + (int64_t)(t.block + i0 + i) * 3 * a.nb * 128, a.nb, a.bf16 != 0, at, r16,
+                          acc[i][j], ad.alpha, ad.rank - at);
+        }
 }
 
 // A wave's 16 RBE rows x 16 CB columns of out.
@@ -589,7 +681,20 @@ void down(const LoraBatchArgs& a, hipStream_t st) {
                        per_xcd(tiles), inner);
 }
 
+template <int TB, int NRB, int RW, int KW, int D, int OCC>
+void down_wide(const LoraBatchArgs& a, hipStream_t st) {
+    const int64_t tiles = most_tiles(a.M, a.n_segments, TB * 16);
+    const int inner = (a.nb * 2 + NRB - 1) / NRB;
+    hipLaunchKernelGGL((lora_down_wide_kernel<TB, NRB, RW, KW, D, OCC>), dim3(grid_of(tiles, inner)),
+                       dim3((TB / RW) * (NRB / KW) * 64), 0, st, a, per_xcd(tiles), inner);
+}
+
 void launch_down(const LoraBatchArgs& a, hipStream_t st) {
+    if (a.nb >= 2 && most_tiles(a.M, a.n_segments, 64) >= 256) {
+        if (a.nb == 4) down_wide<4, 8, 2, 2, 2, 4>(a, st);
+        else down_wide<4, 4, 2, 1, 2, 4>(a, st);
+        return;
+    }
     if (a.M >= 8192) {
         if (a.R <= 16) down<2, 1, 8, 2>(a, st);
         else if (a.R <= 32) down<2, 2, 8, 1>(a, st);
@@ -600,8 +705,8 @@ void launch_down(const LoraBatchArgs& a, hipStream_t st) {
     const int64_t tiles = most_tiles(a.M, a.n_segments, 16);
     const int rb = a.R / 16;
     auto fills = [&](int per) { return tiles * ((rb + per - 1) / per) >= 256; };
-    if (rb == 1 || !fills(2)) down<1, 1, 16, 2>(a, st);
-    else if (rb == 2 || !fills(4)) down<1, 2, 16, 1>(a, st);
+    if (rb == 1 || !fills(2)) down<1, 1, 16, 1>(a, st);
+    else if (rb == 2 || !fills(4)) down<1, 2, 8, 1>(a, st);
     else down<1, 4, 16, 1>(a, st);
 }
 
