@@ -12,28 +12,28 @@
 // Bound: memory, x once and out once.  A workgroup works on a slab: a range of channels that
 // is whole groups (or, for a group too wide, a part of one), so neighbouring lanes read
 // neighbouring channels and no group is shared where it fits.
-//   resident: an image's slab fits the registers of one workgroup: one launch, x read once,
-//             mean, then squares about it, from the registers.
-//   split:    otherwise two launches.  The first takes chunks of 8 rows per thread, two passes
-//             over each in registers, and joins them as (count, mean, sum of squares about the
-//             mean): for two sets the joined M2 is M2a + M2b + d^2 na nb / (na + nb), d the
-//             difference of the means.  The second joins the row tiles' partial sums (every
-//             workgroup for its own groups, in a fixed order) and normalises.
+//   one launch (few rows): every workgroup of a slab takes the statistics of all its rows and
+//             normalises its own share of them, which it keeps in registers meanwhile.  The
+//             others' rows are read again from the caches; nothing is exchanged.
+//   two launches (many rows): statistics of row tiles, then every workgroup joins those of its
+//             groups, in a fixed order, and normalises a tile.
+// Statistics of a thread go chunk by chunk, two passes over each in registers, joined as
+// (count, mean, sum of squares about the mean): for two sets the joined M2 is
+// M2a + M2b + d^2 na nb / (na + nb), d the difference of the means.
 #include "common.hpp"
 #include "launch.hpp"
 
 #include <algorithm>
 #include <numeric>
+#include <type_traits>
 
 namespace svdq {
 namespace {
 
-constexpr int kRows = 8;          // rows of a chunk
 constexpr int kSplitThreads = 256;
-constexpr int kResidentThreads = 1024;
+constexpr int kOneThreads = 512;
 constexpr int kMaxTiles = 256;    // row tiles of an image
-constexpr int kWide8 = 512;       // widest slab in 8-channel vectors, and in single channels
-constexpr int kWide1 = 64;
+constexpr int kWide = 512;        // channels of the widest slab (64 vectors of 8)
 
 struct Shape {
     GroupNormArgs a;
@@ -44,7 +44,7 @@ struct Shape {
     int slabs;     // slabs of an image
     int vpt;       // vectors of a slab
     int ty;        // row lanes of a workgroup
-    int tiles;     // row tiles of an image (split)
+    int tiles;     // row tiles of an image
     int tile_rows;
 };
 
@@ -59,57 +59,39 @@ __device__ __forceinline__ void slab_range(const Shape& p, int s, int& c0, int& 
     }
 }
 
-// VEC consecutive channels of one position, as loaded.
+// VEC consecutive channels of one position, as loaded: 16 bytes (8 of bf16, 4 of fp32) or one.
 template <int VEC, bool BF16>
 struct Vec {
-    static constexpr int kWords = BF16 ? (VEC + 1) / 2 : VEC;
-    uint32_t w[kWords];
+    uint32_t w[VEC == 1 ? 1 : 4];
     __device__ __forceinline__ void load(const void* base, int64_t at) {
-        if constexpr (BF16) {
-            const uint16_t* p = (const uint16_t*)base + at;
-            if constexpr (VEC == 8) put4(0, *(const uint4*)p);
-            else w[0] = p[0];
+        if constexpr (VEC == 1) {
+            w[0] = BF16 ? ((const uint16_t*)base)[at] : ((const uint32_t*)base)[at];
         } else {
-            const uint32_t* p = (const uint32_t*)base + at;
-            if constexpr (VEC == 8) {
-                put4(0, *(const uint4*)p);
-                put4(4, *(const uint4*)(p + 4));
-            } else {
-                w[0] = p[0];
-            }
+            static_assert(VEC == (BF16 ? 8 : 4), "16 bytes");
+            const uint4 u = *(const uint4*)((const char*)base + at * (BF16 ? 2 : 4));
+            w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
         }
     }
     __device__ __forceinline__ float get(int j) const {
         if constexpr (BF16) return __uint_as_float((j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
         else return __uint_as_float(w[j]);
     }
-
-private:
-    __device__ __forceinline__ void put4(int at, uint4 u) {
-        w[at] = u.x; w[at + 1] = u.y; w[at + 2] = u.z; w[at + 3] = u.w;
-    }
 };
 
-template <int VEC>
-__device__ __forceinline__ void store_vec(void* base, int64_t at, const float (&y)[VEC], int bf16) {
-    if (bf16) {
+template <int VEC, bool BF16>
+__device__ __forceinline__ void store_vec(void* base, int64_t at, const float (&y)[VEC]) {
+    if constexpr (BF16) {
         uint16_t* p = (uint16_t*)base + at;
-        if constexpr (VEC == 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16(y[2 * i]) | (f32_to_bf16(y[2 * i + 1]) << 16);
-            *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-            p[0] = (uint16_t)f32_to_bf16(y[0]);
-        }
+        if constexpr (VEC == 8) *(uint4*)p = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
+                                                        pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+        else if constexpr (VEC == 4) *(uint2*)p = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+        else p[0] = (uint16_t)pack_bf16(y[0], 0.f);
     } else {
         float* p = (float*)base + at;
-        if constexpr (VEC == 8) {
-            *(f32x4*)p = f32x4{y[0], y[1], y[2], y[3]};
-            *(f32x4*)(p + 4) = f32x4{y[4], y[5], y[6], y[7]};
-        } else {
-            p[0] = y[0];
-        }
+        if constexpr (VEC == 1) p[0] = y[0];
+        else
+#pragma unroll
+            for (int h = 0; h < VEC; h += 4) *(f32x4*)(p + h) = f32x4{y[h], y[h + 1], y[h + 2], y[h + 3]};
     }
 }
 
@@ -119,217 +101,279 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
-// The channel's factor and offset.
-__device__ __forceinline__ float load_mod(const void* p, int64_t at, int bf16) {
-    return bf16 ? bf16_to_f32(((const uint16_t*)p)[at]) : ((const float*)p)[at];
-}
-
-template <int VEC>
-__device__ __forceinline__ void channel_terms(const GroupNormArgs& a, int b, int c, float r, float& A, float& D) {
-    const float w = a.weight != nullptr ? bf16_to_f32(((const uint16_t*)a.weight)[c]) : 1.f;
-    const float bias = a.bias != nullptr ? bf16_to_f32(((const uint16_t*)a.bias)[c]) : 0.f;
-    const float ms = a.mod_scale != nullptr ? 1.f + load_mod(a.mod_scale, (int64_t)b * a.mod_stride + c, a.mod_bf16) : 1.f;
-    const float mt = a.mod_shift != nullptr ? load_mod(a.mod_shift, (int64_t)b * a.mod_stride + c, a.mod_bf16) : 0.f;
-    A = r * w * ms;
-    D = bias * ms + mt;
-}
-
-// Sums over the entries of group g of an LDS array [ty][vpt * EPV], its columns [g wd, (g + 1) wd).
+// f(activation, whether out is bf16), both as types: the branch stands outside the loop over rows.
 template <class F>
-__device__ __forceinline__ float group_sum(int ty, int row_len, int wd, int g, F f) {
-    const int lane = threadIdx.x & 63, n = ty * wd;
-    float s = 0.f;
-    for (int i = lane; i < n; i += 64) {
-        const int y = i / wd, c = g * wd + (i - y * wd);
-        s += f(y, y * row_len + c);
-    }
-    return wave_sum(s);
+__device__ __forceinline__ void by_kind(int act, int bf16, F f) {
+    auto kind = [&](auto b) {
+        if (act == 1) f(std::integral_constant<int, 1>{}, b);
+        else if (act == 2) f(std::integral_constant<int, 2>{}, b);
+        else f(std::integral_constant<int, 0>{}, b);
+    };
+    if (bf16) kind(std::true_type{});
+    else kind(std::false_type{});
 }
 
-// One workgroup: one image's slab, kept in registers, R rows a thread.
-// WHOLE: every 8-channel vector lies in one group (then a vector is one LDS entry, otherwise
-// each channel is).
-template <int VEC, bool XBF, bool WHOLE, int R, int BD>
-__global__ __launch_bounds__(BD) void norm_resident_kernel(Shape p) {
-    constexpr int EPV = WHOLE ? 1 : VEC;
-    __shared__ float e[BD * EPV];
-    __shared__ float stat[2][kWide8];   // mean and 1 / sqrt(var + eps) of each group
-    const GroupNormArgs& a = p.a;
-    const int tid = threadIdx.x, w = tid >> 6, waves = BD >> 6;
-    const int b = blockIdx.y;
-    int c0, width, g0, part;
-    slab_range(p, blockIdx.x, c0, width, g0, part);
-    const int vpt = p.vpt, ty = tid / vpt, tx = tid - ty * vpt;
-    const bool on = ty < p.ty;
-    const int rows = (int)a.rows;
-    const int64_t x0 = ((int64_t)b * rows) * a.x_stride + c0 + tx * VEC;
-
-    Vec<VEC, XBF> v[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int r = ty + i * p.ty;
-        if (on && r < rows) v[i].load(a.x, x0 + (int64_t)r * a.x_stride);
-    }
-    const int row_len = vpt * EPV, wd = WHOLE ? p.cg / VEC : p.cg;
-    const float inv = 1.f / ((float)rows * (float)p.cg);
-    float s[EPV];
-#pragma unroll
-    for (int j = 0; j < EPV; ++j) s[j] = 0.f;
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-        if (on && ty + i * p.ty < rows) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) s[WHOLE ? 0 : j] += v[i].get(j);
+// A slab's weight, bias, modulation scale and shift in LDS.  The four kinds are loaded by
+// different threads at a time: one after the other each would cost a memory latency.
+struct Terms {
+    float v[4][kWide];
+    __device__ __forceinline__ void load(const GroupNormArgs& a, int image, int c0, int width, int threads) {
+        for (int i = threadIdx.x; i < 4 * width; i += threads) {
+            const int kind = i / width, ch = i - kind * width;
+            const void* p = kind == 0 ? a.weight : kind == 1 ? a.bias : kind == 2 ? a.mod_scale : a.mod_shift;
+            const int64_t at = (kind < 2 ? 0 : (int64_t)image * a.mod_stride) + c0 + ch;
+            float f = kind == 0 ? 1.f : 0.f;
+            if (p != nullptr) f = kind < 2 || a.mod_bf16 ? bf16_to_f32(((const uint16_t*)p)[at]) : ((const float*)p)[at];
+            v[kind][ch] = f;
         }
-    if (on) {
-#pragma unroll
-        for (int j = 0; j < EPV; ++j) e[ty * row_len + tx * EPV + j] = s[j];
     }
-    __syncthreads();
-    for (int g = w; g < p.gs; g += waves) {
-        const float sum = group_sum(p.ty, row_len, wd, g, [&](int, int at) { return e[at]; });
-        if ((tid & 63) == 0) stat[0][g] = sum * inv;
+    // out = act((x - mean) A + D) for channel ch of the slab and r = 1 / sqrt(var + eps)
+    __device__ __forceinline__ void fold(int ch, float r, float& A, float& D) const {
+        const float m = 1.f + v[2][ch];
+        A = r * v[0][ch] * m;
+        D = v[1][ch] * m + v[3][ch];
     }
-    __syncthreads();
-    float mean[EPV];
+};
+
+// A thread's running statistics, channel by channel.
+template <int VEC>
+struct Stats {
+    float n, mean[VEC], m2[VEC];
+    __device__ __forceinline__ void clear() {
+        n = 0.f;
 #pragma unroll
-    for (int j = 0; j < EPV; ++j) {
-        mean[j] = on ? stat[0][(tx * VEC + j) / p.cg] : 0.f;
-        s[j] = 0.f;
+        for (int j = 0; j < VEC; ++j) mean[j] = m2[j] = 0.f;
     }
+    // R rows, the first `live` (1 to R) of them counted
+    template <int R, bool XBF>
+    __device__ __forceinline__ void add(const Vec<VEC, XBF> (&v)[R], int live) {
+        const float nc = (float)live, tot = n + nc, inv = 1.f / nc, share = nc / tot, wgt = n * share;
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-        if (on && ty + i * p.ty < rows) {
+        for (int j = 0; j < VEC; ++j) {
+            float s = 0.f, q = 0.f;
+            if (live == R) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float d = v[i].get(j) - mean[WHOLE ? 0 : j];
-                s[WHOLE ? 0 : j] += d * d;
+                for (int i = 0; i < R; ++i) s += v[i].get(j);
+            } else {
+#pragma unroll
+                for (int i = 0; i < R; ++i) s += i < live ? v[i].get(j) : 0.f;
             }
-        }
-    if (on) {
+            const float cm = s * inv;
+            if (live == R) {
 #pragma unroll
-        for (int j = 0; j < EPV; ++j) e[ty * row_len + tx * EPV + j] = s[j];
-    }
-    __syncthreads();
-    for (int g = w; g < p.gs; g += waves) {
-        const float sum = group_sum(p.ty, row_len, wd, g, [&](int, int at) { return e[at]; });
-        if ((tid & 63) == 0) stat[1][g] = 1.f / sqrtf(sum * inv + a.eps);
-    }
-    __syncthreads();
-    if (!on) return;
-    float A[VEC], D[VEC];
+                for (int i = 0; i < R; ++i) {
+                    const float d = v[i].get(j) - cm;
+                    q += d * d;
+                }
+            } else {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        const int c = tx * VEC + j;
-        channel_terms<VEC>(a, b, c0 + c, stat[1][c / p.cg], A[j], D[j]);
-    }
-    const int64_t o0 = ((int64_t)b * rows) * a.out_stride + c0 + tx * VEC;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int r = ty + i * p.ty;
-        if (r < rows) {
-            float y[VEC];
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) y[j] = activate((v[i].get(j) - mean[WHOLE ? 0 : j]) * A[j] + D[j], a.act);
-            store_vec<VEC>(a.out, o0 + (int64_t)r * a.out_stride, y, a.out_bf16);
-        }
-    }
-}
-
-// Partial statistics of one row tile of a slab: (mean, M2) of each of its groups (or of its
-// part of one) to work[b][group][part * tiles + tile].
-template <int VEC, bool XBF, bool WHOLE>
-__global__ __launch_bounds__(kSplitThreads) void norm_stats_kernel(Shape p) {
-    constexpr int EPV = WHOLE ? 1 : VEC;
-    __shared__ float e[2][kSplitThreads * EPV];   // mean, M2
-    __shared__ float cnt[kSplitThreads];          // values behind an entry, by row lane
-    const GroupNormArgs& a = p.a;
-    const int tid = threadIdx.x, w = tid >> 6;
-    const int tile = blockIdx.x, b = blockIdx.z;
-    int c0, width, g0, part;
-    slab_range(p, blockIdx.y, c0, width, g0, part);
-    const int vpt = p.vpt, ty = tid / vpt, tx = tid - ty * vpt;
-    const bool on = ty < p.ty && tx * VEC < width;
-    const int64_t r_end = min((int64_t)(tile + 1) * p.tile_rows, a.rows);
-    const int64_t x0 = ((int64_t)b * a.rows) * a.x_stride + c0 + tx * VEC;
-
-    float n = 0.f, mean[VEC], m2[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) mean[j] = m2[j] = 0.f;
-    if (on) {
-        for (int64_t r = (int64_t)tile * p.tile_rows + ty; r < r_end; r += (int64_t)p.ty * kRows) {
-            Vec<VEC, XBF> v[kRows];
-            const int live = (int)min((int64_t)kRows, (r_end - r + p.ty - 1) / p.ty);
-#pragma unroll
-            for (int i = 0; i < kRows; ++i)
-                v[i].load(a.x, x0 + (r + (int64_t)min(i, live - 1) * p.ty) * a.x_stride);
-            const float nc = (float)live, tot = n + nc, wgt = n * nc / tot, share = nc / tot;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                float s = 0.f, q = 0.f;
-#pragma unroll
-                for (int i = 0; i < kRows; ++i) s += i < live ? v[i].get(j) : 0.f;
-                const float cm = s / nc;
-#pragma unroll
-                for (int i = 0; i < kRows; ++i) {
+                for (int i = 0; i < R; ++i) {
                     const float d = i < live ? v[i].get(j) - cm : 0.f;
                     q += d * d;
                 }
-                const float d = cm - mean[j];
-                mean[j] += d * share;
-                m2[j] += q + d * d * wgt;
             }
-            n = tot;
+            const float d = cm - mean[j];
+            mean[j] += d * share;
+            m2[j] += q + d * d * wgt;
         }
+        n = tot;
     }
-    const int row_len = vpt * EPV;
-    if (ty < p.ty) {
-        if constexpr (WHOLE) {
-            float mv = 0.f, qv = 0.f;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) mv += mean[j];
-            mv *= 1.f / VEC;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float d = mean[j] - mv;
-                qv += m2[j] + n * d * d;
+};
+
+// Joins a workgroup's statistics by group.  Entries (a vector where it lies in one group, WHOLE,
+// else a channel) stand in LDS as [row lane][entry]; a group's are its columns [g wd, (g + 1) wd).
+// Waves take the groups in turn; where there are fewer groups than waves, several waves share a
+// group's row lanes.  g's mean and M2 end in stat[0][g], stat[1][g] (both for every thread).
+template <int VEC, bool WHOLE, int BD>
+struct GroupJoin {
+    static constexpr int EPV = WHOLE ? 1 : VEC;
+    static constexpr int kWaves = BD / 64;
+    float mean[BD * EPV], m2[BD * EPV], cnt[BD];
+    float part[kWaves];
+    float stat[2][kWide];
+
+    template <class F>
+    __device__ __forceinline__ void sums(const Shape& p, int wd, F f, float* to) {
+        const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, row_len = p.vpt * EPV;
+        const int per = p.gs >= kWaves ? 1 : kWaves / p.gs;       // waves of a group
+        const int lanes = (p.ty + per - 1) / per;                 // row lanes of a wave
+        const int dy = 64 / wd, dc = 64 - dy * wd;
+        for (int u = w; u < p.gs * per; u += kWaves) {
+            const int g = u % p.gs, y0 = u / p.gs * lanes, y1 = min(y0 + lanes, p.ty);
+            int y = y0 + lane / wd, c = lane - lane / wd * wd;
+            float s = 0.f;
+            while (y < y1) {
+                s += f(y, y * row_len + g * wd + c, g);
+                y += dy;
+                c += dc;
+                if (c >= wd) { c -= wd; ++y; }
             }
-            e[0][ty * row_len + tx] = mv;
-            e[1][ty * row_len + tx] = qv;
-        } else {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                e[0][ty * row_len + tx * EPV + j] = mean[j];
-                e[1][ty * row_len + tx * EPV + j] = m2[j];
+            s = wave_sum(s);
+            if (lane == 0) (per == 1 ? to[g] : part[u]) = s;
+        }
+        if (per > 1) {
+            __syncthreads();
+            for (int g = threadIdx.x; g < p.gs; g += BD) {
+                float s = 0.f;
+                for (int k = 0; k < per; ++k) s += part[k * p.gs + g];
+                to[g] = s;
             }
         }
-        if (tx == 0) cnt[ty] = WHOLE ? n * VEC : n;
+        __syncthreads();
     }
-    __syncthreads();
-    const int wd = (p.parts == 1 ? p.cg : width) / (WHOLE ? VEC : 1);
-    const float total = (float)(r_end - (int64_t)tile * p.tile_rows) * (float)(p.parts == 1 ? p.cg : width);
-    const int q_all = p.parts * p.tiles;
-    for (int g = w; g < p.gs; g += kSplitThreads / 64) {
-        const float gm = group_sum(p.ty, row_len, wd, g, [&](int y, int at) { return cnt[y] * e[0][at]; }) / total;
-        const float gq = group_sum(p.ty, row_len, wd, g, [&](int y, int at) {
-            const float d = e[0][at] - gm;
-            return e[1][at] + cnt[y] * d * d;
-        });
-        if ((tid & 63) == 0)
-            ((float2*)a.work)[((int64_t)b * a.groups + g0 + g) * q_all + part * p.tiles + tile] = make_float2(gm, gq);
+
+    // width: channels of a group in this slab; total: values of a group behind the entries
+    __device__ __forceinline__ void join(const Shape& p, int width, float total, const Stats<VEC>& st, int ty, int tx) {
+        const int row_len = p.vpt * EPV, wd = WHOLE ? width / VEC : width;
+        if (ty < p.ty) {
+            const int at = ty * row_len + tx * EPV;
+            if constexpr (WHOLE) {
+                float mv = 0.f, qv = 0.f;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) mv += st.mean[j];
+                mv *= 1.f / VEC;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float d = st.mean[j] - mv;
+                    qv += st.m2[j] + st.n * d * d;
+                }
+                mean[at] = mv;
+                m2[at] = qv;
+            } else {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    mean[at + j] = st.mean[j];
+                    m2[at + j] = st.m2[j];
+                }
+            }
+            if (tx == 0) cnt[ty] = WHOLE ? st.n * VEC : st.n;
+        }
+        __syncthreads();
+        const float inv = 1.f / total;
+        sums(p, wd, [&](int y, int at, int) { return cnt[y] * mean[at]; }, stat[0]);
+        for (int g = threadIdx.x; g < p.gs; g += BD) stat[0][g] *= inv;
+        __syncthreads();
+        sums(p, wd, [&](int y, int at, int g) {
+            const float d = mean[at] - stat[0][g];
+            return m2[at] + cnt[y] * d * d;
+        }, stat[1]);
     }
+};
+
+// One launch: workgroup (tile, slab, image) keeps its R rows a thread and takes the statistics
+// of all tiles in order, so that every workgroup of the slab gets the same ones.
+template <int VEC, bool XBF, bool WHOLE, int R, int BD>
+__global__ __launch_bounds__(BD) void norm_one_kernel(Shape p) {
+    __shared__ GroupJoin<VEC, WHOLE, BD> lds;
+    __shared__ Terms terms;
+    const GroupNormArgs& a = p.a;
+    const int tid = threadIdx.x, tile = blockIdx.y, b = blockIdx.z, rows = (int)a.rows;
+    int c0, width, g0, part;
+    slab_range(p, blockIdx.x, c0, width, g0, part);
+    const int ty = tid / p.vpt, tx = tid - ty * p.vpt, c = c0 + tx * VEC;
+    const bool on = ty < p.ty;
+    const int64_t x0 = ((int64_t)b * rows) * a.x_stride + c;
+    auto live_at = [&](int k) { return min(R, (rows - (k * p.tile_rows + ty) + p.ty - 1) / p.ty); };
+    auto load = [&](Vec<VEC, XBF> (&v)[R], int k, int live) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            v[i].load(a.x, x0 + (int64_t)(k * p.tile_rows + ty + min(i, live - 1) * p.ty) * a.x_stride);
+    };
+    Vec<VEC, XBF> own[R], v[R], next[R];
+    int live = on ? live_at(0) : 0;
+    if (live > 0) load(v, 0, live);
+    terms.load(a, b, c0, width, BD);
+    Stats<VEC> st;
+    st.clear();
+    for (int k = 0; live > 0; ++k) {
+        const int live_next = k + 1 < p.tiles ? live_at(k + 1) : 0;
+        if (live_next > 0) load(next, k + 1, live_next);
+        st.add(v, live);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (k == tile) own[i] = v[i];
+            v[i] = next[i];
+        }
+        live = live_next;
+    }
+    lds.join(p, p.cg, (float)rows * (float)p.cg, st, ty, tx);
+    if (!on) return;
+    const float inv = 1.f / ((float)rows * (float)p.cg);
+    float mean[VEC], A[VEC], D[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        const int g = (tx * VEC + j) / p.cg;
+        mean[j] = lds.stat[0][g];
+        terms.fold(tx * VEC + j, 1.f / sqrtf(lds.stat[1][g] * inv + a.eps), A[j], D[j]);
+    }
+    const int64_t o0 = ((int64_t)b * rows) * a.out_stride + c;
+    by_kind(a.act, a.out_bf16, [&](auto act, auto obf) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int r = tile * p.tile_rows + ty + i * p.ty;
+            if (r < rows) {
+                float y[VEC];
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) y[j] = activate((own[i].get(j) - mean[j]) * A[j] + D[j], act);
+                store_vec<VEC, decltype(obf)::value>(a.out, o0 + (int64_t)r * a.out_stride, y);
+            }
+        }
+    });
 }
 
-template <int VEC, bool XBF>
+// Two launches, the first: (mean, M2) of each group (or part of one) of a row tile to
+// work[b][group][part * tiles + tile].
+template <int VEC, bool XBF, bool WHOLE, int R>
+__global__ __launch_bounds__(kSplitThreads) void norm_stats_kernel(Shape p) {
+    __shared__ GroupJoin<VEC, WHOLE, kSplitThreads> lds;
+    const GroupNormArgs& a = p.a;
+    const int tid = threadIdx.x, tile = blockIdx.y, b = blockIdx.z;
+    int c0, width, g0, part;
+    slab_range(p, blockIdx.x, c0, width, g0, part);
+    const int ty = tid / p.vpt, tx = tid - ty * p.vpt;
+    const int64_t first = (int64_t)tile * p.tile_rows, end = min(first + p.tile_rows, a.rows);
+    const int64_t x0 = ((int64_t)b * a.rows) * a.x_stride + c0 + tx * VEC;
+    Stats<VEC> st;
+    st.clear();
+    if (ty < p.ty && tx * VEC < width)
+        for (int64_t r = first + ty; r < end; r += (int64_t)p.ty * R) {
+            Vec<VEC, XBF> v[R];
+            const int live = (int)min((int64_t)R, (end - r + p.ty - 1) / p.ty);
+#pragma unroll
+            for (int i = 0; i < R; ++i) v[i].load(a.x, x0 + (r + (int64_t)min(i, live - 1) * p.ty) * a.x_stride);
+            st.add(v, live);
+        }
+    const int gw = p.parts == 1 ? p.cg : width;
+    lds.join(p, gw, (float)(end - first) * (float)gw, st, ty, tx);
+    for (int g = tid; g < p.gs; g += kSplitThreads)
+        ((float2*)a.work)[((int64_t)b * a.groups + g0 + g) * p.parts * p.tiles + part * p.tiles + tile] =
+            make_float2(lds.stat[0][g], lds.stat[1][g]);
+}
+
+// The second: the tiles are taken in the other order, the last ones read being the likeliest
+// in the caches.
+template <int VEC, bool XBF, int R>
 __global__ __launch_bounds__(kSplitThreads) void norm_apply_kernel(Shape p) {
-    __shared__ float stat[2][kWide8];   // a slab has at most that many groups
+    __shared__ float stat[2][kWide];
+    __shared__ Terms terms;
     const GroupNormArgs& a = p.a;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const int tile = blockIdx.x, b = blockIdx.z;
+    const int tile = p.tiles - 1 - blockIdx.y, b = blockIdx.z;
     int c0, width, g0, part;
-    slab_range(p, blockIdx.y, c0, width, g0, part);
-    const int vpt = p.vpt, ty = tid / vpt, tx = tid - ty * vpt;
-    const int64_t r_end = min((int64_t)(tile + 1) * p.tile_rows, a.rows);
+    slab_range(p, blockIdx.x, c0, width, g0, part);
+    const int ty = tid / p.vpt, tx = tid - ty * p.vpt, c = c0 + tx * VEC;
+    const bool on = ty < p.ty && tx * VEC < width;
+    const int64_t first = (int64_t)tile * p.tile_rows, end = min(first + p.tile_rows, a.rows);
+    const int64_t x0 = ((int64_t)b * a.rows) * a.x_stride + c;
+    Vec<VEC, XBF> v[R];
+    int64_t r = first + ty;
+    auto load = [&](int live) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) v[i].load(a.x, x0 + (r + (int64_t)min(i, live - 1) * p.ty) * a.x_stride);
+    };
+    auto live_at = [&]() { return (int)min((int64_t)R, (end - r + p.ty - 1) / p.ty); };
+    if (on && r < end) load(live_at());         // ahead of the statistics
+    terms.load(a, b, c0, width, kSplitThreads);
     const int q_all = p.parts * p.tiles;
     const float total = (float)a.rows * (float)p.cg;
     const float last_rows = (float)(a.rows - (int64_t)(p.tiles - 1) * p.tile_rows);
@@ -337,7 +381,7 @@ __global__ __launch_bounds__(kSplitThreads) void norm_apply_kernel(Shape p) {
         const float2* src = (const float2*)a.work + ((int64_t)b * a.groups + g0 + g) * q_all;
         // values behind partial sum q
         auto count = [&](int q) {
-            const int pt = q / p.tiles, ti = q - pt * p.tiles;
+            const int pt = p.parts == 1 ? 0 : q / p.tiles, ti = q - pt * p.tiles;
             const int wq = p.parts == 1 ? p.cg : min(p.width, p.cg - pt * p.width);
             return (ti == p.tiles - 1 ? last_rows : (float)p.tile_rows) * (float)wq;
         };
@@ -346,9 +390,9 @@ __global__ __launch_bounds__(kSplitThreads) void norm_apply_kernel(Shape p) {
         const float mean = wave_sum(s) / total;
         float m2 = 0.f;
         for (int q = lane; q < q_all; q += 64) {
-            const float2 v = src[q];
-            const float d = v.x - mean;
-            m2 += v.y + count(q) * d * d;
+            const float2 u = src[q];
+            const float d = u.x - mean;
+            m2 += u.y + count(q) * d * d;
         }
         m2 = wave_sum(m2);
         if (lane == 0) {
@@ -357,50 +401,51 @@ __global__ __launch_bounds__(kSplitThreads) void norm_apply_kernel(Shape p) {
         }
     }
     __syncthreads();
-    if (ty >= p.ty || tx * VEC >= width) return;
-    float A[VEC], D[VEC], mean[VEC];
+    if (!on) return;
+    float mean[VEC], A[VEC], D[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-        const int c = tx * VEC + j, g = p.parts == 1 ? c / p.cg : 0;
+        const int g = p.parts == 1 ? (tx * VEC + j) / p.cg : 0;
         mean[j] = stat[0][g];
-        channel_terms<VEC>(a, b, c0 + c, stat[1][g], A[j], D[j]);
+        terms.fold(tx * VEC + j, stat[1][g], A[j], D[j]);
     }
-    const int64_t x0 = ((int64_t)b * a.rows) * a.x_stride + c0 + tx * VEC;
-    const int64_t o0 = ((int64_t)b * a.rows) * a.out_stride + c0 + tx * VEC;
-    for (int64_t r = (int64_t)tile * p.tile_rows + ty; r < r_end; r += (int64_t)p.ty * kRows) {
-        Vec<VEC, XBF> v[kRows];
-        const int live = (int)min((int64_t)kRows, (r_end - r + p.ty - 1) / p.ty);
+    const int64_t o0 = ((int64_t)b * a.rows) * a.out_stride + c;
+    by_kind(a.act, a.out_bf16, [&](auto act, auto obf) {
+        while (r < end) {
+            const int live = live_at();
 #pragma unroll
-        for (int i = 0; i < kRows; ++i)
-            v[i].load(a.x, x0 + (r + (int64_t)min(i, live - 1) * p.ty) * a.x_stride);
+            for (int i = 0; i < R; ++i)
+                if (i < live) {
+                    float y[VEC];
 #pragma unroll
-        for (int i = 0; i < kRows; ++i)
-            if (i < live) {
-                float y[VEC];
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) y[j] = activate((v[i].get(j) - mean[j]) * A[j] + D[j], a.act);
-                store_vec<VEC>(a.out, o0 + (r + (int64_t)i * p.ty) * a.out_stride, y, a.out_bf16);
-            }
-    }
+                    for (int j = 0; j < VEC; ++j) y[j] = activate((v[i].get(j) - mean[j]) * A[j] + D[j], act);
+                    store_vec<VEC, decltype(obf)::value>(a.out, o0 + (r + (int64_t)i * p.ty) * a.out_stride, y);
+                }
+            r += (int64_t)p.ty * R;
+            if (r < end) load(live_at());
+        }
+    });
 }
 
-// Whether 8-channel vectors fit the groups: a slab of whole groups and whole vectors is not
+// Whether vectors of v channels fit the groups: a slab of whole groups and whole vectors is not
 // too wide, or a wide group is itself whole vectors.
-bool vectors_fit(int C, int cg) { return C % 8 == 0 && (std::lcm((int64_t)cg, (int64_t)8) <= kWide8 || cg % 8 == 0); }
+bool vectors_fit(int C, int cg, int v) {
+    return C % v == 0 && (std::lcm((int64_t)cg, (int64_t)v) <= 64 * v || cg % v == 0);
+}
 
-// Cuts the channels into slabs of `v`-channel vectors.
-Shape plan(const GroupNormArgs& a, int v) {
+// Cuts the channels into slabs of `v`-channel vectors: the narrowest even cut into whole groups
+// of `least` channels or more, else the widest.
+Shape plan(const GroupNormArgs& a, int v, int least) {
     Shape p{};
     p.a = a;
     p.cg = a.C / a.groups;
-    const int most = v == 8 ? kWide8 : kWide1;
-    const int64_t unit = v == 8 ? std::lcm((int64_t)p.cg, (int64_t)8) : p.cg;
+    const int most = 64 * v;   // at most 64 vectors
+    const int64_t unit = std::lcm((int64_t)p.cg, (int64_t)v);
     if (unit <= most) {
-        // whole groups: the narrowest even cut of 64 channels or more, else the widest
         const int units = (int)(a.C / unit);
         int m = 1;
         for (int k = 1; k <= units && k * unit <= most; ++k)
-            if (units % k == 0 && m * unit < 64) m = k;
+            if (units % k == 0 && m * unit < least) m = k;
         p.parts = 1;
         p.width = (int)unit * m;
         p.gs = p.width / p.cg;
@@ -415,69 +460,75 @@ Shape plan(const GroupNormArgs& a, int v) {
     return p;
 }
 
-// Row tiles of the split form: about 1024 workgroups, each at least one chunk.
-void plan_tiles(Shape& p) {
+constexpr int kOneRows = 32; // rows a thread takes the statistics of in the one launch, at most
+constexpr int kChunk = 8;    // rows of a thread's chunk in the statistics,
+constexpr int kApply = 4;    // and in the other launch
+
+// The cut of the two launches: about 1024 workgroups, each at least one chunk.
+Shape split_plan(const GroupNormArgs& a, int v) {
+    Shape p = plan(a, v, 64);
     p.ty = kSplitThreads / p.vpt;
-    const int64_t step = (int64_t)p.ty * kRows;
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kMaxTiles, 1024 / std::max<int64_t>(1, p.a.B * p.slabs)));
-    const int64_t per = std::max<int64_t>(1, (p.a.rows + want * step - 1) / (want * step)) * step;
+    const int64_t step = (int64_t)p.ty * kChunk;
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kMaxTiles, 1024 / std::max<int64_t>(1, a.B * p.slabs)));
+    const int64_t per = std::max<int64_t>(1, (a.rows + want * step - 1) / (want * step)) * step;
     p.tile_rows = (int)per;
-    p.tiles = (int)((p.a.rows + per - 1) / per);
+    p.tiles = (int)((a.rows + per - 1) / per);
+    return p;
 }
 
 template <int VEC, bool XBF, bool WHOLE>
-void split(Shape p, hipStream_t st) {
-    plan_tiles(p);
-    const dim3 grid((unsigned)p.tiles, (unsigned)p.slabs, (unsigned)p.a.B);
-    hipLaunchKernelGGL((norm_stats_kernel<VEC, XBF, WHOLE>), grid, dim3(kSplitThreads), 0, st, p);
-    hipLaunchKernelGGL((norm_apply_kernel<VEC, XBF>), grid, dim3(kSplitThreads), 0, st, p);
+void split(const GroupNormArgs& a, hipStream_t st) {
+    const Shape p = split_plan(a, VEC);
+    const dim3 grid((unsigned)p.slabs, (unsigned)p.tiles, (unsigned)a.B);
+    hipLaunchKernelGGL((norm_stats_kernel<VEC, XBF, WHOLE, kChunk>), grid, dim3(kSplitThreads), 0, st, p);
+    hipLaunchKernelGGL((norm_apply_kernel<VEC, XBF, kApply>), grid, dim3(kSplitThreads), 0, st, p);
 }
 
-template <int VEC, bool XBF, bool WHOLE, int R>
-void resident(Shape p, hipStream_t st) {
-    p.ty = kResidentThreads / p.vpt;
-    const dim3 grid((unsigned)p.slabs, (unsigned)p.a.B);
-    hipLaunchKernelGGL((norm_resident_kernel<VEC, XBF, WHOLE, R, kResidentThreads>), grid, dim3(kResidentThreads), 0, st, p);
+template <int VEC, bool XBF, bool WHOLE, int R, int BD>
+void one(Shape p, hipStream_t st) {
+    p.ty = BD / p.vpt;
+    p.tile_rows = p.ty * R;
+    p.tiles = (int)((p.a.rows + p.tile_rows - 1) / p.tile_rows);
+    const dim3 grid((unsigned)p.slabs, (unsigned)p.tiles, (unsigned)p.a.B);
+    hipLaunchKernelGGL((norm_one_kernel<VEC, XBF, WHOLE, R, BD>), grid, dim3(BD), 0, st, p);
 }
 
 template <int VEC, bool XBF, bool WHOLE>
-void run(const Shape& p, hipStream_t st) {
-    // rows a thread would hold; 16 of bf16 or 8 of fp32 take 64 of its 128 registers
-    const int64_t ty = kResidentThreads / p.vpt, each = (p.a.rows + ty - 1) / ty;
-    if (p.parts > 1 || each > (XBF ? 16 : 8)) split<VEC, XBF, WHOLE>(p, st);
-    else if (each <= 1) resident<VEC, XBF, WHOLE, 1>(p, st);
-    else if (each <= 4) resident<VEC, XBF, WHOLE, 4>(p, st);
-    else if (each <= 8) resident<VEC, XBF, WHOLE, 8>(p, st);
-    else if constexpr (XBF) resident<VEC, XBF, WHOLE, 16>(p, st);
+void run(const GroupNormArgs& a, hipStream_t st) {
+    const Shape p = plan(a, VEC, 4 * VEC);
+    const int64_t ty = kOneThreads / p.vpt;                  // row lanes of a workgroup
+    const int64_t each = (a.rows + ty - 1) / ty;             // rows a thread of one workgroup would take
+    if (p.parts > 1 || each > kOneRows) split<VEC, XBF, WHOLE>(a, st);
+    else if (p.vpt * a.rows <= 256) one<VEC, XBF, WHOLE, 1, 256>(p, st);
+    else if (each <= 1) one<VEC, XBF, WHOLE, 1, kOneThreads>(p, st);
+    else one<VEC, XBF, WHOLE, 4, kOneThreads>(p, st);
 }
 
 template <int VEC, bool XBF>
-void run_vec(const Shape& p, hipStream_t st) {
-    if (VEC == 1 || p.cg % VEC == 0) run<VEC, XBF, true>(p, st);
-    else run<VEC, XBF, VEC == 1>(p, st);
+void run_vec(const GroupNormArgs& a, hipStream_t st) {
+    if (VEC == 1 || (a.C / a.groups) % VEC == 0) run<VEC, XBF, true>(a, st);
+    else run<VEC, XBF, VEC == 1>(a, st);
 }
 
 }  // namespace
 
 int64_t group_norm_workspace_bytes(int64_t B, int64_t rows, int C, int groups) {
-    // either cut may be taken, by the buffers' alignment
+    // any of the vectors may be taken, by the types and the buffers' alignment
     int64_t most = 0;
-    for (int v = 1; v <= 8; v += 7) {
+    for (int v : {1, 4, 8}) {
         GroupNormArgs a{};
         a.B = B; a.rows = rows; a.C = C; a.groups = groups;
-        if (B == 0 || rows == 0 || (v == 8 && !vectors_fit(C, C / groups))) continue;
-        Shape p = plan(a, v);
-        plan_tiles(p);
+        if (B == 0 || rows == 0 || !vectors_fit(C, C / groups, v)) continue;
+        const Shape p = split_plan(a, v);
         most = std::max(most, B * groups * (int64_t)p.parts * p.tiles * (int64_t)sizeof(float2));
     }
     return most;
 }
 
 void launch_group_norm(const GroupNormArgs& a, hipStream_t st) {
-    const int v = a.vec && vectors_fit(a.C, a.C / a.groups) ? 8 : 1;
-    const Shape p = plan(a, v);
-    if (v == 8) a.x_bf16 ? run_vec<8, true>(p, st) : run_vec<8, false>(p, st);
-    else a.x_bf16 ? run_vec<1, true>(p, st) : run_vec<1, false>(p, st);
+    const bool vec = a.vec && vectors_fit(a.C, a.C / a.groups, a.x_bf16 ? 8 : 4);
+    if (a.x_bf16) vec ? run_vec<8, true>(a, st) : run_vec<1, true>(a, st);
+    else vec ? run_vec<4, false>(a, st) : run_vec<1, false>(a, st);
 }
 
 }  // namespace svdq
