@@ -31,7 +31,9 @@ namespace svdq {
 namespace {
 
 constexpr int kSplitThreads = 256;
-constexpr int kOneThreads = 512;
+constexpr int kChunk = 8;         // rows of a thread's chunk in the statistics,
+constexpr int kApply = 4;         // and in the launch that only normalises
+constexpr int kOneRows = 8;       // rows a thread takes the statistics of in the one launch, at most
 constexpr int kMaxTiles = 256;    // row tiles of an image
 constexpr int kWide = 512;        // channels of the widest slab (64 vectors of 8)
 
@@ -95,11 +97,23 @@ __device__ __forceinline__ void store_vec(void* base, int64_t at, const float (&
     }
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-    return v;
-}
+// Statistics of a set of n values: their mean and the sum of their squares about it.
+struct Moments {
+    float n, mean, m2;
+    // The union with another set, in this order; an empty set changes nothing.
+    __device__ __forceinline__ void join(float bn, float bmean, float bm2) {
+        if (bn > 0.f) {
+            const float share = bn * __builtin_amdgcn_rcpf(n + bn), d = bmean - mean;
+            mean += d * share;
+            m2 += bm2 + d * d * (n * share);
+            n += bn;
+        }
+    }
+    // The union over the first `lanes` (a power of two) lanes, in lane 0.
+    __device__ __forceinline__ void join_lanes(int lanes) {
+        for (int d = 1; d < lanes; d <<= 1) join(__shfl_down(n, d, 64), __shfl_down(mean, d, 64), __shfl_down(m2, d, 64));
+    }
+};
 
 // f(activation, whether out is bf16), both as types: the branch stands outside the loop over rows.
 template <class F>
@@ -147,7 +161,8 @@ struct Stats {
     // R rows, the first `live` (1 to R) of them counted
     template <int R, bool XBF>
     __device__ __forceinline__ void add(const Vec<VEC, XBF> (&v)[R], int live) {
-        const float nc = (float)live, tot = n + nc, inv = 1.f / nc, share = nc / tot, wgt = n * share;
+        const float nc = (float)live, tot = n + nc, inv = __builtin_amdgcn_rcpf(nc);
+        const float share = nc * __builtin_amdgcn_rcpf(tot), wgt = n * share;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
             float s = 0.f, q = 0.f;
@@ -180,91 +195,112 @@ struct Stats {
     }
 };
 
-// Joins a workgroup's statistics by group.  Entries (a vector where it lies in one group, WHOLE,
-// else a channel) stand in LDS as [row lane][entry]; a group's are its columns [g wd, (g + 1) wd).
-// Waves take the groups in turn; where there are fewer groups than waves, several waves share a
-// group's row lanes.  g's mean and M2 end in stat[0][g], stat[1][g] (both for every thread).
-template <int VEC, bool WHOLE, int BD>
+// How a thread's vector lies in the groups: all of it in one, parts of it in two (a group has at
+// least as many channels), or anyhow.
+enum Span { kWhole, kTwo, kAny };
+
+// Joins a workgroup's statistics by group.  A thread first joins its channels of one group; the
+// entries (one, two or VEC a vector) stand in LDS as [row lane][vector][entry].  Waves take the
+// groups in turn; where there are fewer groups than waves, several share a group's row lanes.
+// In the end stat[0][g] is group g's mean and stat[1][g] its M2, for every thread.
+template <int VEC, Span SPAN, int BD>
 struct GroupJoin {
-    static constexpr int EPV = WHOLE ? 1 : VEC;
+    static constexpr int EPV = SPAN == kWhole ? 1 : SPAN == kTwo ? 2 : VEC;
     static constexpr int kWaves = BD / 64;
-    float mean[BD * EPV], m2[BD * EPV], cnt[BD];
-    float part[kWaves];
+    float n[BD * EPV], mean[BD * EPV], m2[BD * EPV];
+    float part[3][kWaves];
     float stat[2][kWide];
 
-    template <class F>
-    __device__ __forceinline__ void sums(const Shape& p, int wd, F f, float* to) {
-        const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, row_len = p.vpt * EPV;
-        const int per = p.gs >= kWaves ? 1 : kWaves / p.gs;       // waves of a group
+    // cg: channels of a group in this slab
+    __device__ __forceinline__ void join(const Shape& p, int cg, const Stats<VEC>& st, int ty, int tx) {
+        const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+        if (ty < p.ty) {
+            const int at = (ty * p.vpt + tx) * EPV;
+            if constexpr (SPAN == kAny) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    n[at + j] = st.n;
+                    mean[at + j] = st.mean[j];
+                    m2[at + j] = st.m2[j];
+                }
+            } else {
+                // the first k channels lie in one group, the others in the next
+                const int k = SPAN == kWhole ? VEC : min(VEC, (tx * VEC / cg + 1) * cg - tx * VEC);
+#pragma unroll
+                for (int h = 0; h < EPV; ++h) {
+                    const int cnt = h == 0 ? k : VEC - k;
+                    const float inv = cnt > 0 ? __builtin_amdgcn_rcpf((float)cnt) : 0.f;
+                    float mv = 0.f, qv = 0.f;
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) mv += SPAN == kWhole || (j < k) == (h == 0) ? st.mean[j] : 0.f;
+                    mv *= inv;
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        const float d = st.mean[j] - mv;
+                        qv += SPAN == kWhole || (j < k) == (h == 0) ? st.m2[j] + st.n * d * d : 0.f;
+                    }
+                    n[at + h] = st.n * (float)cnt;
+                    mean[at + h] = mv;
+                    m2[at + h] = qv;
+                }
+            }
+        }
+        __syncthreads();
+        int per = 1;                                              // waves of a group
+        while (per * 2 * p.gs <= kWaves) per *= 2;
         const int lanes = (p.ty + per - 1) / per;                 // row lanes of a wave
-        const int dy = 64 / wd, dc = 64 - dy * wd;
         for (int u = w; u < p.gs * per; u += kWaves) {
-            const int g = u % p.gs, y0 = u / p.gs * lanes, y1 = min(y0 + lanes, p.ty);
+            const int g = u / per, y0 = (u - g * per) * lanes, y1 = min(y0 + lanes, p.ty);
+            // the group's entries of a row lane: of vectors v0 to v0 + wd - 1 (kAny: of channels)
+            const int lo = g * cg, v0 = SPAN == kAny ? lo : lo / VEC;
+            const int wd = SPAN == kAny ? cg : (lo + cg - 1) / VEC - v0 + 1;
+            const int dy = 64 / wd, dc = 64 - dy * wd;
             int y = y0 + lane / wd, c = lane - lane / wd * wd;
-            float s = 0.f;
+            Moments m{0.f, 0.f, 0.f};
             while (y < y1) {
-                s += f(y, y * row_len + g * wd + c, g);
+                const int v = v0 + c;
+                const int at = SPAN == kAny ? y * p.vpt * VEC + v
+                                            : (y * p.vpt + v) * EPV + (SPAN == kTwo && v * VEC < lo ? 1 : 0);
+                m.join(n[at], mean[at], m2[at]);
                 y += dy;
                 c += dc;
                 if (c >= wd) { c -= wd; ++y; }
             }
-            s = wave_sum(s);
-            if (lane == 0) (per == 1 ? to[g] : part[u]) = s;
+            m.join_lanes(64);
+            if (lane == 0) {
+                if (per == 1) {
+                    stat[0][g] = m.mean;
+                    stat[1][g] = m.m2;
+                } else {
+                    part[0][u] = m.n;
+                    part[1][u] = m.mean;
+                    part[2][u] = m.m2;
+                }
+            }
         }
+        __syncthreads();
         if (per > 1) {
+            if (w < p.gs) {
+                const bool on = lane < per;
+                Moments m{on ? part[0][w * per + lane] : 0.f, on ? part[1][w * per + lane] : 0.f,
+                          on ? part[2][w * per + lane] : 0.f};
+                m.join_lanes(per);
+                if (lane == 0) {
+                    stat[0][w] = m.mean;
+                    stat[1][w] = m.m2;
+                }
+            }
             __syncthreads();
-            for (int g = threadIdx.x; g < p.gs; g += BD) {
-                float s = 0.f;
-                for (int k = 0; k < per; ++k) s += part[k * p.gs + g];
-                to[g] = s;
-            }
         }
-        __syncthreads();
-    }
-
-    // width: channels of a group in this slab; total: values of a group behind the entries
-    __device__ __forceinline__ void join(const Shape& p, int width, float total, const Stats<VEC>& st, int ty, int tx) {
-        const int row_len = p.vpt * EPV, wd = WHOLE ? width / VEC : width;
-        if (ty < p.ty) {
-            const int at = ty * row_len + tx * EPV;
-            if constexpr (WHOLE) {
-                float mv = 0.f, qv = 0.f;
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) mv += st.mean[j];
-                mv *= 1.f / VEC;
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float d = st.mean[j] - mv;
-                    qv += st.m2[j] + st.n * d * d;
-                }
-                mean[at] = mv;
-                m2[at] = qv;
-            } else {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    mean[at + j] = st.mean[j];
-                    m2[at + j] = st.m2[j];
-                }
-            }
-            if (tx == 0) cnt[ty] = WHOLE ? st.n * VEC : st.n;
-        }
-        __syncthreads();
-        const float inv = 1.f / total;
-        sums(p, wd, [&](int y, int at, int) { return cnt[y] * mean[at]; }, stat[0]);
-        for (int g = threadIdx.x; g < p.gs; g += BD) stat[0][g] *= inv;
-        __syncthreads();
-        sums(p, wd, [&](int y, int at, int g) {
-            const float d = mean[at] - stat[0][g];
-            return m2[at] + cnt[y] * d * d;
-        }, stat[1]);
     }
 };
 
-// One launch: workgroup (tile, slab, image) keeps its R rows a thread and takes the statistics
-// of all tiles in order, so that every workgroup of the slab gets the same ones.
-template <int VEC, bool XBF, bool WHOLE, int R, int BD>
+// One launch: workgroup (tile, slab, image) normalises R rows a thread, which it keeps, and takes
+// the statistics of the whole slab, kChunk rows a thread at a time, in the same order as every
+// other workgroup of the slab, so that all get the same ones.
+template <int VEC, bool XBF, Span SPAN, int R, int BD>
 __global__ __launch_bounds__(BD) void norm_one_kernel(Shape p) {
-    __shared__ GroupJoin<VEC, WHOLE, BD> lds;
+    __shared__ GroupJoin<VEC, SPAN, BD> lds;
     __shared__ Terms terms;
     const GroupNormArgs& a = p.a;
     const int tid = threadIdx.x, tile = blockIdx.y, b = blockIdx.z, rows = (int)a.rows;
@@ -273,30 +309,28 @@ __global__ __launch_bounds__(BD) void norm_one_kernel(Shape p) {
     const int ty = tid / p.vpt, tx = tid - ty * p.vpt, c = c0 + tx * VEC;
     const bool on = ty < p.ty;
     const int64_t x0 = ((int64_t)b * rows) * a.x_stride + c;
-    auto live_at = [&](int k) { return min(R, (rows - (k * p.tile_rows + ty) + p.ty - 1) / p.ty); };
-    auto load = [&](Vec<VEC, XBF> (&v)[R], int k, int live) {
+    Vec<VEC, XBF> own[R], v[kChunk];
+    auto load = [&](int r, int live) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) v[i].load(a.x, x0 + (int64_t)(r + min(i, live - 1) * p.ty) * a.x_stride);
+    };
+    auto live_at = [&](int r) { return min(kChunk, (rows - r + p.ty - 1) / p.ty); };
+    int r = ty;
+    if (on && r < rows) {
+        load(r, live_at(r));
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            v[i].load(a.x, x0 + (int64_t)(k * p.tile_rows + ty + min(i, live - 1) * p.ty) * a.x_stride);
-    };
-    Vec<VEC, XBF> own[R], v[R], next[R];
-    int live = on ? live_at(0) : 0;
-    if (live > 0) load(v, 0, live);
+            own[i].load(a.x, x0 + (int64_t)min(tile * p.tile_rows + ty + i * p.ty, rows - 1) * a.x_stride);
+    }
     terms.load(a, b, c0, width, BD);
     Stats<VEC> st;
     st.clear();
-    for (int k = 0; live > 0; ++k) {
-        const int live_next = k + 1 < p.tiles ? live_at(k + 1) : 0;
-        if (live_next > 0) load(next, k + 1, live_next);
-        st.add(v, live);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            if (k == tile) own[i] = v[i];
-            v[i] = next[i];
-        }
-        live = live_next;
+    while (on && r < rows) {
+        st.add(v, live_at(r));
+        r += p.ty * kChunk;
+        if (r < rows) load(r, live_at(r));
     }
-    lds.join(p, p.cg, (float)rows * (float)p.cg, st, ty, tx);
+    lds.join(p, p.cg, st, ty, tx);
     if (!on) return;
     const float inv = 1.f / ((float)rows * (float)p.cg);
     float mean[VEC], A[VEC], D[VEC];
@@ -323,9 +357,9 @@ __global__ __launch_bounds__(BD) void norm_one_kernel(Shape p) {
 
 // Two launches, the first: (mean, M2) of each group (or part of one) of a row tile to
 // work[b][group][part * tiles + tile].
-template <int VEC, bool XBF, bool WHOLE, int R>
+template <int VEC, bool XBF, Span SPAN, int R>
 __global__ __launch_bounds__(kSplitThreads) void norm_stats_kernel(Shape p) {
-    __shared__ GroupJoin<VEC, WHOLE, kSplitThreads> lds;
+    __shared__ GroupJoin<VEC, SPAN, kSplitThreads> lds;
     const GroupNormArgs& a = p.a;
     const int tid = threadIdx.x, tile = blockIdx.y, b = blockIdx.z;
     int c0, width, g0, part;
@@ -343,8 +377,7 @@ __global__ __launch_bounds__(kSplitThreads) void norm_stats_kernel(Shape p) {
             for (int i = 0; i < R; ++i) v[i].load(a.x, x0 + (r + (int64_t)min(i, live - 1) * p.ty) * a.x_stride);
             st.add(v, live);
         }
-    const int gw = p.parts == 1 ? p.cg : width;
-    lds.join(p, gw, (float)(end - first) * (float)gw, st, ty, tx);
+    lds.join(p, p.parts == 1 ? p.cg : width, st, ty, tx);
     for (int g = tid; g < p.gs; g += kSplitThreads)
         ((float2*)a.work)[((int64_t)b * a.groups + g0 + g) * p.parts * p.tiles + part * p.tiles + tile] =
             make_float2(lds.stat[0][g], lds.stat[1][g]);
@@ -375,29 +408,21 @@ __global__ __launch_bounds__(kSplitThreads) void norm_apply_kernel(Shape p) {
     if (on && r < end) load(live_at());         // ahead of the statistics
     terms.load(a, b, c0, width, kSplitThreads);
     const int q_all = p.parts * p.tiles;
-    const float total = (float)a.rows * (float)p.cg;
+    const float inv = 1.f / ((float)a.rows * (float)p.cg);
     const float last_rows = (float)(a.rows - (int64_t)(p.tiles - 1) * p.tile_rows);
     for (int g = w; g < p.gs; g += kSplitThreads / 64) {
         const float2* src = (const float2*)a.work + ((int64_t)b * a.groups + g0 + g) * q_all;
-        // values behind partial sum q
-        auto count = [&](int q) {
+        Moments m{0.f, 0.f, 0.f};
+        for (int q = lane; q < q_all; q += 64) {
             const int pt = p.parts == 1 ? 0 : q / p.tiles, ti = q - pt * p.tiles;
             const int wq = p.parts == 1 ? p.cg : min(p.width, p.cg - pt * p.width);
-            return (ti == p.tiles - 1 ? last_rows : (float)p.tile_rows) * (float)wq;
-        };
-        float s = 0.f;
-        for (int q = lane; q < q_all; q += 64) s += count(q) * src[q].x;
-        const float mean = wave_sum(s) / total;
-        float m2 = 0.f;
-        for (int q = lane; q < q_all; q += 64) {
-            const float2 u = src[q];
-            const float d = u.x - mean;
-            m2 += u.y + count(q) * d * d;
+            const float2 v = src[q];
+            m.join((ti == p.tiles - 1 ? last_rows : (float)p.tile_rows) * (float)wq, v.x, v.y);
         }
-        m2 = wave_sum(m2);
+        m.join_lanes(64);
         if (lane == 0) {
-            stat[0][g] = mean;
-            stat[1][g] = 1.f / sqrtf(m2 / total + a.eps);
+            stat[0][g] = m.mean;
+            stat[1][g] = 1.f / sqrtf(m.m2 * inv + a.eps);
         }
     }
     __syncthreads();
@@ -460,9 +485,6 @@ Shape plan(const GroupNormArgs& a, int v, int least) {
     return p;
 }
 
-constexpr int kOneRows = 32; // rows a thread takes the statistics of in the one launch, at most
-constexpr int kChunk = 8;    // rows of a thread's chunk in the statistics,
-constexpr int kApply = 4;    // and in the other launch
 
 // The cut of the two launches: about 1024 workgroups, each at least one chunk.
 Shape split_plan(const GroupNormArgs& a, int v) {
@@ -476,38 +498,43 @@ Shape split_plan(const GroupNormArgs& a, int v) {
     return p;
 }
 
-template <int VEC, bool XBF, bool WHOLE>
+template <int VEC, bool XBF, Span SPAN>
 void split(const GroupNormArgs& a, hipStream_t st) {
     const Shape p = split_plan(a, VEC);
     const dim3 grid((unsigned)p.slabs, (unsigned)p.tiles, (unsigned)a.B);
-    hipLaunchKernelGGL((norm_stats_kernel<VEC, XBF, WHOLE, kChunk>), grid, dim3(kSplitThreads), 0, st, p);
+    hipLaunchKernelGGL((norm_stats_kernel<VEC, XBF, SPAN, kChunk>), grid, dim3(kSplitThreads), 0, st, p);
     hipLaunchKernelGGL((norm_apply_kernel<VEC, XBF, kApply>), grid, dim3(kSplitThreads), 0, st, p);
 }
 
-template <int VEC, bool XBF, bool WHOLE, int R, int BD>
+template <int VEC, bool XBF, Span SPAN, int R, int BD>
 void one(Shape p, hipStream_t st) {
     p.ty = BD / p.vpt;
     p.tile_rows = p.ty * R;
     p.tiles = (int)((p.a.rows + p.tile_rows - 1) / p.tile_rows);
     const dim3 grid((unsigned)p.slabs, (unsigned)p.tiles, (unsigned)p.a.B);
-    hipLaunchKernelGGL((norm_one_kernel<VEC, XBF, WHOLE, R, BD>), grid, dim3(BD), 0, st, p);
+    hipLaunchKernelGGL((norm_one_kernel<VEC, XBF, SPAN, R, BD>), grid, dim3(BD), 0, st, p);
 }
 
-template <int VEC, bool XBF, bool WHOLE>
+template <int VEC, bool XBF, Span SPAN>
 void run(const GroupNormArgs& a, hipStream_t st) {
+    constexpr int BD = SPAN == kAny ? 512 : 1024;
     const Shape p = plan(a, VEC, 4 * VEC);
-    const int64_t ty = kOneThreads / p.vpt;                  // row lanes of a workgroup
-    const int64_t each = (a.rows + ty - 1) / ty;             // rows a thread of one workgroup would take
-    if (p.parts > 1 || each > kOneRows) split<VEC, XBF, WHOLE>(a, st);
-    else if (p.vpt * a.rows <= 256) one<VEC, XBF, WHOLE, 1, 256>(p, st);
-    else if (each <= 1) one<VEC, XBF, WHOLE, 1, kOneThreads>(p, st);
-    else one<VEC, XBF, WHOLE, 4, kOneThreads>(p, st);
+    const int64_t ty = BD / p.vpt;                           // row lanes of a workgroup
+    const int64_t each = (a.rows + ty - 1) / ty;             // rows a thread takes the statistics of
+    if (p.parts > 1 || each > kOneRows) split<VEC, XBF, SPAN>(a, st);
+    else if (p.vpt * a.rows <= 256) one<VEC, XBF, SPAN, 1, 256>(p, st);
+    else if (p.vpt * a.rows <= 512) one<VEC, XBF, SPAN, 1, 512>(p, st);
+    else if (each * p.slabs * a.B <= 512) one<VEC, XBF, SPAN, 1, BD>(p, st);
+    else one<VEC, XBF, SPAN, 4, BD>(p, st);
 }
 
 template <int VEC, bool XBF>
 void run_vec(const GroupNormArgs& a, hipStream_t st) {
-    if (VEC == 1 || (a.C / a.groups) % VEC == 0) run<VEC, XBF, true>(a, st);
-    else run<VEC, XBF, VEC == 1>(a, st);
+    const int cg = a.C / a.groups;
+    if constexpr (VEC == 1) run<1, XBF, kWhole>(a, st);
+    else if (cg % VEC == 0) run<VEC, XBF, kWhole>(a, st);
+    else if (cg > VEC) run<VEC, XBF, kTwo>(a, st);
+    else run<VEC, XBF, kAny>(a, st);
 }
 
 }  // namespace
