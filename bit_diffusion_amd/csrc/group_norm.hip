@@ -33,7 +33,7 @@ namespace {
 constexpr int kSplitThreads = 256;
 constexpr int kChunk = 8;         // rows of a thread's chunk in the statistics,
 constexpr int kApply = 4;         // and in the launch that only normalises
-constexpr int kOneRows = 8;       // rows a thread takes the statistics of in the one launch, at most
+constexpr int kOneVectors = 8192; // vectors of a slab in the one launch, at most
 constexpr int kMaxTiles = 256;    // row tiles of an image
 constexpr int kWide = 512;        // channels of the widest slab (64 vectors of 8)
 
@@ -103,7 +103,8 @@ struct Moments {
     // The union with another set, in this order; an empty set changes nothing.
     __device__ __forceinline__ void join(float bn, float bmean, float bm2) {
         if (bn > 0.f) {
-            const float share = bn * __builtin_amdgcn_rcpf(n + bn), d = bmean - mean;
+            // 1 and not nearly 1 for the first set: equal values keep their mean exactly
+            const float share = n > 0.f ? bn * __builtin_amdgcn_rcpf(n + bn) : 1.f, d = bmean - mean;
             mean += d * share;
             m2 += bm2 + d * d * (n * share);
             n += bn;
@@ -127,25 +128,41 @@ __device__ __forceinline__ void by_kind(int act, int bf16, F f) {
     else kind(std::false_type{});
 }
 
-// A slab's weight, bias, modulation scale and shift in LDS.  The four kinds are loaded by
-// different threads at a time: one after the other each would cost a memory latency.
+// A slab's channels in LDS: first weight, bias, modulation scale and shift, loaded by different
+// waves at a time (one after the other each would cost a memory latency); then what
+// out = act((x - mean) A + D) takes, formed once for the workgroup.
 struct Terms {
     float v[4][kWide];
     __device__ __forceinline__ void load(const GroupNormArgs& a, int image, int c0, int width, int threads) {
-        for (int i = threadIdx.x; i < 4 * width; i += threads) {
-            const int kind = i / width, ch = i - kind * width;
-            const void* p = kind == 0 ? a.weight : kind == 1 ? a.bias : kind == 2 ? a.mod_scale : a.mod_shift;
-            const int64_t at = (kind < 2 ? 0 : (int64_t)image * a.mod_stride) + c0 + ch;
+        const int w = threadIdx.x >> 6, kind = w & 3;
+        const void* p = kind == 0 ? a.weight : kind == 1 ? a.bias : kind == 2 ? a.mod_scale : a.mod_shift;
+        const int64_t at = (kind < 2 ? 0 : (int64_t)image * a.mod_stride) + c0;
+        const bool half = kind < 2 || a.mod_bf16;
+        for (int ch = (w >> 2) * 64 + (threadIdx.x & 63); ch < width; ch += threads / 4) {
             float f = kind == 0 ? 1.f : 0.f;
-            if (p != nullptr) f = kind < 2 || a.mod_bf16 ? bf16_to_f32(((const uint16_t*)p)[at]) : ((const float*)p)[at];
+            if (p != nullptr) f = half ? bf16_to_f32(((const uint16_t*)p)[at + ch]) : ((const float*)p)[at + ch];
             v[kind][ch] = f;
         }
     }
-    // out = act((x - mean) A + D) for channel ch of the slab and r = 1 / sqrt(var + eps)
-    __device__ __forceinline__ void fold(int ch, float r, float& A, float& D) const {
-        const float m = 1.f + v[2][ch];
-        A = r * v[0][ch] * m;
-        D = v[1][ch] * m + v[3][ch];
+    // v[0], v[1], v[2] become mean, A, D; cg: channels of a group in this slab
+    __device__ __forceinline__ void fold(const float* mean, const float* rstd, int width, int cg, int threads) {
+        for (int ch = threadIdx.x; ch < width; ch += threads) {
+            const int g = ch / cg;
+            const float m = 1.f + v[2][ch], A = rstd[g] * v[0][ch] * m, D = v[1][ch] * m + v[3][ch];
+            v[0][ch] = mean[g];
+            v[1][ch] = A;
+            v[2][ch] = D;
+        }
+        __syncthreads();
+    }
+    template <int VEC>
+    __device__ __forceinline__ void take(int ch, float (&mean)[VEC], float (&A)[VEC], float (&D)[VEC]) const {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            mean[j] = v[0][ch + j];
+            A[j] = v[1][ch + j];
+            D[j] = v[2][ch + j];
+        }
     }
 };
 
@@ -161,37 +178,49 @@ struct Stats {
     // R rows, the first `live` (1 to R) of them counted
     template <int R, bool XBF>
     __device__ __forceinline__ void add(const Vec<VEC, XBF> (&v)[R], int live) {
-        const float nc = (float)live, tot = n + nc, inv = __builtin_amdgcn_rcpf(nc);
-        const float share = nc * __builtin_amdgcn_rcpf(tot), wgt = n * share;
+        const float nc = (float)live, tot = n + nc;
+        const float share = n > 0.f ? nc * __builtin_amdgcn_rcpf(tot) : 1.f, wgt = n * share;
+        float s[VEC], q[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) s[j] = v[0].get(j);
+        rows(v, live, [&](const Vec<VEC, XBF>& r) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) s[j] += r.get(j);
+        });
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            float s = 0.f, q = 0.f;
-            if (live == R) {
+            s[j] = live == R ? s[j] * (1.f / R) : s[j] / nc;   // exact for equal values
+            const float d = v[0].get(j) - s[j];
+            q[j] = d * d;
+        }
+        rows(v, live, [&](const Vec<VEC, XBF>& r) {
 #pragma unroll
-                for (int i = 0; i < R; ++i) s += v[i].get(j);
-            } else {
-#pragma unroll
-                for (int i = 0; i < R; ++i) s += i < live ? v[i].get(j) : 0.f;
+            for (int j = 0; j < VEC; ++j) {
+                const float d = r.get(j) - s[j];
+                q[j] += d * d;
             }
-            const float cm = s * inv;
-            if (live == R) {
+        });
 #pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const float d = v[i].get(j) - cm;
-                    q += d * d;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const float d = i < live ? v[i].get(j) - cm : 0.f;
-                    q += d * d;
-                }
-            }
-            const float d = cm - mean[j];
+        for (int j = 0; j < VEC; ++j) {
+            const float d = s[j] - mean[j];
             mean[j] += d * share;
-            m2[j] += q + d * d * wgt;
+            m2[j] += q[j] + d * d * wgt;
         }
         n = tot;
+    }
+
+private:
+    // f for rows 1 to live - 1; a whole chunk has no branch
+    template <int R, bool XBF, class F>
+    static __device__ __forceinline__ void rows(const Vec<VEC, XBF> (&v)[R], int live, F f) {
+        if (live == R) {
+#pragma unroll
+            for (int i = 1; i < R; ++i) f(v[i]);
+        } else {
+#pragma unroll
+            for (int i = 1; i < R; ++i)
+                if (i < live) f(v[i]);
+        }
     }
 };
 
@@ -202,7 +231,8 @@ enum Span { kWhole, kTwo, kAny };
 // Joins a workgroup's statistics by group.  A thread first joins its channels of one group; the
 // entries (one, two or VEC a vector) stand in LDS as [row lane][vector][entry].  Waves take the
 // groups in turn; where there are fewer groups than waves, several share a group's row lanes.
-// In the end stat[0][g] is group g's mean and stat[1][g] its M2, for every thread.
+// In the end stat[0][g] is group g's mean and stat[1][g] what `finish` makes of its M2, for every
+// thread.
 template <int VEC, Span SPAN, int BD>
 struct GroupJoin {
     static constexpr int EPV = SPAN == kWhole ? 1 : SPAN == kTwo ? 2 : VEC;
@@ -212,7 +242,8 @@ struct GroupJoin {
     float stat[2][kWide];
 
     // cg: channels of a group in this slab
-    __device__ __forceinline__ void join(const Shape& p, int cg, const Stats<VEC>& st, int ty, int tx) {
+    template <class F>
+    __device__ __forceinline__ void join(const Shape& p, int cg, const Stats<VEC>& st, int ty, int tx, F finish) {
         const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
         if (ty < p.ty) {
             const int at = (ty * p.vpt + tx) * EPV;
@@ -226,22 +257,27 @@ struct GroupJoin {
             } else {
                 // the first k channels lie in one group, the others in the next
                 const int k = SPAN == kWhole ? VEC : min(VEC, (tx * VEC / cg + 1) * cg - tx * VEC);
+                float mv[2] = {0.f, 0.f}, qv[2] = {0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const bool in = SPAN == kWhole || j < k;
+                    mv[0] += in ? st.mean[j] : 0.f;
+                    mv[1] += in ? 0.f : st.mean[j];
+                }
+                mv[0] /= (float)k;
+                mv[1] = k < VEC ? mv[1] / (float)(VEC - k) : 0.f;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const bool in = SPAN == kWhole || j < k;
+                    const float d = st.mean[j] - (in ? mv[0] : mv[1]), t = st.m2[j] + st.n * d * d;
+                    qv[0] += in ? t : 0.f;
+                    qv[1] += in ? 0.f : t;
+                }
 #pragma unroll
                 for (int h = 0; h < EPV; ++h) {
-                    const int cnt = h == 0 ? k : VEC - k;
-                    const float inv = cnt > 0 ? __builtin_amdgcn_rcpf((float)cnt) : 0.f;
-                    float mv = 0.f, qv = 0.f;
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) mv += SPAN == kWhole || (j < k) == (h == 0) ? st.mean[j] : 0.f;
-                    mv *= inv;
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const float d = st.mean[j] - mv;
-                        qv += SPAN == kWhole || (j < k) == (h == 0) ? st.m2[j] + st.n * d * d : 0.f;
-                    }
-                    n[at + h] = st.n * (float)cnt;
-                    mean[at + h] = mv;
-                    m2[at + h] = qv;
+                    n[at + h] = st.n * (float)(h == 0 ? k : VEC - k);
+                    mean[at + h] = mv[h];
+                    m2[at + h] = qv[h];
                 }
             }
         }
@@ -270,7 +306,7 @@ struct GroupJoin {
             if (lane == 0) {
                 if (per == 1) {
                     stat[0][g] = m.mean;
-                    stat[1][g] = m.m2;
+                    stat[1][g] = finish(m.m2);
                 } else {
                     part[0][u] = m.n;
                     part[1][u] = m.mean;
@@ -287,7 +323,7 @@ struct GroupJoin {
                 m.join_lanes(per);
                 if (lane == 0) {
                     stat[0][w] = m.mean;
-                    stat[1][w] = m.m2;
+                    stat[1][w] = finish(m.m2);
                 }
             }
             __syncthreads();
@@ -330,16 +366,12 @@ __global__ __launch_bounds__(BD) void norm_one_kernel(Shape p) {
         r += p.ty * kChunk;
         if (r < rows) load(r, live_at(r));
     }
-    lds.join(p, p.cg, st, ty, tx);
-    if (!on) return;
     const float inv = 1.f / ((float)rows * (float)p.cg);
+    lds.join(p, p.cg, st, ty, tx, [&](float m2) { return 1.f / sqrtf(m2 * inv + a.eps); });
+    terms.fold(lds.stat[0], lds.stat[1], width, p.cg, BD);
+    if (!on) return;
     float mean[VEC], A[VEC], D[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        const int g = (tx * VEC + j) / p.cg;
-        mean[j] = lds.stat[0][g];
-        terms.fold(tx * VEC + j, 1.f / sqrtf(lds.stat[1][g] * inv + a.eps), A[j], D[j]);
-    }
+    terms.take(tx * VEC, mean, A, D);
     const int64_t o0 = ((int64_t)b * rows) * a.out_stride + c;
     by_kind(a.act, a.out_bf16, [&](auto act, auto obf) {
 #pragma unroll
@@ -377,7 +409,7 @@ __global__ __launch_bounds__(kSplitThreads) void norm_stats_kernel(Shape p) {
             for (int i = 0; i < R; ++i) v[i].load(a.x, x0 + (r + (int64_t)min(i, live - 1) * p.ty) * a.x_stride);
             st.add(v, live);
         }
-    lds.join(p, p.parts == 1 ? p.cg : width, st, ty, tx);
+    lds.join(p, p.parts == 1 ? p.cg : width, st, ty, tx, [](float m2) { return m2; });
     for (int g = tid; g < p.gs; g += kSplitThreads)
         ((float2*)a.work)[((int64_t)b * a.groups + g0 + g) * p.parts * p.tiles + part * p.tiles + tile] =
             make_float2(lds.stat[0][g], lds.stat[1][g]);
@@ -426,14 +458,10 @@ __global__ __launch_bounds__(kSplitThreads) void norm_apply_kernel(Shape p) {
         }
     }
     __syncthreads();
+    terms.fold(stat[0], stat[1], width, p.parts == 1 ? p.cg : width, kSplitThreads);
     if (!on) return;
     float mean[VEC], A[VEC], D[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        const int g = p.parts == 1 ? (tx * VEC + j) / p.cg : 0;
-        mean[j] = stat[0][g];
-        terms.fold(tx * VEC + j, stat[1][g], A[j], D[j]);
-    }
+    terms.take(tx * VEC, mean, A, D);
     const int64_t o0 = ((int64_t)b * a.rows) * a.out_stride + c;
     by_kind(a.act, a.out_bf16, [&](auto act, auto obf) {
         while (r < end) {
@@ -517,15 +545,11 @@ void one(Shape p, hipStream_t st) {
 
 template <int VEC, bool XBF, Span SPAN>
 void run(const GroupNormArgs& a, hipStream_t st) {
-    constexpr int BD = SPAN == kAny ? 512 : 1024;
     const Shape p = plan(a, VEC, 4 * VEC);
-    const int64_t ty = BD / p.vpt;                           // row lanes of a workgroup
-    const int64_t each = (a.rows + ty - 1) / ty;             // rows a thread takes the statistics of
-    if (p.parts > 1 || each > kOneRows) split<VEC, XBF, SPAN>(a, st);
-    else if (p.vpt * a.rows <= 256) one<VEC, XBF, SPAN, 1, 256>(p, st);
-    else if (p.vpt * a.rows <= 512) one<VEC, XBF, SPAN, 1, 512>(p, st);
-    else if (each * p.slabs * a.B <= 512) one<VEC, XBF, SPAN, 1, BD>(p, st);
-    else one<VEC, XBF, SPAN, 4, BD>(p, st);
+    const int64_t vectors = p.vpt * a.rows;                  // of a slab
+    if (p.parts > 1 || vectors > kOneVectors) split<VEC, XBF, SPAN>(a, st);
+    else if (vectors <= 256 || vectors * p.slabs * a.B <= 256 * 256) one<VEC, XBF, SPAN, 1, 256>(p, st);
+    else one<VEC, XBF, SPAN, 4, 256>(p, st);
 }
 
 template <int VEC, bool XBF>
