@@ -400,13 +400,13 @@ struct UpTile {
     static constexpr int kChunks = NB == 0 ? 2 : NB * 4;      // 16-byte chunks of a row of B
     static constexpr int kUp = CB * 16 * kChunks / 64;        // a lane's chunks
     static constexpr int kLds = (CB * 16 * kChunks > RBE * 64 * CB ? CB * 16 * kChunks : RBE * 64 * CB);   // uint4 a wave
-    uint4 base[kPieces];
+    using Base = uint4[kPieces];
     uint4 up[kUp];
 
     static __device__ __forceinline__ int piece_row(int p) { return (p * 64 + (threadIdx.x & 63)) / kLanes; }
     static __device__ __forceinline__ int piece_col() { return (threadIdx.x & 63) % kLanes * kPer; }
 
-    __device__ __forceinline__ void load_base(const LoraBatchArgs& a, const Tile& t, int c0) {
+    static __device__ __forceinline__ void load_base(const LoraBatchArgs& a, const Tile& t, int c0, Base& base) {
         const int c = c0 + piece_col();
         const bool on = a.vec && a.base != nullptr && c + kPer <= a.N;
 #pragma unroll
@@ -431,11 +431,11 @@ struct UpTile {
         }
     }
 
-    // acc = t B^T, lane (q, r16) with columns 16 c + 4 q to 16 c + 4 q + 3 of row 16 i + r16
-    // (B is the MFMA's row operand)
-    __device__ __forceinline__ void products(uint4* lds, const uint4 (&tm)[RBE][kOps][kBlocks], f32x4 (&acc)[RBE][CB]) {
-        constexpr int kSpread = 16 / kChunks;   // rows of B to 256 bytes of LDS
-        const int lane = threadIdx.x & 63, q = lane >> 4, r16 = lane & 15;
+    static constexpr int kSpread = 16 / kChunks;   // rows of B to 256 bytes of LDS
+
+    // B to LDS; its registers are free then
+    __device__ __forceinline__ void stage_up(uint4* lds) {
+        const int lane = threadIdx.x & 63;
         wave_sync();
 #pragma unroll
         for (int i = 0; i < kUp; ++i) {
@@ -443,6 +443,13 @@ struct UpTile {
             lds[n * kChunks + (j ^ (n / kSpread % kChunks))] = up[i];
         }
         wave_sync();
+    }
+
+    // acc = t B^T, lane (q, r16) with columns 16 c + 4 q to 16 c + 4 q + 3 of row 16 i + r16
+    // (B is the MFMA's row operand)
+    static __device__ __forceinline__ void products(const uint4* lds, const uint4 (&tm)[RBE][kOps][kBlocks],
+                                                    f32x4 (&acc)[RBE][CB]) {
+        const int lane = threadIdx.x & 63, q = lane >> 4, r16 = lane & 15;
 #pragma unroll
         for (int i = 0; i < RBE; ++i)
 #pragma unroll
@@ -468,7 +475,7 @@ struct UpTile {
     }
 
     // acc from lanes that hold 4 columns to pieces of kPer columns
-    __device__ __forceinline__ void turn(uint4* lds, const f32x4 (&acc)[RBE][CB], float (&y)[kPieces][kPer]) {
+    static __device__ __forceinline__ void turn(uint4* lds, const f32x4 (&acc)[RBE][CB], float (&y)[kPieces][kPer]) {
         const int lane = threadIdx.x & 63, q = lane >> 4, r16 = lane & 15;
         static_assert(CB == 4 || CB == 2, "slots of a row");
         f32x4* buf = (f32x4*)lds;
@@ -489,7 +496,8 @@ struct UpTile {
     }
 
     template <int ACT>
-    __device__ __forceinline__ void store_as(const LoraBatchArgs& a, const Tile& t, int c0, const float (&y)[kPieces][kPer]) {
+    static __device__ __forceinline__ void store_as(const LoraBatchArgs& a, const Tile& t, int c0, const Base& base,
+                                                    const float (&y)[kPieces][kPer]) {
         const int c = c0 + piece_col();
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
@@ -525,33 +533,38 @@ struct UpTile {
         }
     }
 
-    __device__ __forceinline__ void store(const LoraBatchArgs& a, const Tile& t, int c0, const float (&y)[kPieces][kPer]) {
-        if (a.act == 1) store_as<1>(a, t, c0, y);
-        else if (a.act == 2) store_as<2>(a, t, c0, y);
-        else store_as<0>(a, t, c0, y);
+    static __device__ __forceinline__ void store(const LoraBatchArgs& a, const Tile& t, int c0, const Base& base,
+                                                 const float (&y)[kPieces][kPer]) {
+        if (a.act == 1) store_as<1>(a, t, c0, base, y);
+        else if (a.act == 2) store_as<2>(a, t, c0, base, y);
+        else store_as<0>(a, t, c0, base, y);
     }
 
     // rows without adapter: out = act(base)
-    __device__ __forceinline__ void store_base(const LoraBatchArgs& a, const Tile& t, int c0) {
+    static __device__ __forceinline__ void store_base(const LoraBatchArgs& a, const Tile& t, int c0, const Base& base) {
         float y[kPieces][kPer];
 #pragma unroll
         for (int p = 0; p < kPieces; ++p)
 #pragma unroll
             for (int e = 0; e < kPer; ++e) y[p][e] = 0.f;
-        store(a, t, c0, y);
+        store(a, t, c0, base, y);
     }
 };
 
 // A workgroup's rows x `blocks` blocks of 64 CB columns, 16 CB columns to each of 4 waves: t
-// stays in registers, and a block's base and B are loaded while the one before is worked on.
-template <int RBE, int CB, int NB, bool BF16>
+// stays in registers; base is loaded D blocks ahead, B as soon as the block before has its own
+// in LDS.
+template <int RBE, int CB, int NB, bool BF16, int D>
 __device__ __forceinline__ void up_blocks(const LoraBatchArgs& a, const Tile& t, const Adapter& ad, int first,
                                           int blocks, uint4* lds) {
     using Up = UpTile<RBE, CB, NB, BF16>;
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
     auto col = [&](int b) { return ((first + b) * 4 + w) * 16 * CB; };
-    Up u, next;
-    u.load_base(a, t, col(0));
+    Up u;
+    typename Up::Base base[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (d < blocks) Up::load_base(a, t, col(d), base[d]);
     u.load_up(a, ad, col(0));
     uint4 tm[RBE][Up::kOps][Up::kBlocks];
     const int wb = blocks_of(a.nb), ops = a.nb == 0 ? 2 : 3;
@@ -564,22 +577,24 @@ __device__ __forceinline__ void up_blocks(const LoraBatchArgs& a, const Tile& t,
 #pragma unroll
             for (int b = 0; b < Up::kBlocks; ++b) tm[i][o][b] = src[(o * wb + b) * 64];
     }
-    for (int b = 0; b < blocks; ++b) {
-        if (b + 1 < blocks) {
-            next.load_base(a, t, col(b + 1));
-            next.load_up(a, ad, col(b + 1));
+    for (int b = 0; b < blocks; b += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (b + d >= blocks) break;
+            u.stage_up(lds);
+            u.load_up(a, ad, col(min(b + d + 1, blocks - 1)));
+            f32x4 acc[RBE][CB];
+            float y[Up::kPieces][Up::kPer];
+            Up::products(lds, tm, acc);
+            Up::turn(lds, acc, y);
+            Up::store(a, t, col(b + d), base[d], y);
+            if (b + d + D < blocks) Up::load_base(a, t, col(b + d + D), base[d]);
         }
-        f32x4 acc[RBE][CB];
-        float y[Up::kPieces][Up::kPer];
-        u.products(lds, tm, acc);
-        u.turn(lds, acc, y);
-        u.store(a, t, col(b), y);
-        u = next;
     }
 }
 
 // Up-projection of a tile of 16 RBE rows, `span` blocks of columns.
-template <int RBE, int CB, int NB, bool BF16>
+template <int RBE, int CB, int NB, bool BF16, int D>
 __global__ __launch_bounds__(256) void lora_up_kernel(LoraBatchArgs a, int per, int inner, int span) {
     using Up = UpTile<RBE, CB, NB, BF16>;
     __shared__ uint4 lds[4][Up::kLds];
@@ -593,20 +608,20 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraBatchArgs a, int per, 
     if (ad.rank == 0) {
         if (unchanged(a)) return;
         for (int b = 0; b < blocks; ++b) {
-            UpTile<RBE, CB, 0, BF16> u;
             const int c0 = ((first + b) * 4 + w) * 16 * CB;
-            u.load_base(a, t, c0);
-            u.store_base(a, t, c0);
+            typename Up::Base base;
+            Up::load_base(a, t, c0, base);
+            Up::store_base(a, t, c0, base);
         }
         return;
     }
     if constexpr (NB > 2) {
         if (ad.rank <= 64) {
-            up_blocks<RBE, CB, 2, BF16>(a, t, ad, first, blocks, lds[w]);
+            up_blocks<RBE, CB, 2, BF16, D>(a, t, ad, first, blocks, lds[w]);
             return;
         }
     }
-    up_blocks<RBE, CB, NB, BF16>(a, t, ad, first, blocks, lds[w]);
+    up_blocks<RBE, CB, NB, BF16, D>(a, t, ad, first, blocks, lds[w]);
 }
 
 // Both products for a tile of 16 rows x 256 columns, 32 columns to each of 8 waves: the waves
@@ -627,10 +642,11 @@ __global__ __launch_bounds__(512) void lora_few_rows_kernel(LoraBatchArgs a, int
     if (t.rows == 0) return;
     const int c0 = part * kColTile + w * 32;
     Up u;
-    u.load_base(a, t, c0);
+    typename Up::Base base;
+    Up::load_base(a, t, c0, base);
     const Adapter ad = adapter_of(a, t.id);
     if (ad.rank == 0) {
-        if (!unchanged(a)) u.store_base(a, t, c0);
+        if (!unchanged(a)) Up::store_base(a, t, c0, base);
         return;
     }
     u.load_up(a, ad, c0);
@@ -655,9 +671,10 @@ __global__ __launch_bounds__(512) void lora_few_rows_kernel(LoraBatchArgs a, int
         for (int b = 0; b < Up::kBlocks; ++b) tm[0][o][b] = terms[o][b][lane];
     f32x4 out[1][2];
     float y[Up::kPieces][Up::kPer];
-    u.products(lds[w], tm, out);
-    u.turn(lds[w], out, y);
-    u.store(a, t, c0, y);
+    u.stage_up(lds[w]);
+    Up::products(lds[w], tm, out);
+    Up::turn(lds[w], out, y);
+    Up::store(a, t, c0, base, y);
 }
 
 // Most tiles of `tm` rows that n segments of M rows can need.
@@ -712,13 +729,15 @@ void launch_down(const LoraBatchArgs& a, hipStream_t st) {
 
 template <int RBE, int NB, bool BF16>
 void up(const LoraBatchArgs& a, hipStream_t st) {
-    constexpr int CB = NB == 4 ? 2 : 4;
+    // columns of a wave: 64 cover whole cache lines of out, 32 leave registers for more waves
+    // (rank 16, 4096 x 3072: 13.5 us with 64, 11.5 with 32; rank 32, 4608 x 12288: 59 and 62)
+    constexpr int CB = NB == 0 || NB == 4 ? 2 : 4;
     const int64_t tiles = most_tiles(a.M, a.n_segments, RBE * 16);
     const int blocks = (a.N + 64 * CB - 1) / (64 * CB);
     int span = 1;
     while (span < 8 && span < blocks && tiles * ((blocks + 2 * span - 1) / (2 * span)) >= 1024) span *= 2;
     const int inner = (blocks + span - 1) / span;
-    hipLaunchKernelGGL((lora_up_kernel<RBE, CB, NB, BF16>), dim3(grid_of(tiles, inner)), dim3(256), 0, st, a,
+    hipLaunchKernelGGL((lora_up_kernel<RBE, CB, NB, BF16, 2>), dim3(grid_of(tiles, inner)), dim3(256), 0, st, a,
                        per_xcd(tiles), inner, span);
 }
 
@@ -744,6 +763,7 @@ void few_rows(const LoraBatchArgs& a, hipStream_t st) {
 }  // namespace
 
 int64_t lora_batch_workspace_bytes(int64_t M, int R, int n_segments) {
+    if (n_segments == 0) return 0;
     // the operands of t for an fp32 output, every block of 16 rows
     const int nb = rank_blocks(R);
     return most_tiles(M, n_segments, 16) * ops_of(nb, false) * blocks_of(nb) * 1024;
@@ -754,7 +774,7 @@ void launch_lora_batch(const LoraBatchArgs& args, hipStream_t st) {
     a.nb = rank_blocks(a.R);
     a.max_blocks = (int)most_tiles(a.M, a.n_segments, 16);
     const int64_t inner = (a.N + kColTile - 1) / kColTile;
-    if (a.R <= 64 && a.max_blocks * inner <= 512 && (int64_t)a.R * a.K <= 1 << 18) {
+    if (a.R <= 64 && a.max_blocks * inner <= 256 && (int64_t)a.R * a.K <= 1 << 18) {
         a.bf16 ? few_rows<true>(a, st) : few_rows<false>(a, st);
         return;
     }
