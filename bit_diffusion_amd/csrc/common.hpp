@@ -41,6 +41,20 @@ __device__ __forceinline__ float wave_max_xor(float v, int mask) {
     return fmaxf(v, __shfl_xor(v, mask, kWave));
 }
 
+// Lane moves by DPP (a few cycles where a shuffle through LDS takes a hundred): lane i gets
+// `src` of lane i - N of its row of 16 (kShr + N), of the row before's last lane (kBcast15, rows 1
+// and 3) or of lane 31 (kBcast31, rows 2 and 3), and `old` where there is no such lane.  Joining
+// with kShr + 1, 2, 4, 8, then kBcast15 (rows 0xa), then kBcast31 (rows 0xc) is an inclusive scan.
+constexpr int kShr = 0x110, kBcast15 = 0x142, kBcast31 = 0x143;
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ int dpp(int old, int src) {
+    return __builtin_amdgcn_update_dpp(old, src, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ float dpp(float old, float src) {
+    return __int_as_float(dpp<CTRL, ROWS>(__float_as_int(old), __float_as_int(src)));
+}
+
 // GELU, tanh form: 0.5 y (1 + tanh(u)), u = sqrt(2/pi) (y + 0.044715 y^3).  Evaluated as
 // the identical y / (1 + exp(-2u)), which keeps full relative accuracy for negative y where
 // 1 + tanh(u) would cancel, with the hardware's exp2 and reciprocal (about 1 ulp each):

@@ -46,6 +46,7 @@ struct Shape {
     int parts;     // slabs of one group (1: a slab is whole groups)
     int slabs;     // slabs of an image
     int vpt;       // vectors of a slab
+    float inv_vpt;
     int ty;        // row lanes of a workgroup
     int tiles;     // row tiles of an image
     int tile_rows;
@@ -108,19 +109,31 @@ struct Moments {
     float n, mean, m2;
     // The union with another set, in this order; an empty set changes nothing.
     __device__ __forceinline__ void join(float bn, float bmean, float bm2) {
-        if (bn > 0.f) {
-            // 1 and not nearly 1 for the first set: equal values keep their mean exactly
-            const float share = n > 0.f ? bn * __builtin_amdgcn_rcpf(n + bn) : 1.f, d = bmean - mean;
-            mean += d * share;
-            m2 += bm2 + d * d * (n * share);
-            n += bn;
-        }
+        const float tot = n + bn, inv = __builtin_amdgcn_rcpf(tot);
+        // 1 and not nearly 1 for the first set: equal values keep their mean exactly
+        const float share = bn > 0.f ? (n > 0.f ? bn * inv : 1.f) : 0.f, d = bmean - mean;
+        mean += d * share;
+        m2 += bm2 + d * d * (n * share);
+        n = tot;
     }
-    // The union over each `lanes` (a power of two) lanes, in the first of them.
+    template <int CTRL, int ROWS = 0xf>
+    __device__ __forceinline__ void join_dpp() {
+        join(dpp<CTRL, ROWS>(0.f, n), dpp<CTRL, ROWS>(0.f, mean), dpp<CTRL, ROWS>(0.f, m2));
+    }
+    // The union over each `lanes` (a power of two) lanes, in the last of them.
     __device__ __forceinline__ void join_lanes(int lanes) {
-        for (int d = 1; d < lanes; d <<= 1) join(__shfl_down(n, d, 64), __shfl_down(mean, d, 64), __shfl_down(m2, d, 64));
+        if (lanes > 1) join_dpp<kShr + 1>();
+        if (lanes > 2) join_dpp<kShr + 2>();
+        if (lanes > 4) join_dpp<kShr + 4>();
+        if (lanes > 8) join_dpp<kShr + 8>();
+        if (lanes > 16) join_dpp<kBcast15, 0xa>();
+        if (lanes > 32) join_dpp<kBcast31, 0xc>();
     }
 };
+
+// n / d for 0 <= n < 2^15, 0 < d < 2^15 and inv = 1 / d to an ulp: n + 1/2 keeps the quotient half a
+// 2^15th away from the whole numbers.
+__device__ __forceinline__ int quotient(int n, float inv) { return (int)(((float)n + 0.5f) * inv); }
 
 // f(activation, whether out is bf16), both as types: the branch stands outside the loop over rows.
 template <class F>
@@ -139,21 +152,38 @@ __device__ __forceinline__ void by_kind(int act, int bf16, F f) {
 // out = act((x - mean) A + D) takes, formed once for the workgroup.
 struct Terms {
     float v[4][kWide];
-    __device__ __forceinline__ void load(const GroupNormArgs& a, int image, int c0, int width, int threads) {
-        const int w = threadIdx.x >> 6, kind = w & 3;
-        const void* p = kind == 0 ? a.weight : kind == 1 ? a.bias : kind == 2 ? a.mod_scale : a.mod_shift;
-        const int64_t at = (kind < 2 ? 0 : (int64_t)image * a.mod_stride) + c0;
-        const bool half = kind < 2 || a.mod_bf16;
-        for (int ch = (w >> 2) * 64 + (threadIdx.x & 63); ch < width; ch += threads / 4) {
-            float f = kind == 0 ? 1.f : 0.f;
-            if (p != nullptr) f = half ? bf16_to_f32(((const uint16_t*)p)[at + ch]) : ((const float*)p)[at + ch];
-            v[kind][ch] = f;
+    struct Source {
+        const void* p;
+        int64_t at;
+        int kind;
+        bool half;
+        uint32_t first;   // the thread's first value as loaded
+        __device__ __forceinline__ uint32_t get(int ch) const {
+            return half ? ((const uint16_t*)p)[at + ch] : ((const uint32_t*)p)[at + ch];
         }
+        __device__ __forceinline__ float value(uint32_t u) const {
+            return p == nullptr ? (kind == 0 ? 1.f : 0.f) : __uint_as_float(half ? u << 16 : u);
+        }
+    };
+    static __device__ __forceinline__ int channel() { return (threadIdx.x >> 8) * 64 + (threadIdx.x & 63); }
+    // starts the loads; what comes between this and put() need not wait for them
+    static __device__ __forceinline__ Source load(const GroupNormArgs& a, int image, int c0, int width) {
+        const int kind = (threadIdx.x >> 6) & 3;
+        Source s{kind == 0 ? a.weight : kind == 1 ? a.bias : kind == 2 ? a.mod_scale : a.mod_shift,
+                 (kind < 2 ? 0 : (int64_t)image * a.mod_stride) + c0, kind, kind < 2 || a.mod_bf16 != 0, 0};
+        if (s.p != nullptr && channel() < width) s.first = s.get(channel());
+        return s;
+    }
+    __device__ __forceinline__ void put(const Source& s, int width, int threads) {
+        if (channel() < width) v[s.kind][channel()] = s.value(s.first);
+        for (int ch = channel() + threads / 4; ch < width; ch += threads / 4)
+            v[s.kind][ch] = s.value(s.p == nullptr ? 0u : s.get(ch));
     }
     // v[0], v[1], v[2] become mean, A, D; cg: channels of a group in this slab
     __device__ __forceinline__ void fold(const float* mean, const float* rstd, int width, int cg, int threads) {
+        const float inv = __builtin_amdgcn_rcpf((float)cg);
         for (int ch = threadIdx.x; ch < width; ch += threads) {
-            const int g = ch / cg;
+            const int g = quotient(ch, inv);
             const float m = 1.f + v[2][ch], A = rstd[g] * v[0][ch] * m, D = v[1][ch] * m + v[3][ch];
             v[0][ch] = mean[g];
             v[1][ch] = A;
@@ -181,31 +211,35 @@ struct Stats {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) mean[j] = m2[j] = 0.f;
     }
-    // R rows, the first `live` (1 to R) of them counted
-    template <int R, bool XBF>
+    // R rows, the first `live` (1 to R) of them counted; WHOLE: all of them
+    template <bool WHOLE, int R, bool XBF>
     __device__ __forceinline__ void add(const Vec<VEC, XBF> (&v)[R], int live) {
-        const float nc = (float)live, tot = n + nc;
+        const float nc = WHOLE ? (float)R : (float)live, tot = n + nc;
         const float share = n > 0.f ? nc * __builtin_amdgcn_rcpf(tot) : 1.f, wgt = n * share;
         float s[VEC], q[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) s[j] = v[0].get(j);
-        rows(v, live, [&](const Vec<VEC, XBF>& r) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) s[j] += r.get(j);
-        });
+        for (int i = 1; i < R; ++i)
+            if (WHOLE || i < live) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) s[j] += v[i].get(j);
+            }
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            s[j] = live == R ? s[j] * (1.f / R) : s[j] / nc;   // exact for equal values
+            s[j] = WHOLE ? s[j] * (1.f / R) : s[j] / nc;   // exact for equal values
             const float d = v[0].get(j) - s[j];
             q[j] = d * d;
         }
-        rows(v, live, [&](const Vec<VEC, XBF>& r) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float d = r.get(j) - s[j];
-                q[j] += d * d;
+        for (int i = 1; i < R; ++i)
+            if (WHOLE || i < live) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float d = v[i].get(j) - s[j];
+                    q[j] += d * d;
+                }
             }
-        });
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
             const float d = s[j] - mean[j];
@@ -214,18 +248,20 @@ struct Stats {
         }
         n = tot;
     }
-
-private:
-    // f for rows 1 to live - 1; a whole chunk has no branch
-    template <int R, bool XBF, class F>
-    static __device__ __forceinline__ void rows(const Vec<VEC, XBF> (&v)[R], int live, F f) {
-        if (live == R) {
+    // `count` rows from x, `step` values apart
+    template <int R, bool XBF>
+    __device__ __forceinline__ void take(const void* x, int64_t at, int64_t step, int64_t count) {
+        Vec<VEC, XBF> v[R];
+        for (; count >= R; count -= R, at += R * step) {
 #pragma unroll
-            for (int i = 1; i < R; ++i) f(v[i]);
-        } else {
+            for (int i = 0; i < R; ++i) v[i].load(x, at + i * step);
+            add<true>(v, R);
+        }
+        if (count > 0) {
 #pragma unroll
-            for (int i = 1; i < R; ++i)
-                if (i < live) f(v[i]);
+            for (int i = 0; i < R; ++i)
+                if (i < count) v[i].load(x, at + i * step);
+            add<false>(v, (int)count);
         }
     }
 };
@@ -262,7 +298,7 @@ struct GroupJoin {
                 }
             } else {
                 // the first k channels lie in one group, the others in the next
-                const int k = SPAN == kWhole ? VEC : min(VEC, (tx * VEC / cg + 1) * cg - tx * VEC);
+                const int k = SPAN == kWhole ? VEC : min(VEC, (quotient(tx * VEC, __builtin_amdgcn_rcpf((float)cg)) + 1) * cg - tx * VEC);
                 float mv[2] = {0.f, 0.f}, qv[2] = {0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
@@ -288,16 +324,18 @@ struct GroupJoin {
             }
         }
         __syncthreads();
-        int per = 1;                                              // waves of a group
-        while (per * 2 * p.gs <= kWaves) per *= 2;
-        const int lanes = (p.ty + per - 1) / per;                 // row lanes of a wave
+        int log_per = 0;
+        while ((2 << log_per) * p.gs <= kWaves) ++log_per;
+        const int per = 1 << log_per;                             // waves of a group
+        const int lanes = (p.ty + per - 1) >> log_per;            // row lanes of a wave
         for (int u = w; u < p.gs * per; u += kWaves) {
-            const int g = u / per, y0 = (u - g * per) * lanes, y1 = min(y0 + lanes, p.ty);
+            const int g = u >> log_per, y0 = (u - (g << log_per)) * lanes, y1 = min(y0 + lanes, p.ty);
             // the group's entries of a row lane: of vectors v0 to v0 + wd - 1 (kAny: of channels)
             const int lo = g * cg, v0 = SPAN == kAny ? lo : lo / VEC;
             const int wd = SPAN == kAny ? cg : (lo + cg - 1) / VEC - v0 + 1;
-            const int dy = 64 / wd, dc = 64 - dy * wd;
-            int y = y0 + lane / wd, c = lane - lane / wd * wd;
+            const float inv = __builtin_amdgcn_rcpf((float)wd);
+            const int dy = quotient(64, inv), dc = 64 - dy * wd, ly = quotient(lane, inv);
+            int y = y0 + ly, c = lane - ly * wd;
             Moments m{0.f, 0.f, 0.f};
             while (y < y1) {
                 const int v = v0 + c;
@@ -309,7 +347,7 @@ struct GroupJoin {
                 if (c >= wd) { c -= wd; ++y; }
             }
             m.join_lanes(64);
-            if (lane == 0) {
+            if (lane == 63) {
                 if (per == 1) {
                     stat[0][g] = m.mean;
                     stat[1][g] = finish(m.m2);
@@ -327,7 +365,7 @@ struct GroupJoin {
                 Moments m{on ? part[0][w * per + lane] : 0.f, on ? part[1][w * per + lane] : 0.f,
                           on ? part[2][w * per + lane] : 0.f};
                 m.join_lanes(per);
-                if (lane == 0) {
+                if (lane == per - 1) {
                     stat[0][w] = m.mean;
                     stat[1][w] = finish(m.m2);
                 }
@@ -348,30 +386,22 @@ __global__ __launch_bounds__(BD) void norm_one_kernel(Shape p) {
     const int tid = threadIdx.x, tile = blockIdx.y, b = blockIdx.z, rows = (int)a.rows;
     int c0, width, g0, part;
     slab_range(p, blockIdx.x, c0, width, g0, part);
-    const int ty = tid / p.vpt, tx = tid - ty * p.vpt, c = c0 + tx * VEC;
+    const int ty = quotient(tid, p.inv_vpt), tx = tid - ty * p.vpt, c = c0 + tx * VEC;
     const bool on = ty < p.ty;
     const int64_t x0 = ((int64_t)b * rows) * a.x_stride + c;
-    Vec<VEC, XBF> own[R], v[kChunk];
-    auto load = [&](int r, int live) {
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) v[i].load(a.x, x0 + (int64_t)(r + min(i, live - 1) * p.ty) * a.x_stride);
-    };
-    auto live_at = [&](int r) { return min(kChunk, (rows - r + p.ty - 1) / p.ty); };
-    int r = ty;
-    if (on && r < rows) {
-        load(r, live_at(r));
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            own[i].load(a.x, x0 + (int64_t)min(tile * p.tile_rows + ty + i * p.ty, rows - 1) * a.x_stride);
-    }
-    terms.load(a, b, c0, width, BD);
+    const Terms::Source src = Terms::load(a, b, c0, width);
+    const int64_t step = (int64_t)p.ty * a.x_stride;
+    Vec<VEC, XBF> own[R];
     Stats<VEC> st;
     st.clear();
-    while (on && r < rows) {
-        st.add(v, live_at(r));
-        r += p.ty * kChunk;
-        if (r < rows) load(r, live_at(r));
+    if (on && ty < rows) {
+        const int64_t own0 = x0 + (int64_t)(tile * p.tile_rows + ty) * a.x_stride;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (tile * p.tile_rows + ty + i * p.ty < rows) own[i].load(a.x, own0 + i * step);
+        st.template take<kChunk, XBF>(a.x, x0 + (int64_t)ty * a.x_stride, step, (rows - ty + p.ty - 1) / p.ty);
     }
+    terms.put(src, width, BD);
     const float inv = 1.f / ((float)rows * (float)p.cg);
     lds.join(p, p.cg, st, ty, tx, [&](float m2) { return 1.f / sqrtf(m2 * inv + a.eps); });
     terms.fold(lds.stat[0], lds.stat[1], width, p.cg, BD);
@@ -402,19 +432,14 @@ __global__ __launch_bounds__(kSplitThreads) void norm_stats_kernel(Shape p) {
     const int tid = threadIdx.x, tile = blockIdx.y, b = blockIdx.z;
     int c0, width, g0, part;
     slab_range(p, blockIdx.x, c0, width, g0, part);
-    const int ty = tid / p.vpt, tx = tid - ty * p.vpt;
+    const int ty = quotient(tid, p.inv_vpt), tx = tid - ty * p.vpt;
     const int64_t first = (int64_t)tile * p.tile_rows, end = min(first + p.tile_rows, a.rows);
     const int64_t x0 = ((int64_t)b * a.rows) * a.x_stride + c0 + tx * VEC;
+    const int64_t step = (int64_t)p.ty * a.x_stride;
     Stats<VEC> st;
     st.clear();
-    if (ty < p.ty && tx * VEC < width)
-        for (int64_t r = first + ty; r < end; r += (int64_t)p.ty * R) {
-            Vec<VEC, XBF> v[R];
-            const int live = (int)min((int64_t)R, (end - r + p.ty - 1) / p.ty);
-#pragma unroll
-            for (int i = 0; i < R; ++i) v[i].load(a.x, x0 + (r + (int64_t)min(i, live - 1) * p.ty) * a.x_stride);
-            st.add(v, live);
-        }
+    if (ty < p.ty && tx * VEC < width && first + ty < end)
+        st.template take<R, XBF>(a.x, x0 + (first + ty) * a.x_stride, step, (end - first - ty + p.ty - 1) / p.ty);
     lds.join(p, p.parts == 1 ? p.cg : width, st, ty, tx, [](float m2) { return m2; });
     for (int g = tid; g < p.gs; g += kSplitThreads)
         ((float2*)a.work)[((int64_t)b * a.groups + g0 + g) * p.parts * p.tiles + part * p.tiles + tile] =
@@ -432,19 +457,20 @@ __global__ __launch_bounds__(kSplitThreads) void norm_apply_kernel(Shape p) {
     const int tile = p.tiles - 1 - blockIdx.y, b = blockIdx.z;
     int c0, width, g0, part;
     slab_range(p, blockIdx.x, c0, width, g0, part);
-    const int ty = tid / p.vpt, tx = tid - ty * p.vpt, c = c0 + tx * VEC;
+    const int ty = quotient(tid, p.inv_vpt), tx = tid - ty * p.vpt, c = c0 + tx * VEC;
     const bool on = ty < p.ty && tx * VEC < width;
     const int64_t first = (int64_t)tile * p.tile_rows, end = min(first + p.tile_rows, a.rows);
     const int64_t x0 = ((int64_t)b * a.rows) * a.x_stride + c;
+    const Terms::Source src = Terms::load(a, b, c0, width);
+    const int64_t step = (int64_t)p.ty * a.x_stride, out_step = (int64_t)p.ty * a.out_stride;
     Vec<VEC, XBF> v[R];
     int64_t r = first + ty;
-    auto load = [&](int live) {
+    auto load = [&]() {
 #pragma unroll
-        for (int i = 0; i < R; ++i) v[i].load(a.x, x0 + (r + (int64_t)min(i, live - 1) * p.ty) * a.x_stride);
+        for (int i = 0; i < R; ++i)
+            if (r + (int64_t)i * p.ty < end) v[i].load(a.x, x0 + r * a.x_stride + i * step);
     };
-    auto live_at = [&]() { return (int)min((int64_t)R, (end - r + p.ty - 1) / p.ty); };
-    if (on && r < end) load(live_at());         // ahead of the statistics
-    terms.load(a, b, c0, width, kSplitThreads);
+    if (on) load();                             // ahead of the statistics
     const int q_all = p.parts * p.tiles;
     const float inv = 1.f / ((float)a.rows * (float)p.cg);
     const float last_rows = (float)(a.rows - (int64_t)(p.tiles - 1) * p.tile_rows);
@@ -461,11 +487,12 @@ __global__ __launch_bounds__(kSplitThreads) void norm_apply_kernel(Shape p) {
             m.join((ti == p.tiles - 1 ? last_rows : (float)p.tile_rows) * (float)wq, v.x, v.y);
         }
         m.join_lanes(lanes);
-        if ((lane & (lanes - 1)) == 0) {
+        if ((lane & (lanes - 1)) == lanes - 1) {
             stat[0][g] = m.mean;
             stat[1][g] = 1.f / sqrtf(m.m2 * inv + a.eps);
         }
     }
+    terms.put(src, width, kSplitThreads);
     __syncthreads();
     terms.fold(stat[0], stat[1], width, p.parts == 1 ? p.cg : width, kSplitThreads);
     if (!on) return;
@@ -474,17 +501,17 @@ __global__ __launch_bounds__(kSplitThreads) void norm_apply_kernel(Shape p) {
     const int64_t o0 = ((int64_t)b * a.rows) * a.out_stride + c;
     by_kind(a.act, a.out_bf16, [&](auto act, auto obf) {
         while (r < end) {
-            const int live = live_at();
+            const int64_t o = o0 + r * a.out_stride;
 #pragma unroll
             for (int i = 0; i < R; ++i)
-                if (i < live) {
+                if (r + (int64_t)i * p.ty < end) {
                     float y[VEC];
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) y[j] = activate((v[i].get(j) - mean[j]) * A[j] + D[j], act);
-                    store_vec<VEC, decltype(obf)::value, STREAM>(a.out, o0 + (r + (int64_t)i * p.ty) * a.out_stride, y);
+                    store_vec<VEC, decltype(obf)::value, STREAM>(a.out, o + i * out_step, y);
                 }
             r += (int64_t)p.ty * R;
-            if (r < end) load(live_at());
+            load();
         }
     });
 }
@@ -519,6 +546,7 @@ Shape plan(const GroupNormArgs& a, int v, int least) {
         p.slabs = a.groups * p.parts;
     }
     p.vpt = p.width / v;
+    p.inv_vpt = 1.f / (float)p.vpt;
     return p;
 }
 

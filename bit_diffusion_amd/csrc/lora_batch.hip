@@ -44,12 +44,12 @@ struct Tile {
 };
 
 __device__ __forceinline__ int wave_scan(int v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(v, d, 64);
-        if (lane >= d) v += o;
-    }
+    v += dpp<kShr + 1>(0, v);
+    v += dpp<kShr + 2>(0, v);
+    v += dpp<kShr + 4>(0, v);
+    v += dpp<kShr + 8>(0, v);
+    v += dpp<kBcast15, 0xa>(0, v);
+    v += dpp<kBcast31, 0xc>(0, v);
     return v;
 }
 
