@@ -698,6 +698,8 @@ void down(const LoraBatchArgs& a, hipStream_t st) {
                        per_xcd(tiles), inner);
 }
 
+constexpr int64_t kWideRows = 4096;
+
 template <int TB, int NRB, int RW, int KW, int D, int OCC>
 void down_wide(const LoraBatchArgs& a, hipStream_t st) {
     const int64_t tiles = most_tiles(a.M, a.n_segments, TB * 16);
@@ -707,9 +709,20 @@ void down_wide(const LoraBatchArgs& a, hipStream_t st) {
 }
 
 void launch_down(const LoraBatchArgs& a, hipStream_t st) {
-    if (a.nb >= 2 && most_tiles(a.M, a.n_segments, 64) >= 256) {
-        if (a.nb == 4) down_wide<4, 8, 2, 2, 2, 4>(a, st);
-        else down_wide<4, 4, 2, 1, 2, 4>(a, st);
+    if (a.nb >= 2 && a.M >= kWideRows) {
+        // the lowest tiles that need one round of 256 CUs at most: a workgroup has a CU's LDS and
+        // registers nearly to itself, and a few tiles too many cost another round
+        const int tall = most_tiles(a.M, a.n_segments, 32) <= 256 ? 2
+                         : most_tiles(a.M, a.n_segments, 64) <= 256 || most_tiles(a.M, a.n_segments, 96) > 256 ? 4 : 6;
+        if (a.nb == 4) {
+            if (tall == 2) down_wide<2, 8, 2, 1, 2, 4>(a, st);
+            else if (tall == 4) down_wide<4, 8, 2, 2, 2, 4>(a, st);
+            else down_wide<6, 8, 3, 2, 2, 2>(a, st);
+        } else {
+            if (tall == 2) down_wide<2, 4, 1, 1, 2, 4>(a, st);
+            else if (tall == 4) down_wide<4, 4, 2, 1, 2, 4>(a, st);
+            else down_wide<6, 4, 3, 1, 2, 4>(a, st);
+        }
         return;
     }
     if (a.M >= 8192) {
