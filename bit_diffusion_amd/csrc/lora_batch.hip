@@ -714,21 +714,11 @@ void launch_down(const LoraBatchArgs& a, hipStream_t st) {
         // registers nearly to itself, and a few tiles too many cost another round
         const int tall = most_tiles(a.M, a.n_segments, 32) <= 256 ? 2
                          : most_tiles(a.M, a.n_segments, 64) <= 256 || most_tiles(a.M, a.n_segments, 96) > 256 ? 4 : 6;
-        if (a.nb == 4) {
-            if (tall == 2) down_wide<2, 8, 2, 1, 2, 4>(a, st);
-            else if (tall == 4) down_wide<4, 8, 2, 2, 2, 4>(a, st);
-            else down_wide<6, 8, 3, 2, 2, 2>(a, st);
-        } else {
-            if (tall == 2) down_wide<2, 4, 1, 1, 2, 4>(a, st);
-            else if (tall == 4) down_wide<4, 4, 2, 1, 2, 4>(a, st);
-            else down_wide<6, 4, 3, 1, 2, 4>(a, st);
-        }
-        return;
-    }
-    if (a.M >= 8192) {
-        if (a.R <= 16) down<2, 1, 8, 2>(a, st);
-        else if (a.R <= 32) down<2, 2, 8, 1>(a, st);
-        else down<2, 4, 8, 1>(a, st);
+        // low tiles leave CUs for a second workgroup on the other half of 128 ranks (4096 rows,
+        // K = 4096: 46 us in all, 50 with one workgroup for all ranks)
+        if (tall == 2) down_wide<2, 4, 1, 1, 2, 4>(a, st);
+        else if (a.nb == 4) tall == 4 ? down_wide<4, 8, 2, 2, 3, 2>(a, st) : down_wide<6, 8, 3, 2, 3, 2>(a, st);
+        else tall == 4 ? down_wide<4, 4, 2, 1, 3, 2>(a, st) : down_wide<6, 4, 3, 1, 3, 2>(a, st);
         return;
     }
     // rank blocks of a workgroup: as many as leave a workgroup for each of 256 CUs
@@ -740,15 +730,15 @@ void launch_down(const LoraBatchArgs& a, hipStream_t st) {
     else down<1, 4, 16, 1>(a, st);
 }
 
-template <int RBE, int NB, bool BF16>
+template <int RBE, int CB, int NB, bool BF16>
 void up(const LoraBatchArgs& a, hipStream_t st) {
-    // columns of a wave: 64 cover whole cache lines of out, 32 leave registers for more waves
-    // (rank 16, 4096 x 3072: 13.5 us with 64, 11.5 with 32; rank 32, 4608 x 12288: 59 and 62)
-    constexpr int CB = NB == 0 || NB == 4 ? 2 : 4;
     const int64_t tiles = most_tiles(a.M, a.n_segments, RBE * 16);
     const int blocks = (a.N + 64 * CB - 1) / (64 * CB);
+    // up to 2 blocks a workgroup, so that neighbours work on the rest of the same rows at a time;
+    // 8 where t is large (16384 x 4096: rank 32 105 us in all, 122 with 8; rank 128 157, 165 with 2)
+    constexpr int kMost = NB == 4 ? 8 : 2;
     int span = 1;
-    while (span < 8 && span < blocks && tiles * ((blocks + 2 * span - 1) / (2 * span)) >= 1024) span *= 2;
+    while (span < kMost && span < blocks && tiles * ((blocks + 2 * span - 1) / (2 * span)) >= 1024) span *= 2;
     const int inner = (blocks + span - 1) / span;
     hipLaunchKernelGGL((lora_up_kernel<RBE, CB, NB, BF16, 2>), dim3(grid_of(tiles, inner)), dim3(256), 0, st, a,
                        per_xcd(tiles), inner, span);
@@ -756,11 +746,14 @@ void up(const LoraBatchArgs& a, hipStream_t st) {
 
 template <int RBE, bool BF16>
 void up_rank(const LoraBatchArgs& a, hipStream_t st) {
+    // columns of a wave: 64 cover whole cache lines of out, 32 make more and smaller workgroups
+    // (rank 16: 16384 x 4096 73 us in all with 64, 79 with 32; 4096 x 3072 22.4 and 21.2)
+    const bool wide = most_tiles(a.M, a.n_segments, RBE * 16) * ((a.N + 255) / 256) >= 2048;
     switch (a.nb) {
-        case 0: up<RBE, 0, BF16>(a, st); break;
-        case 1: up<RBE, 1, BF16>(a, st); break;
-        case 2: up<RBE, 2, BF16>(a, st); break;
-        default: up<RBE, 4, BF16>(a, st);
+        case 0: wide ? up<RBE, 4, 0, BF16>(a, st) : up<RBE, 2, 0, BF16>(a, st); break;
+        case 1: wide ? up<RBE, 4, 1, BF16>(a, st) : up<RBE, 2, 1, BF16>(a, st); break;
+        case 2: wide ? up<RBE, 4, 2, BF16>(a, st) : up<RBE, 2, 2, BF16>(a, st); break;
+        default: up<RBE, 2, 4, BF16>(a, st);
     }
 }
 
@@ -792,9 +785,11 @@ void launch_lora_batch(const LoraBatchArgs& args, hipStream_t st) {
         return;
     }
     launch_down(a, st);
-    const bool tall = (a.M / 32) * inner >= 1024;
-    if (a.bf16) tall ? up_rank<2, true>(a, st) : up_rank<1, true>(a, st);
-    else tall ? up_rank<2, false>(a, st) : up_rank<1, false>(a, st);
+    // 32 rows to a workgroup where that leaves 1024 of them; t's third term for fp32 takes the
+    // registers of the second 16 rows (30000 x 1024, rank 64: 90 us in all, 99 with 32 rows)
+    if (!a.bf16) up_rank<1, false>(a, st);
+    else if ((a.M / 32) * inner >= 1024) up_rank<2, true>(a, st);
+    else up_rank<1, true>(a, st);
 }
 
 }  // namespace svdq
