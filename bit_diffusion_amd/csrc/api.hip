@@ -146,10 +146,13 @@ svdq_status check_lora_batch(int64_t M, int32_t K, int32_t N, int32_t max_rank, 
     if (max_rank > 128)
         return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "max_rank %d exceeds the supported maximum 128", max_rank);
     if (n_segments < 0) return fail(SVDQ_ERR_INVALID_ARG, "n_segments = %d is negative", n_segments);
-    if (n_segments > 1 << 20)
-        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "n_segments = %d exceeds the supported maximum 2^20", n_segments);
-    if (M > (int64_t)1 << 26 || N > 1 << 23)
-        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "M = %lld, N = %d too large for one launch", (long long)M, N);
+    if (n_segments > 1 << 16)
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "n_segments = %d exceeds the supported maximum 2^16", n_segments);
+    if (K > 1 << 24)
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "K %d exceeds the supported maximum 2^24", K);
+    if (M > (int64_t)1 << 22 || !svdq::lora_batch_fits(M, N, n_segments))
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "M = %lld, N = %d, n_segments = %d too large for one launch",
+                    (long long)M, N, n_segments);
     return SVDQ_OK;
 }
 

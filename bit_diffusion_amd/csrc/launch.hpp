@@ -154,6 +154,7 @@ void launch_read(const void* src, int64_t bytes, void* out, hipStream_t st);
 int64_t quantize_next_workspace_bytes(int64_t M, int N, int next_r);
 
 // adapters of many requests (lora_batch.hip)
+bool lora_batch_fits(int64_t M, int N, int n_segments);   // one launch's grid
 int64_t lora_batch_workspace_bytes(int64_t M, int R, int n_segments);
 void launch_lora_batch(const LoraBatchArgs& a, hipStream_t st);
 

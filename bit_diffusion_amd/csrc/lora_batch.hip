@@ -130,58 +130,49 @@ __device__ __forceinline__ void to_operands(uint4* buf, const uint4 (&v)[4], boo
     for (int k = 0; k < 4; ++k) op[k] = buf[r16 * 16 + ((k * 4 + q) ^ r16)];
 }
 
-// One wave's share of the down-projection: every stride-th step of 128 channels from `first`,
-// 16 RBM rows x rank blocks rb0 to rb0 + RB - 1 (those past the adapter's last repeat it; the
-// caller drops them).  U steps are loaded at a time; channels past K count as zeros.
-// acc[i][j]: lane (q, r16) holds ranks 4 q to 4 q + 3 of block j for row 16 i + r16.
-template <int RBM, int RB, int U>
+// One wave's share of the down-projection: every stride-th step of 128 channels from `first`, 16
+// rows x rank blocks rb0 to rb0 + RB - 1 (those past the adapter's last repeat it; the caller
+// drops them).  U steps are loaded at a time; channels past K count as zeros.
+// acc[j]: lane (q, r16) holds ranks 4 q to 4 q + 3 of block j for row r16.
+template <int RB, int U>
 __device__ __forceinline__ void down_steps(const LoraBatchArgs& a, const Tile& t, const Adapter& ad, int rb0,
-                                           int first, int stride, uint4* buf, f32x4 (&acc)[RBM][RB]) {
+                                           int first, int stride, uint4* buf, f32x4 (&acc)[RB]) {
     const int lane = threadIdx.x & 63, q = lane >> 4, r16 = lane & 15, K = a.K;
-    const uint16_t* xp[RBM][4];
+    const uint16_t* xp[4];
 #pragma unroll
-    for (int i = 0; i < RBM; ++i)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-            xp[i][g] = (const uint16_t*)a.x + (int64_t)(t.row0 + min(i * 16 + g * 4 + q, t.rows - 1)) * a.x_stride;
+    for (int g = 0; g < 4; ++g)
+        xp[g] = (const uint16_t*)a.x + (int64_t)(t.row0 + min(g * 4 + q, t.rows - 1)) * a.x_stride;
     const uint16_t* dp = (const uint16_t*)a.down + ((int64_t)ad.s * a.R + q) * K;
     const int last = ((ad.rank + 15) >> 4) - 1;
 #pragma unroll
-    for (int i = 0; i < RBM; ++i)
-#pragma unroll
-        for (int j = 0; j < RB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < RB; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     const int steps = (K + 127) >> 7;
     for (int st = first; st < steps; st += U * stride) {
-        uint4 xv[U][RBM][4], dv[U][RB][4];
+        uint4 xv[U][4], dv[U][RB][4];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k = (st + u * stride) * 128 + r16 * 8, kk = min(k, K - 8);
+            const int k = min((st + u * stride) * 128 + r16 * 8, K - 8);
 #pragma unroll
-            for (int i = 0; i < RBM; ++i)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) xv[u][i][g] = *(const uint4*)(xp[i][g] + kk);
+            for (int g = 0; g < 4; ++g) xv[u][g] = *(const uint4*)(xp[g] + k);
 #pragma unroll
             for (int j = 0; j < RB; ++j)
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
-                    dv[u][j][g] = *(const uint4*)(dp + (int64_t)(min(rb0 + j, last) * 16 + g * 4) * K + kk);
+                    dv[u][j][g] = *(const uint4*)(dp + (int64_t)(min(rb0 + j, last) * 16 + g * 4) * K + k);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             // zeroed here and not at the load, which nothing should have to wait for
             const bool on = (st + u * stride) * 128 + r16 * 8 < K;
-            uint4 xo[RBM][4];
-#pragma unroll
-            for (int i = 0; i < RBM; ++i) to_operands(buf, xv[u][i], on, xo[i]);
+            uint4 x[4];
+            to_operands(buf, xv[u], on, x);
 #pragma unroll
             for (int j = 0; j < RB; ++j) {
                 uint4 d[4];
                 to_operands(buf, dv[u][j], on, d);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int i = 0; i < RBM; ++i) acc[i][j] = mfma16(d[k], xo[i][k], acc[i][j]);
+                for (int k = 0; k < 4; ++k) acc[j] = mfma16(d[k], x[k], acc[j]);
             }
         }
     }
@@ -249,53 +240,54 @@ __device__ __forceinline__ void tile_of(int id, int per, int inner, int& tile, i
     if (per > 0) tile += (id & 7) * per;
 }
 
-// Down-projection of a tile of 16 RBM rows, RB rank blocks: the W waves take the steps of K
-// in turn and their sums are added in wave order through LDS.
-template <int RBM, int RB, int W, int U>
+// Down-projection of a tile of 16 rows, RB rank blocks: the W waves take the steps of K in turn
+// and their sums are added in wave order through LDS.  16 waves of one step at a time (64
+// registers) leave room for a second workgroup on the CU, which the few tiles past 256 need:
+// 4096 x 3072, rank 16: 10.7 us; 12.9 with two steps at a time and one workgroup a CU.
+template <int RB, int W, int U>
 __global__ __launch_bounds__(W * 64) void lora_down_kernel(LoraBatchArgs a, int per, int inner) {
-    constexpr int kSums = W * RBM * RB * 64, kStage = W * 256;
+    constexpr int kSums = W * RB * 64, kStage = W * 256;
     static_assert(kSums * 16 <= 65536 && kStage * 16 <= 65536, "64 KB of LDS");
     __shared__ uint4 lds[kSums > kStage ? kSums : kStage];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, q = lane >> 4, r16 = lane & 15;
     int tile, part;
     tile_of(blockIdx.x, per, inner, tile, part);
-    const Tile t = find_tile<RBM>(a, tile);
-    if (t.rows == 0) return;
+    const Tile t = find_tile<1>(a, tile);
+    // offsets that break the rules may make more blocks than there is room for
+    if (t.rows == 0 || t.block >= a.max_blocks) return;
     const Adapter ad = adapter_of(a, t.id);
     if (ad.rank == 0) return;
     const int rb0 = part * RB;
     const bool some = rb0 * 16 < ad.rank;   // uniform over the workgroup
     f32x4* red = (f32x4*)lds;
     if (some) {
-        f32x4 acc[RBM][RB];
-        down_steps<RBM, RB, U>(a, t, ad, rb0, w, W, lds + w * 256, acc);
+        f32x4 acc[RB];
+        down_steps<RB, U>(a, t, ad, rb0, w, W, lds + w * 256, acc);
         __syncthreads();                    // the sums take the operands' place
 #pragma unroll
-        for (int i = 0; i < RBM; ++i)
-#pragma unroll
-            for (int j = 0; j < RB; ++j) red[(w * RBM * RB + i * RB + j) * 64 + lane] = acc[i][j];
+        for (int j = 0; j < RB; ++j) red[(w * RB + j) * 64 + lane] = acc[j];
         __syncthreads();
     }
     const int ranks = a.nb == 0 ? 16 : a.nb * 32, ops = a.nb == 0 ? 2 : 3;
-    for (int b = w; b < RBM * RB; b += W) {
-        const int i = b / RB, j0 = (rb0 + b % RB) * 16 + q * 4;
-        // offsets that break the rules may make more blocks than there is room for
-        if (i * 16 >= t.rows || j0 >= ranks || t.block + i >= a.max_blocks) continue;
+    for (int b = w; b < RB; b += W) {
+        const int j0 = (rb0 + b) * 16 + q * 4;
+        if (j0 >= ranks) continue;
         f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
         if (some) {
 #pragma unroll
-            for (int o = 0; o < W; ++o) v += red[(o * RBM * RB + b) * 64 + lane];
+            for (int o = 0; o < W; ++o) v += red[(o * RB + b) * 64 + lane];
         }
-        put_terms((uint2*)a.work + (int64_t)(t.block + i) * ops * blocks_of(a.nb) * 128, a.nb, a.bf16 != 0, j0, r16, v,
-                  ad.alpha, ad.rank - j0);
+        put_terms((uint2*)a.work + (int64_t)t.block * ops * blocks_of(a.nb) * 128, a.nb, a.bf16 != 0, j0, r16, v, ad.alpha,
+                  ad.rank - j0);
     }
 }
 
 // Down-projection of a tile of 16 TB rows, 16 NRB ranks, for ranks past 32: the rows and the
 // adapter's A are staged once for the workgroup, 128 channels at a time, and each wave has RW
-// row blocks x KW rank blocks over all of K.  D steps are in flight in registers.  OCC waves a
-// SIMD: ragged segments make a few more tiles than fill the CUs evenly, and those must find
-// room beside the others, or they cost a whole round.
+// row blocks x KW rank blocks over all of K.  D steps are in flight in registers (OCC: waves a
+// SIMD that the registers must leave room for).  Bound by the CU's LDS and its barriers: 1.4 us
+// a step of 96 rows x 128 ranks, of which LDS moves 216 KB; 16384 x 4096 at rank 128 takes 60 us
+// (2.2 TB/s of x).
 // Steps are counted from another one in each tile, round the end of K: rows of x and A lie K
 // elements apart, a distance that falls on few memory channels, and workgroups that walk K in
 // step would all ask the same ones.
@@ -552,12 +544,13 @@ struct UpTile {
 };
 
 // A workgroup's rows x `blocks` blocks of 64 CB columns, 16 CB columns to each of 4 waves: t
-// stays in registers; base is loaded D blocks ahead, B as soon as the block before has its own
+// stays in registers; base is loaded two blocks ahead, B as soon as the block before has its own
 // in LDS.
-template <int RBE, int CB, int NB, bool BF16, int D>
+template <int RBE, int CB, int NB, bool BF16>
 __device__ __forceinline__ void up_blocks(const LoraBatchArgs& a, const Tile& t, const Adapter& ad, int first,
                                           int blocks, uint4* lds) {
     using Up = UpTile<RBE, CB, NB, BF16>;
+    constexpr int D = 2;
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
     auto col = [&](int b) { return ((first + b) * 4 + w) * 16 * CB; };
     Up u;
@@ -594,7 +587,7 @@ __device__ __forceinline__ void up_blocks(const LoraBatchArgs& a, const Tile& t,
 }
 
 // Up-projection of a tile of 16 RBE rows, `span` blocks of columns.
-template <int RBE, int CB, int NB, bool BF16, int D>
+template <int RBE, int CB, int NB, bool BF16>
 __global__ __launch_bounds__(256) void lora_up_kernel(LoraBatchArgs a, int per, int inner, int span) {
     using Up = UpTile<RBE, CB, NB, BF16>;
     __shared__ uint4 lds[4][Up::kLds];
@@ -617,15 +610,18 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraBatchArgs a, int per, 
     }
     if constexpr (NB > 2) {
         if (ad.rank <= 64) {
-            up_blocks<RBE, CB, 2, BF16, D>(a, t, ad, first, blocks, lds[w]);
+            up_blocks<RBE, CB, 2, BF16>(a, t, ad, first, blocks, lds[w]);
             return;
         }
     }
-    up_blocks<RBE, CB, NB, BF16, D>(a, t, ad, first, blocks, lds[w]);
+    up_blocks<RBE, CB, NB, BF16>(a, t, ad, first, blocks, lds[w]);
 }
 
 // Both products for a tile of 16 rows x 256 columns, 32 columns to each of 8 waves: the waves
-// share the steps of K, and the rows' t goes through LDS.
+// share the steps of K, and the rows' t goes through LDS.  Every workgroup of a tile reads its
+// rows and A again (from the L2s), which costs less than a second launch while they are few
+// and fit one round of CUs: 2 rows, 3072 -> 18432, rank 16: 7.5 us, two launches 11; 1237 rows,
+// rank 64, in 332 workgroups: 15.0 us, in two launches 12.8.
 template <int RB, bool BF16, int U>
 __global__ __launch_bounds__(512) void lora_few_rows_kernel(LoraBatchArgs a, int inner) {
     constexpr int W = 8, NB = RB / 2;
@@ -650,11 +646,11 @@ __global__ __launch_bounds__(512) void lora_few_rows_kernel(LoraBatchArgs a, int
         return;
     }
     u.load_up(a, ad, c0);
-    f32x4 acc[1][RB];
-    down_steps<1, RB, U>(a, t, ad, 0, w, W, lds[w], acc);
+    f32x4 acc[RB];
+    down_steps<RB, U>(a, t, ad, 0, w, W, lds[w], acc);
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < RB; ++j) red[(w * RB + j) * 64 + lane] = acc[0][j];
+    for (int j = 0; j < RB; ++j) red[(w * RB + j) * 64 + lane] = acc[j];
     __syncthreads();
     if (w < RB) {
         const int j0 = w * 16 + q * 4;
@@ -690,14 +686,15 @@ unsigned grid_of(int64_t tiles, int inner) {
     return (unsigned)((per > 0 ? 8 * per : tiles) * inner);
 }
 
-template <int RBM, int RB, int W, int U>
+template <int RB, int W, int U>
 void down(const LoraBatchArgs& a, hipStream_t st) {
-    const int64_t tiles = most_tiles(a.M, a.n_segments, RBM * 16);
+    const int64_t tiles = most_tiles(a.M, a.n_segments, 16);
     const int inner = ((a.nb == 0 ? 1 : a.nb * 2) + RB - 1) / RB;
-    hipLaunchKernelGGL((lora_down_kernel<RBM, RB, W, U>), dim3(grid_of(tiles, inner)), dim3(W * 64), 0, st, a,
-                       per_xcd(tiles), inner);
+    hipLaunchKernelGGL((lora_down_kernel<RB, W, U>), dim3(grid_of(tiles, inner)), dim3(W * 64), 0, st, a, per_xcd(tiles),
+                       inner);
 }
 
+// Rows from which A is staged once a workgroup (4096 x 1024, rank 64, fp32: 34.6 us in all, 38.9 without).
 constexpr int64_t kWideRows = 4096;
 
 template <int TB, int NRB, int RW, int KW, int D, int OCC>
@@ -725,9 +722,9 @@ void launch_down(const LoraBatchArgs& a, hipStream_t st) {
     const int64_t tiles = most_tiles(a.M, a.n_segments, 16);
     const int rb = a.R / 16;
     auto fills = [&](int per) { return tiles * ((rb + per - 1) / per) >= 256; };
-    if (rb == 1 || !fills(2)) down<1, 1, 16, 1>(a, st);
-    else if (rb == 2 || !fills(4)) down<1, 2, 8, 1>(a, st);
-    else down<1, 4, 16, 1>(a, st);
+    if (rb == 1 || !fills(2)) down<1, 16, 1>(a, st);
+    else if (rb == 2 || !fills(4)) down<2, 8, 1>(a, st);
+    else down<4, 16, 1>(a, st);
 }
 
 template <int RBE, int CB, int NB, bool BF16>
@@ -740,7 +737,7 @@ void up(const LoraBatchArgs& a, hipStream_t st) {
     int span = 1;
     while (span < kMost && span < blocks && tiles * ((blocks + 2 * span - 1) / (2 * span)) >= 1024) span *= 2;
     const int inner = (blocks + span - 1) / span;
-    hipLaunchKernelGGL((lora_up_kernel<RBE, CB, NB, BF16, 2>), dim3(grid_of(tiles, inner)), dim3(256), 0, st, a,
+    hipLaunchKernelGGL((lora_up_kernel<RBE, CB, NB, BF16>), dim3(grid_of(tiles, inner)), dim3(256), 0, st, a,
                        per_xcd(tiles), inner, span);
 }
 
@@ -767,6 +764,13 @@ void few_rows(const LoraBatchArgs& a, hipStream_t st) {
 }
 
 }  // namespace
+
+// Grids stay below 2^32 threads: at most 8 workgroups of 1024 a tile in the down-projection, one
+// of 256 for each 128 columns in the other, tiles rounded up to whole XCDs.
+bool lora_batch_fits(int64_t M, int N, int n_segments) {
+    const int64_t tiles = most_tiles(M, n_segments, 16) + 8;
+    return tiles < (int64_t)1 << 19 && tiles * (((int64_t)N + 127) / 128) < (int64_t)1 << 24;
+}
 
 int64_t lora_batch_workspace_bytes(int64_t M, int R, int n_segments) {
     if (n_segments == 0) return 0;

@@ -384,8 +384,9 @@ svdq_status svdq_merge_lora(const svdq_layer_cfg* cfg, int32_t r_lora, const voi
  *   out        [M, N] of out_dtype, rows out_stride apart (>= N).
  *   workspace  svdq_lora_batch_workspace_bytes(M, K, N, max_rank, n_segments) bytes at least,
  *              16-byte aligned, overwritten; calls that may overlap in time need one each.
- * K a positive multiple of 64; max_rank a multiple of 16 up to 128; M up to 2^26; n_segments
- * up to 2^20 (0 is valid and enqueues nothing).  The segments' arrays are read when the work
+ * K a positive multiple of 64 up to 2^24; max_rank a multiple of 16 up to 128; M up to 2^22 and
+ * n_segments up to 2^16 (0 is valid and enqueues nothing), where (M / 16 + n_segments + 8)
+ * ceil(N / 128) stays below 2^24.  The segments' arrays are read when the work
  * runs, so a captured graph replays with what they hold then.  x, lora_down and lora_up must
  * be 16-byte aligned, base and out aligned to their type (16-byte aligned rows are faster).
  * All buffers are device memory on the current device.  Bit-reproducible from run to run. */

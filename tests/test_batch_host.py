@@ -24,7 +24,10 @@ def _lora(**kw):
     (dict(M=-1), INV, "M"), (dict(M=(1 << 26) + 1), UNS, "too large"), (dict(K=100), INV, "K"), (dict(K=0), INV, "K"),
     (dict(N=0), INV, "N"), (dict(R=0), INV, "max_rank"), (dict(R=24), INV, "max_rank"),
     (dict(R=144), UNS, "max_rank"), (dict(S=0), INV, "n_adapters"), (dict(n=-1), INV, "n_segments"),
-    (dict(n=(1 << 20) + 1), UNS, "n_segments"), (dict(x=None), INV, "x is NULL"), (dict(x=FAKE + 8), INV, "aligned"),
+    (dict(n=(1 << 20) + 1), UNS, "n_segments"), (dict(n=(1 << 16) + 1), UNS, "n_segments"),
+    (dict(K=(1 << 24) + 64, xs=1 << 25), UNS, "K"), (dict(M=(1 << 22) + 1), UNS, "too large"),
+    (dict(M=1 << 22, N=1 << 13, bs=1 << 13, os=1 << 13), UNS, "too large"),
+    (dict(N=(1 << 31) - 1, bs=1 << 31, os=1 << 31), UNS, "too large"), (dict(x=None), INV, "x is NULL"), (dict(x=FAKE + 8), INV, "aligned"),
     (dict(xs=120), INV, "x_stride"), (dict(xs=132), INV, "x_stride"), (dict(down=None), INV, "lora_down"),
     (dict(up=FAKE + 4), INV, "lora_up"), (dict(alphas=None), INV, "alphas"), (dict(ranks=FAKE + 2), INV, "ranks"),
     (dict(starts=None), INV, "seg_start"), (dict(ids=None), INV, "seg_adapter"), (dict(base=FAKE + 2), INV, "base"),

@@ -120,6 +120,22 @@ CASES = {
     "64 rows exactly": dict(M=64, K=64, N=256, R=16, starts=[0, 64], ids=[0]),
     "tall tiles": dict(M=8300, K=128, N=1030, R=32, starts=cuts(4100, 1, 4190), ids=[0, 1, 2]),
     "tall tiles, rank 128, fp32": dict(M=8200, K=64, N=1100, R=128, starts=cuts(63, 65, 8000, 72), ids=[0, 1, 2, 0], bf=False, act=1),
+    "wide, 32 rows": dict(M=4100, K=192, N=72, R=64, starts=cuts(2000, 33, 0, 2067), ids=[0, 1, 2, 2], ranks=[64, 3, 40], act=1),
+    "wide, 32 rows, rank 128": dict(M=4200, K=320, N=40, R=128, starts=cuts(1, 4000, 150, first=9), ids=[0, 1, 2], ranks=[128, 64, 17], bf=False),
+    "wide, 64 rows": dict(M=9000, K=448, N=56, R=64, starts=cuts(63, 65, 8000, 872), ids=[0, 1, 2, 0], ranks=[48, 64, 64]),
+    "wide, 64 rows, rank 128": dict(M=9001, K=320, N=130, R=128, starts=cuts(4500, 4501), ids=[0, 1], ranks=[128, 100, 7]),
+    "wide, 96 rows": dict(M=17000, K=128, N=48, R=64, starts=cuts(95, 97, 16000, 700), ids=[0, -1, 2, 0], bf=False),
+    "wide, 96 rows, rank 128": dict(M=16600, K=256, N=40, R=128, starts=cuts(8000, 0, 8500, 90), ids=[0, 1, 2, 1], ranks=[128, 1, 64]),
+    "wide, more than one round": dict(M=33000, K=64, N=33, R=48, starts=cuts(33000), ids=[1]),
+    "many one-row segments, rank 64": dict(M=300, K=128, N=140, R=64, starts=list(range(301)), ids=[i % 4 - 1 for i in range(300)], ranks=[64, 12, 33]),
+    "many one-row segments, rank 128, fp32": dict(M=300, K=256, N=270, R=128, starts=list(range(301)), ids=[i % 3 for i in range(300)], bf=False),
+    "two rank blocks": dict(M=4500, K=128, N=80, R=32, starts=cuts(4500), ids=[1]),
+    "whole lines, rank 16": dict(M=8200, K=64, N=2060, R=16, starts=cuts(4000, 4200), ids=[0, 1], act=2),
+    "whole lines, rank 16, fp32": dict(M=8200, K=64, N=1028, R=16, starts=cuts(4000, 4200), ids=[0, 1], bf=False),
+    "whole lines, rank 64": dict(M=8200, K=64, N=2060, R=64, starts=cuts(4000, 4200), ids=[0, 1], ranks=[64, 30, 1]),
+    "whole lines, rank 32, fp32": dict(M=8200, K=64, N=1027, R=32, starts=cuts(4000, 4200), ids=[0, 1], bf=False, act=1),
+    "whole lines, rank 64, fp32": dict(M=8200, K=64, N=1028, R=64, starts=cuts(8200), ids=[2], bf=False),
+    "32 rows, rank 128": dict(M=8200, K=64, N=1100, R=128, starts=cuts(4000, 4200), ids=[0, 1], ranks=[128, 64, 1], act=1),
     "long K": dict(M=20, K=12288, N=64, R=16, starts=cuts(7, 13), ids=[0, 1], bf=False),
 }
 
