@@ -14,7 +14,8 @@
 // neighbouring channels and no group is shared where it fits.
 //   one launch (few rows): every workgroup of a slab takes the statistics of all its rows and
 //             normalises its own share of them, which it keeps in registers meanwhile.  The
-//             others' rows are read again from the caches; nothing is exchanged.
+//             others' rows are read again from the caches; nothing is exchanged.  In place only
+//             where a slab has one workgroup.
 //   two launches (many rows): statistics of row tiles, then every workgroup joins those of its
 //             groups, in a fixed order, and normalises a tile.
 // Statistics of a thread go chunk by chunk, two passes over each in registers, joined as
@@ -590,8 +591,12 @@ template <int VEC, bool XBF, Span SPAN>
 void run(const GroupNormArgs& a, hipStream_t st) {
     const Shape p = plan(a, VEC, 4 * VEC);
     const int64_t vectors = p.vpt * a.rows;                  // of a slab
-    if (p.parts > 1 || vectors > kOneVectors) split<VEC, XBF, SPAN>(a, st);
-    else if (vectors <= 256 || vectors * p.slabs * a.B <= 256 * 256) one<VEC, XBF, SPAN, 1, 256>(p, st);
+    const int lanes = 256 / p.vpt;
+    const bool few = vectors <= 256 || vectors * p.slabs * a.B <= 256 * 256;
+    // in place, a slab's second workgroup would overwrite rows that the first still reads
+    const bool alone = a.x != a.out || a.rows <= lanes * (few ? 1 : 4);
+    if (p.parts > 1 || vectors > kOneVectors || !alone) split<VEC, XBF, SPAN>(a, st);
+    else if (few) one<VEC, XBF, SPAN, 1, 256>(p, st);
     else one<VEC, XBF, SPAN, 4, 256>(p, st);
 }
 

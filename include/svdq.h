@@ -408,7 +408,7 @@ svdq_status svdq_lora_batch(int64_t M, int32_t K, int32_t N, int32_t max_rank, i
  *   out  = act(((x - mean) / sqrt(var + eps) weight_c + bias_c) (1 + mod_scale[b, c])
  *              + mod_shift[b, c])
  *
- * in fp32, rounded once.
+ * in fp32, rounded once (the sum of squares about a group's mean must stay in fp32's range).
  *   x          [B rows, C] of x_dtype, rows x_stride elements apart (>= C).
  *   weight, bias [C] bf16, or NULL: 1 and 0.
  *   mod_scale, mod_shift  [B, C] of mod_dtype, rows mod_stride apart (>= C), or NULL: 0.  Two

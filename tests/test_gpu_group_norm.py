@@ -143,14 +143,17 @@ def test_nan_stays_in_its_group(rows):
     assert torch.equal(got, want)
 
 
-@pytest.mark.parametrize("rows,xd", [(150, BF), (150, F32), (40000, BF)])
-def test_in_place(rows, xd):
-    c = Case(7, 1, rows, 64, 8, xd=xd, od=xd, mod=F32)
-    want = c.call().clone()
+# in place, rows that other workgroups still read must stay: more workgroups than run at a time,
+# in images that out of place take one launch
+@pytest.mark.parametrize("B,rows,C,G,xd", [(1, 150, 64, 8, BF), (1, 150, 64, 8, F32), (1, 40000, 64, 8, BF), (2, 16, 64, 8, F32),
+                                           (40, 1024, 320, 32, BF), (40, 1000, 96, 12, F32), (64, 64, 640, 32, BF),
+                                           (300, 256, 64, 2, BF), (8, 300, 50, 5, F32)])
+def test_in_place(B, rows, C, G, xd):
+    c = Case(7, B, rows, C, G, xd=xd, od=xd, mod=F32)
     buf = c.x.to(DEV)
     c.call(x=buf, out=buf)
     torch.cuda.synchronize()
-    assert torch.equal(buf, want)
+    c.check(buf)
 
 
 @pytest.mark.parametrize("rows", [100, 50000])
