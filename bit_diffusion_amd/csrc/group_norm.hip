@@ -34,7 +34,12 @@ namespace {
 constexpr int kSplitThreads = 256;
 constexpr int kChunk = 8;         // rows of a thread's chunk in the statistics,
 constexpr int kApply = 4;         // and in the launch that only normalises
-constexpr int kOneVectors = 8192; // vectors of a slab in the one launch, at most
+// The one launch: vectors of a slab, at most (1 x 2048 x 256 channels, 8192 vectors: 6.8 us, in
+// two launches 8.6; 2 x 2048 x 320 fp32, 10240: 14.8 us, 9.3), and vectors that all its
+// workgroups read (2 x 1024 x 640, 0.8 million: 8.9 us, in two launches 10.9; 8 images, 3.3
+// million: 18.5 us, 14.7).
+constexpr int kOneVectors = 8192;
+constexpr int64_t kOneReads = 1 << 20;
 constexpr int64_t kStreamBytes = (int64_t)32 << 20;   // x that the L2s do not hold
 constexpr int kMaxTiles = 256;    // row tiles of an image
 constexpr int kWide = 512;        // channels of the widest slab (64 vectors of 8)
@@ -376,6 +381,9 @@ struct GroupJoin {
     }
 };
 
+// Bound by the launch, the latency of its loads and the joins: 2 x 64 x 1280 channels 4.6 us in a
+// graph, 2 x 1024 x 640 8.9 us.
+//
 // One launch: workgroup (tile, slab, image) normalises R rows a thread, which it keeps, and takes
 // the statistics of the whole slab, kChunk rows a thread at a time, in the same order as every
 // other workgroup of the slab, so that all get the same ones.
@@ -424,6 +432,9 @@ __global__ __launch_bounds__(BD) void norm_one_kernel(Shape p) {
     });
 }
 
+// Bound by memory: 65536 x 512 channels 13 us (5.2 TB/s), 262144 x 256 channels of fp32 52 us
+// (5.2 TB/s).
+//
 // Two launches, the first: (mean, M2) of each group (or part of one) of a row tile to
 // work[b][group][part * tiles + tile].
 template <int VEC, bool XBF, Span SPAN, int R>
@@ -448,7 +459,9 @@ __global__ __launch_bounds__(kSplitThreads) void norm_stats_kernel(Shape p) {
 }
 
 // The second: the tiles are taken in the other order, the last ones read being the likeliest
-// in the caches, and out goes past them where x is large (STREAM), to leave them to x.
+// in the caches, and out goes past them where x is large (STREAM), to leave them to x.  Bound by
+// memory: 65536 x 512 channels 22 us (6.1 TB/s, part of x from the caches), 262144 x 256 channels
+// of fp32 to bf16 65 us (6.2 TB/s).
 template <int VEC, bool XBF, int R, bool STREAM>
 __global__ __launch_bounds__(kSplitThreads) void norm_apply_kernel(Shape p) {
     __shared__ float stat[2][kWide];
@@ -551,8 +564,8 @@ Shape plan(const GroupNormArgs& a, int v, int least) {
     return p;
 }
 
-
-// The cut of the two launches: about 1024 workgroups, each at least one chunk.
+// The cut of the two launches: about 1024 workgroups, each at least one chunk (2 x 65536 x 256
+// channels: 38.8 us; with 512 38.9, with 2048 43.6).
 Shape split_plan(const GroupNormArgs& a, int v) {
     // slabs of 64 channels make whole cache lines (33.5 million values: 47 us, with 32 61 us), of 32
     // more workgroups (1.3 million: 12.1 us, with 64 12.5 us)
@@ -589,13 +602,17 @@ void one(Shape p, hipStream_t st) {
 
 template <int VEC, bool XBF, Span SPAN>
 void run(const GroupNormArgs& a, hipStream_t st) {
+    // slabs of 4 vectors or more (2 x 256 x 1280 channels: 6.1 us, of 8 6.9 us)
     const Shape p = plan(a, VEC, 4 * VEC);
-    const int64_t vectors = p.vpt * a.rows;                  // of a slab
-    const int lanes = 256 / p.vpt;
-    const bool few = vectors <= 256 || vectors * p.slabs * a.B <= 256 * 256;
+    const int64_t vectors = p.vpt * a.rows, all = vectors * p.slabs * a.B;   // of a slab, of x
+    // one row a thread while that takes 256 workgroups at most, else four (2 x 64 x 1280 channels:
+    // 4.6 us, with four 4.85; 8 x 64 x 1280: 5.1 us, with one 5.4)
+    const bool few = vectors <= 256 || all <= 256 * 256;
+    const int own = 256 / p.vpt * (few ? 1 : 4);             // rows of a workgroup
+    const int64_t tiles = (a.rows + own - 1) / own;          // each reads the whole slab
     // in place, a slab's second workgroup would overwrite rows that the first still reads
-    const bool alone = a.x != a.out || a.rows <= lanes * (few ? 1 : 4);
-    if (p.parts > 1 || vectors > kOneVectors || !alone) split<VEC, XBF, SPAN>(a, st);
+    if (p.parts > 1 || vectors > kOneVectors || all * tiles > kOneReads || (a.x == a.out && tiles > 1))
+        split<VEC, XBF, SPAN>(a, st);
     else if (few) one<VEC, XBF, SPAN, 1, 256>(p, st);
     else one<VEC, XBF, SPAN, 4, 256>(p, st);
 }

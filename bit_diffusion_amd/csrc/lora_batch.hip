@@ -230,28 +230,33 @@ __device__ __forceinline__ uint4 keep_first(uint4 v, int live) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Workgroup `id` of a grid of tiles x inner: consecutive workgroups go to the 8 XCDs in turn,
-// so with per > 0 XCD x takes tiles x per to (x + 1) per - 1, each with all its inner parts:
-// rows of one segment, hence its adapter, stay in one XCD's L2.  per = 0: tiles in order.
-__device__ __forceinline__ void tile_of(int id, int per, int inner, int& tile, int& part) {
-    const int l = per > 0 ? id >> 3 : id;
+// Workgroup `id` of a grid of tiles x inner.  Consecutive workgroups go to the 8 XCDs in turn.
+// DEAL: the tiles go to the XCDs in turn, each with all its inner parts, which read the same rows
+// of x, so these come to one L2 (2048 x 3072, rank 128: 28.9 us in all, 30.0 without).  The
+// up-projection goes in order, neighbours on neighbouring columns of out: 600 x 4096, rank 128:
+// 17.9 us in all, dealt 19.8; ranges of neighbouring tiles to an XCD cost most, 16384 x 4096 at
+// rank 32 105 us for 95.
+template <bool DEAL>
+__device__ __forceinline__ void tile_of(int id, int inner, int& tile, int& part) {
+    const int l = DEAL ? id >> 3 : id;
     tile = l / inner;
     part = l - tile * inner;
-    if (per > 0) tile += (id & 7) * per;
+    if (DEAL) tile = tile * 8 + (id & 7);
 }
 
 // Down-projection of a tile of 16 rows, RB rank blocks: the W waves take the steps of K in turn
 // and their sums are added in wave order through LDS.  16 waves of one step at a time (64
 // registers) leave room for a second workgroup on the CU, which the few tiles past 256 need:
-// 4096 x 3072, rank 16: 10.7 us; 12.9 with two steps at a time and one workgroup a CU.
+// 4096 x 3072, rank 16: 10.5 us (2.4 TB/s of x); 12.9 with two steps at a time and one workgroup
+// a CU.  Bound by the latency of its few steps and the line look-ups of x and A.
 template <int RB, int W, int U>
-__global__ __launch_bounds__(W * 64) void lora_down_kernel(LoraBatchArgs a, int per, int inner) {
+__global__ __launch_bounds__(W * 64) void lora_down_kernel(LoraBatchArgs a, int inner) {
     constexpr int kSums = W * RB * 64, kStage = W * 256;
     static_assert(kSums * 16 <= 65536 && kStage * 16 <= 65536, "64 KB of LDS");
     __shared__ uint4 lds[kSums > kStage ? kSums : kStage];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, q = lane >> 4, r16 = lane & 15;
     int tile, part;
-    tile_of(blockIdx.x, per, inner, tile, part);
+    tile_of<true>(blockIdx.x, inner, tile, part);
     const Tile t = find_tile<1>(a, tile);
     // offsets that break the rules may make more blocks than there is room for
     if (t.rows == 0 || t.block >= a.max_blocks) return;
@@ -292,14 +297,13 @@ __global__ __launch_bounds__(W * 64) void lora_down_kernel(LoraBatchArgs a, int 
 // elements apart, a distance that falls on few memory channels, and workgroups that walk K in
 // step would all ask the same ones.
 template <int TB, int NRB, int RW, int KW, int D, int OCC>
-__global__ __launch_bounds__((TB / RW) * (NRB / KW) * 64, OCC) void lora_down_wide_kernel(LoraBatchArgs a, int per,
-                                                                                          int inner) {
+__global__ __launch_bounds__((TB / RW) * (NRB / KW) * 64, OCC) void lora_down_wide_kernel(LoraBatchArgs a, int inner) {
     constexpr int kWaves = (TB / RW) * (NRB / KW), kRows = 16 * (TB + NRB), kSet = kWaves * 4, kLoads = kRows / kSet;
     static_assert(kRows % kSet == 0 && kSet % 16 == 0, "whole loads");
     __shared__ uint4 lds[kRows * 16];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, q = lane >> 4, r16 = lane & 15, K = a.K;
     int tile, part;
-    tile_of(blockIdx.x, per, inner, tile, part);
+    tile_of<true>(blockIdx.x, inner, tile, part);
     const Tile t = find_tile<TB>(a, tile);
     if (t.rows == 0) return;
     const Adapter ad = adapter_of(a, t.id);
@@ -543,6 +547,9 @@ struct UpTile {
     }
 };
 
+// Up-projection, bound by memory (base and out once) and, at rank 128, by the registers that t
+// takes: 16384 x 4096 at rank 16 takes 48 us (5.6 TB/s), at rank 128 94 us (3 TB/s).
+//
 // A workgroup's rows x `blocks` blocks of 64 CB columns, 16 CB columns to each of 4 waves: t
 // stays in registers; base is loaded two blocks ahead, B as soon as the block before has its own
 // in LDS.
@@ -588,11 +595,11 @@ __device__ __forceinline__ void up_blocks(const LoraBatchArgs& a, const Tile& t,
 
 // Up-projection of a tile of 16 RBE rows, `span` blocks of columns.
 template <int RBE, int CB, int NB, bool BF16>
-__global__ __launch_bounds__(256) void lora_up_kernel(LoraBatchArgs a, int per, int inner, int span) {
+__global__ __launch_bounds__(256) void lora_up_kernel(LoraBatchArgs a, int inner, int span) {
     using Up = UpTile<RBE, CB, NB, BF16>;
     __shared__ uint4 lds[4][Up::kLds];
     int tile, part;
-    tile_of(blockIdx.x, per, inner, tile, part);
+    tile_of<false>(blockIdx.x, inner, tile, part);
     const Tile t = find_tile<RBE>(a, tile);
     if (t.rows == 0) return;
     const int first = part * span, w = threadIdx.x >> 6;
@@ -620,8 +627,9 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraBatchArgs a, int per, 
 // Both products for a tile of 16 rows x 256 columns, 32 columns to each of 8 waves: the waves
 // share the steps of K, and the rows' t goes through LDS.  Every workgroup of a tile reads its
 // rows and A again (from the L2s), which costs less than a second launch while they are few
-// and fit one round of CUs: 2 rows, 3072 -> 18432, rank 16: 7.5 us, two launches 11; 1237 rows,
-// rank 64, in 332 workgroups: 15.0 us, in two launches 12.8.
+// and fit one round of CUs: 2 rows, 3072 -> 18432, rank 16: 6.7 us, two launches 8.3; 1237 rows,
+// rank 64, in 332 workgroups: 15.0 us, in two launches 12.8.  Bound by the launch and the
+// latency of K / 1024 steps.
 template <int RB, bool BF16, int U>
 __global__ __launch_bounds__(512) void lora_few_rows_kernel(LoraBatchArgs a, int inner) {
     constexpr int W = 8, NB = RB / 2;
@@ -633,7 +641,7 @@ __global__ __launch_bounds__(512) void lora_few_rows_kernel(LoraBatchArgs a, int
     __shared__ uint4 terms[ops_of(NB, BF16)][Up::kBlocks][64];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, q = lane >> 4, r16 = lane & 15;
     int tile, part;
-    tile_of(blockIdx.x, 0, inner, tile, part);
+    tile_of<false>(blockIdx.x, inner, tile, part);
     const Tile t = find_tile<1>(a, tile);
     if (t.rows == 0) return;
     const int c0 = part * kColTile + w * 32;
@@ -679,30 +687,25 @@ int64_t most_tiles(int64_t M, int n, int tm) { return std::min<int64_t>((M + (in
 // Blocks of 32 ranks of the pool (0: 16 ranks).
 int rank_blocks(int R) { return R <= 16 ? 0 : R <= 32 ? 1 : R <= 64 ? 2 : 4; }
 
-// Tiles a XCD takes (tile_of): with few tiles they are dealt over all XCDs instead.
-int per_xcd(int64_t tiles) { return tiles >= 64 ? (int)((tiles + 7) / 8) : 0; }
-unsigned grid_of(int64_t tiles, int inner) {
-    const int per = per_xcd(tiles);
-    return (unsigned)((per > 0 ? 8 * per : tiles) * inner);
-}
+unsigned grid_of(int64_t tiles, int inner, bool deal) { return (unsigned)((deal ? (tiles + 7) / 8 * 8 : tiles) * inner); }
 
 template <int RB, int W, int U>
 void down(const LoraBatchArgs& a, hipStream_t st) {
     const int64_t tiles = most_tiles(a.M, a.n_segments, 16);
     const int inner = ((a.nb == 0 ? 1 : a.nb * 2) + RB - 1) / RB;
-    hipLaunchKernelGGL((lora_down_kernel<RB, W, U>), dim3(grid_of(tiles, inner)), dim3(W * 64), 0, st, a, per_xcd(tiles),
-                       inner);
+    hipLaunchKernelGGL((lora_down_kernel<RB, W, U>), dim3(grid_of(tiles, inner, true)), dim3(W * 64), 0, st, a, inner);
 }
 
-// Rows from which A is staged once a workgroup (4096 x 1024, rank 64, fp32: 34.6 us in all, 38.9 without).
+// Rows from which A is staged once a workgroup: 4096 x 1024, rank 64, fp32: 34.6 us in all, 38.9
+// without; 3500 x 3072, rank 64: 31.4 us with, 24.9 without (its tiles leave CUs idle).
 constexpr int64_t kWideRows = 4096;
 
 template <int TB, int NRB, int RW, int KW, int D, int OCC>
 void down_wide(const LoraBatchArgs& a, hipStream_t st) {
     const int64_t tiles = most_tiles(a.M, a.n_segments, TB * 16);
     const int inner = (a.nb * 2 + NRB - 1) / NRB;
-    hipLaunchKernelGGL((lora_down_wide_kernel<TB, NRB, RW, KW, D, OCC>), dim3(grid_of(tiles, inner)),
-                       dim3((TB / RW) * (NRB / KW) * 64), 0, st, a, per_xcd(tiles), inner);
+    hipLaunchKernelGGL((lora_down_wide_kernel<TB, NRB, RW, KW, D, OCC>), dim3(grid_of(tiles, inner, true)),
+                       dim3((TB / RW) * (NRB / KW) * 64), 0, st, a, inner);
 }
 
 void launch_down(const LoraBatchArgs& a, hipStream_t st) {
@@ -718,13 +721,14 @@ void launch_down(const LoraBatchArgs& a, hipStream_t st) {
         else tall == 4 ? down_wide<4, 4, 2, 1, 3, 2>(a, st) : down_wide<6, 4, 3, 1, 3, 2>(a, st);
         return;
     }
-    // rank blocks of a workgroup: as many as leave a workgroup for each of 256 CUs
     const int64_t tiles = most_tiles(a.M, a.n_segments, 16);
+    // two rank blocks to a workgroup halve the reads of x where there are workgroups enough (two
+    // and one, us in all: rank 32: 2000 rows of 3072 16.1 and 15.5, 16000 75 and 82; rank 64: 300
+    // rows of 4096 12.9 and 12.3, 1000 of 3072 15.1 and 16.3; rank 128: 64 rows 11.4 and 10.2,
+    // 600 17.5 and 21; four at 3500 47.7, two 45.0)
     const int rb = a.R / 16;
-    auto fills = [&](int per) { return tiles * ((rb + per - 1) / per) >= 256; };
-    if (rb == 1 || !fills(2)) down<1, 16, 1>(a, st);
-    else if (rb == 2 || !fills(4)) down<2, 8, 1>(a, st);
-    else down<4, 16, 1>(a, st);
+    if (rb >= 2 && tiles * ((rb + 1) / 2) >= (rb == 2 ? 256 : 128)) down<2, 8, 1>(a, st);
+    else down<1, 16, 1>(a, st);
 }
 
 template <int RBE, int CB, int NB, bool BF16>
@@ -737,8 +741,8 @@ void up(const LoraBatchArgs& a, hipStream_t st) {
     int span = 1;
     while (span < kMost && span < blocks && tiles * ((blocks + 2 * span - 1) / (2 * span)) >= 1024) span *= 2;
     const int inner = (blocks + span - 1) / span;
-    hipLaunchKernelGGL((lora_up_kernel<RBE, CB, NB, BF16>), dim3(grid_of(tiles, inner)), dim3(256), 0, st, a,
-                       per_xcd(tiles), inner, span);
+    hipLaunchKernelGGL((lora_up_kernel<RBE, CB, NB, BF16>), dim3(grid_of(tiles, inner, false)), dim3(256), 0, st, a,
+                       inner, span);
 }
 
 template <int RBE, bool BF16>
@@ -784,12 +788,15 @@ void launch_lora_batch(const LoraBatchArgs& args, hipStream_t st) {
     a.nb = rank_blocks(a.R);
     a.max_blocks = (int)most_tiles(a.M, a.n_segments, 16);
     const int64_t inner = (a.N + kColTile - 1) / kColTile;
-    if (a.R <= 64 && a.max_blocks * inner <= 256 && (int64_t)a.R * a.K <= 1 << 18) {
+    // one launch while A is small (4 rows, one and two launches: rank 32, K = 4096 8.1 and 9.1 us,
+    // 8192 11.8 and 11.6; rank 64, K = 2048 8.2 and 8.1, 3072 10.1 and 8.7)
+    if (a.R <= 64 && a.max_blocks * inner <= 256 && (int64_t)a.R * a.K <= (a.R <= 32 ? 1 << 18 : 1 << 17)) {
         a.bf16 ? few_rows<true>(a, st) : few_rows<false>(a, st);
         return;
     }
     launch_down(a, st);
-    // 32 rows to a workgroup where that leaves 1024 of them; t's third term for fp32 takes the
+    // 32 rows to a workgroup where that leaves 1024 of them (16384 x 4096, rank 128: 156 us in all,
+    // with 16 178; 300 x 3072, rank 32: 9.4, with 16 9.1); t's third term for fp32 takes the
     // registers of the second 16 rows (30000 x 1024, rank 64: 90 us in all, 99 with 32 rows)
     if (!a.bf16) up_rank<1, false>(a, st);
     else if ((a.M / 32) * inner >= 1024) up_rank<2, true>(a, st);
