@@ -203,3 +203,17 @@ def test_zero_sizes():
         bd.svdq_group_norm(B, rows, 64, 8, 1e-5, 0, t, 64, None, None, 0, None, None, 64, 0, 0, t, 64, None, 0)
     torch.cuda.synchronize()
     assert bool((t == 5.0).all())
+
+
+# positions whose offsets pass 2^31 elements: one launch, two, and single elements
+@pytest.mark.parametrize("B,rows,C,G", [(1, 40, 64, 8), (1, 20000, 64, 8), (2, 3000, 33, 3)])
+def test_offsets_past_32_bits(B, rows, C, G):
+    c = Case(70, B, rows, C, G, mod=F32)
+    c.xs = c.os = ((1 << 31) // (B * rows - 1) // 8 + 1) * 8
+    n = (B * rows - 1) * c.xs + C
+    assert n > 1 << 31
+    x, out = (torch.empty(n, dtype=BF, device=DEV).as_strided((B * rows, C), (c.xs, 1)) for _ in range(2))
+    x.copy_(c.x)
+    c.call(x=x, out=out)
+    torch.cuda.synchronize()
+    c.check(out)

@@ -293,3 +293,42 @@ def test_offsets_that_break_the_rules_stay_inside(starts):
     w = c.wout.clone()
     w[:, :96] = 9.0
     assert bool((w == 9.0).all())
+
+
+def far(t, stride):
+    """t's rows `stride` elements apart in a buffer of 2^31 elements or more."""
+    buf = torch.empty((t.shape[0] - 1) * stride + t.shape[1], dtype=t.dtype, device=DEV)
+    assert buf.numel() > 1 << 31
+    view = buf.as_strided(t.shape, (stride, 1))
+    view.copy_(t)
+    return view
+
+
+# rows and pool entries whose offsets pass 2^31 elements give what near ones give, bit for bit
+@pytest.mark.parametrize("M,K,N,R", [(40, 64, 72, 16), (600, 128, 130, 64), (4200, 64, 40, 64)])
+def test_offsets_past_32_bits(M, K, N, R):
+    c = Case(70 + R, M, K, N, R, cuts(M // 3, M - M // 3), [0, 2])
+    want = c.call().clone()
+    stride = ((1 << 31) // (M - 1) // 8 + 1) * 8
+    x, base, out = (far(t.to(DEV), stride) for t in (c.x, c.base, c.out))
+    bd.svdq_lora_batch(M, K, N, R, c.S, 2, x, x.stride(0), c.ddown, c.dup, c.dalphas, None, c.dstarts, c.dids, base,
+                       stride, 0, bd.SVDQ_DT_BF16, out, stride, c.ws, c.nb)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_pools_past_32_bits():
+    S, R, K, N = 4200, 128, 4096, 4096
+    c = Case(71, 40, K, N, R, cuts(15, 25), [0, 1], S=2)
+    want = c.call().clone()
+    down = torch.empty(S, R, K, dtype=torch.bfloat16, device=DEV)
+    up = torch.empty(S, N, R, dtype=torch.bfloat16, device=DEV)
+    assert down.numel() > 1 << 31 and up.numel() > 1 << 31
+    alphas = torch.empty(S, dtype=torch.float32, device=DEV)
+    for i, s in ((0, S - 1), (1, S - 2)):
+        down[s], up[s], alphas[s] = c.ddown[i], c.dup[i], c.dalphas[i]
+    c.ddown, c.dup, c.dalphas, c.S = down, up, alphas, S
+    c.dids = torch.tensor([S - 1, S - 2], dtype=torch.int32, device=DEV)
+    got = c.call(out=c.out.to(DEV))
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
