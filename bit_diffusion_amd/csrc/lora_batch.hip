@@ -22,10 +22,8 @@
 // slots exclusive-ored with the row so that neither side meets a bank twice.  t itself is
 // kept in operand order in the workspace.
 //
-// t keeps fp32 accuracy through the bf16 MFMA: it is split into bf16 terms h = bf16(t),
-// m = bf16(t - h), l = bf16(t - h - m) which multiply the same operand.  Two terms
-// (off by 2^-16 of t at most) stand far below the half step 2^-8 of a bf16 output; a fp32
-// output takes three (2^-24, fp32's own half step).
+// t passes the bf16 MFMA as it is: its 24 significant bits are cut into three bf16 terms of 8
+// which multiply the same operand, for a bf16 output too (base and the delta may cancel).
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -178,32 +176,36 @@ __device__ __forceinline__ void down_steps(const LoraBatchArgs& a, const Tile& t
     }
 }
 
-// bf16 terms of v: the first is v rounded (to the largest finite value where rounding would
-// overflow), the next ones the rests; an infinity or NaN stands in the first term alone.
+constexpr uint32_t kHalf = 0x80;   // a step of a bf16's exponent
+
+// bf16 terms of v: its first 8 significant bits, the next 8 and the last, cut and not rounded, so
+// that they have v's sign and their sum is v (bits below 2^-133 apart).  In the place of a term
+// whose bits are all zero stand halves of the one before it: an infinite operand then meets no
+// zero, and gives the infinity that v itself gives (from |v| = 2^-100 on, where halves are exact).
 __device__ __forceinline__ void split_terms(float v, uint32_t (&t)[3]) {
-    uint32_t h = f32_to_bf16(v);
-    const bool finite = (__float_as_uint(v) & 0x7F800000u) != 0x7F800000u;
-    if (finite && (h & 0x7FFFu) == 0x7F80u) h -= 1;
-    t[0] = h;
-    float rest = v - bf16_to_f32(h);
-#pragma unroll
-    for (int i = 1; i < 3; ++i) {
-        t[i] = finite ? f32_to_bf16(rest) : 0u;
-        rest -= bf16_to_f32(t[i]);
-    }
+    const uint32_t u = __float_as_uint(v), h = (u >> 16) | (v != v ? 0x40u : 0u);   // a NaN keeps a bit
+    const float rest = v - __uint_as_float(u & 0xFFFF0000u);
+    const uint32_t m = __float_as_uint(rest) >> 16;
+    const uint32_t l = __float_as_uint(rest - __uint_as_float(m << 16)) >> 16;
+    const bool no_m = (m & 0x7FFFu) == 0, no_l = (l & 0x7FFFu) == 0;
+    const bool cut_h = no_m && (h & 0x7FFFu) >= 3 * kHalf, cut_m = !no_m && no_l && (m & 0x7FFFu) >= 2 * kHalf;
+    const uint32_t half = h - kHalf, quarter = half - kHalf, half_m = m - kHalf;
+    t[0] = cut_h ? half : h;
+    t[1] = cut_h ? (no_l ? quarter : half) : cut_m ? half_m : m;
+    t[2] = cut_h && no_l ? quarter : cut_m ? half_m : l;
+    if ((u & 0x7F800000u) == 0x7F800000u) t[0] = t[1] = t[2] = h;   // an infinity or a NaN: all three
 }
 
 // Ranks of the up-projection go in NB blocks of 32 (16 ranks in all: NB = 0, one half block).
 // Every block of the instantiation is multiplied, with zeros at and past the adapter's rank.
 constexpr int blocks_of(int NB) { return NB == 0 ? 1 : NB; }
 // Operands of a block of 16 rows' t: one for each term; in the half block the first holds the
-// first term in lanes q = 0, 1 and the second in q = 2, 3, the other the third and zeros.
-constexpr int ops_of(int NB, bool bf16) { return NB == 0 ? (bf16 ? 1 : 2) : (bf16 ? 2 : 3); }
+// first term in lanes q = 0, 1 and the second in q = 2, 3, the other a half of the third in both.
+constexpr int ops_of(int NB) { return NB == 0 ? 2 : 3; }
 
 // alpha times ranks j0 to j0 + 3 of row r16, `live` of them below the rank, to their places in
 // the operands `to` [ops][blocks][64 lanes] (blocks = 0: the half block).
-__device__ __forceinline__ void put_terms(uint2* to, int blocks, bool bf16, int j0, int r16, f32x4 v, float alpha,
-                                          int live) {
+__device__ __forceinline__ void put_terms(uint2* to, int blocks, int j0, int r16, f32x4 v, float alpha, int live) {
     uint32_t t[4][3];
 #pragma unroll
     for (int e = 0; e < 4; ++e) split_terms(e < live ? alpha * v[e] : 0.f, t[e]);
@@ -212,13 +214,21 @@ __device__ __forceinline__ void put_terms(uint2* to, int blocks, bool bf16, int 
     for (int n = 0; n < 3; ++n) {
         const uint2 w = make_uint2(t[0][n] | (t[1][n] << 16), t[2][n] | (t[3][n] << 16));
         if (blocks > 0) {
-            if (n < 2 || !bf16) to[(n * blocks + (j0 >> 5)) * 128 + at] = w;
+            to[(n * blocks + (j0 >> 5)) * 128 + at] = w;
         } else if (n < 2) {
             to[n * 64 + at] = w;
-        } else if (!bf16) {
-            to[128 + at] = w;
-            to[192 + at] = make_uint2(0, 0);
         }
+    }
+    if (blocks == 0) {
+        uint32_t half[4], rest[4];   // halves but for the least values, which stand whole in one place
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool cut = (t[e][2] & 0x7FFFu) >= 2 * kHalf;
+            half[e] = cut ? t[e][2] - kHalf : t[e][2];
+            rest[e] = cut ? half[e] : 0u;
+        }
+        to[128 + at] = make_uint2(half[0] | (half[1] << 16), half[2] | (half[3] << 16));
+        to[192 + at] = make_uint2(rest[0] | (rest[1] << 16), rest[2] | (rest[3] << 16));
     }
 }
 
@@ -273,7 +283,7 @@ __global__ __launch_bounds__(W * 64) void lora_down_kernel(LoraBatchArgs a, int 
         for (int j = 0; j < RB; ++j) red[(w * RB + j) * 64 + lane] = acc[j];
         __syncthreads();
     }
-    const int ranks = a.nb == 0 ? 16 : a.nb * 32, ops = a.nb == 0 ? 2 : 3;
+    const int ranks = a.nb == 0 ? 16 : a.nb * 32;
     for (int b = w; b < RB; b += W) {
         const int j0 = (rb0 + b) * 16 + q * 4;
         if (j0 >= ranks) continue;
@@ -282,7 +292,7 @@ __global__ __launch_bounds__(W * 64) void lora_down_kernel(LoraBatchArgs a, int 
 #pragma unroll
             for (int o = 0; o < W; ++o) v += red[(o * RB + b) * 64 + lane];
         }
-        put_terms((uint2*)a.work + (int64_t)t.block * ops * blocks_of(a.nb) * 128, a.nb, a.bf16 != 0, j0, r16, v, ad.alpha,
+        put_terms((uint2*)a.work + (int64_t)t.block * ops_of(a.nb) * blocks_of(a.nb) * 128, a.nb, j0, r16, v, ad.alpha,
                   ad.rank - j0);
     }
 }
@@ -381,15 +391,19 @@ __global__ __launch_bounds__((TB / RW) * (NRB / KW) * 64, OCC) void lora_down_wi
         for (int j = 0; j < KW; ++j) {
             const int at = (rb0 + j0 + j) * 16 + q * 4;
             if ((i0 + i) * 16 < t.rows && at < ranks && t.block + i0 + i < a.max_blocks)
-                put_terms((uint2*)a.work + (int64_t)(t.block + i0 + i) * 3 * a.nb * 128, a.nb, a.bf16 != 0, at, r16,
-                          acc[i][j], ad.alpha, ad.rank - at);
+                put_terms((uint2*)a.work + (int64_t)(t.block + i0 + i) * 3 * a.nb * 128, a.nb, at, r16, acc[i][j], ad.alpha,
+                          ad.rank - at);
         }
 }
 
 // A wave's 16 RBE rows x 16 CB columns of out.
 template <int RBE, int CB, int NB, bool BF16>
 struct UpTile {
-    static constexpr int kOps = ops_of(NB, BF16), kBlocks = blocks_of(NB);
+    static constexpr int kOps = ops_of(NB), kBlocks = blocks_of(NB);
+    // operands of t in registers; the last one's in LDS where that makes room for another wave a
+    // SIMD (16384 x 4096 at rank 32 96 us in all, 100 with it in registers; 8192 x 1024 at rank
+    // 128, fp32, 37 and 39; rank 16 no less, 8192 x 3072 at rank 64 61 and 60)
+    static constexpr int kHeld = (NB == 1 && CB == 4) || (NB == 4 && !BF16) ? kOps - 1 : kOps;
     static constexpr int kPer = BF16 ? 8 : 4;                 // columns of a 16-byte piece
     static constexpr int kLanes = 16 * CB / kPer;             // pieces, and lanes, of a row
     static constexpr int kPieces = RBE * 16 * kLanes / 64;    // a lane's pieces
@@ -442,28 +456,30 @@ struct UpTile {
     }
 
     // acc = t B^T, lane (q, r16) with columns 16 c + 4 q to 16 c + 4 q + 3 of row 16 i + r16
-    // (B is the MFMA's row operand)
-    static __device__ __forceinline__ void products(const uint4* lds, const uint4 (&tm)[RBE][kOps][kBlocks],
-                                                    f32x4 (&acc)[RBE][CB]) {
+    // (B is the MFMA's row operand; low: t's last operand, [RBE][kBlocks][64], where it is in LDS)
+    static __device__ __forceinline__ void products(const uint4* lds, const uint4 (&tm)[RBE][kHeld][kBlocks],
+                                                    const uint4* low, f32x4 (&acc)[RBE][CB]) {
         const int lane = threadIdx.x & 63, q = lane >> 4, r16 = lane & 15;
 #pragma unroll
         for (int i = 0; i < RBE; ++i)
 #pragma unroll
             for (int c = 0; c < CB; ++c) acc[i][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
+        for (int b = 0; b < kBlocks; ++b) {
+            uint4 last[RBE];
+#pragma unroll
+            for (int i = 0; i < RBE; ++i) last[i] = kHeld < kOps ? low[(i * kBlocks + b) * 64 + lane] : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int c = 0; c < CB; ++c) {
                 const int n = c * 16 + r16, j = NB == 0 ? q & 1 : b * 4 + q;
                 const uint4 m = lds[n * kChunks + (j ^ (n / kSpread % kChunks))];
 #pragma unroll
                 for (int o = 0; o < kOps; ++o) {
-                    // the half block's zeros must not meet an infinite B
-                    const uint4 mo = only_if(NB > 0 || o == 0 || q < 2, m);
 #pragma unroll
-                    for (int i = 0; i < RBE; ++i) acc[i][c] = mfma16(mo, tm[i][o][b], acc[i][c]);
+                    for (int i = 0; i < RBE; ++i) acc[i][c] = mfma16(m, o < kHeld ? tm[i][o % kHeld][b] : last[i], acc[i][c]);
                 }
             }
+        }
     }
 
     static __device__ __forceinline__ int slot(int row, int chunk) {
@@ -548,14 +564,14 @@ struct UpTile {
 };
 
 // Up-projection, bound by memory (base and out once) and, at rank 128, by the registers that t
-// takes: 16384 x 4096 at rank 16 takes 50 us (5.3 TB/s), at rank 128 90 us (3 TB/s).
+// takes: 16384 x 4096 at rank 16 takes 52 us (5.2 TB/s), at rank 128 97 us (2.8 TB/s).
 //
 // A workgroup's rows x `blocks` blocks of 64 CB columns, 16 CB columns to each of 4 waves: t
 // stays in registers; base is loaded two blocks ahead, B as soon as the block before has its own
 // in LDS.
 template <int RBE, int CB, int NB, bool BF16>
 __device__ __forceinline__ void up_blocks(const LoraBatchArgs& a, const Tile& t, const Adapter& ad, int first,
-                                          int blocks, uint4* lds) {
+                                          int blocks, uint4* lds, uint4* low) {
     using Up = UpTile<RBE, CB, NB, BF16>;
     constexpr int D = 2;
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -566,17 +582,23 @@ __device__ __forceinline__ void up_blocks(const LoraBatchArgs& a, const Tile& t,
     for (int d = 0; d < D; ++d)
         if (d < blocks) Up::load_base(a, t, col(d), base[d]);
     u.load_up(a, ad, col(0));
-    uint4 tm[RBE][Up::kOps][Up::kBlocks];
-    const int wb = blocks_of(a.nb), ops = a.nb == 0 ? 2 : 3;
+    uint4 tm[RBE][Up::kHeld][Up::kBlocks];
+    const int wb = blocks_of(a.nb), ops = ops_of(a.nb);
 #pragma unroll
     for (int i = 0; i < RBE; ++i) {
         const uint4* src = (const uint4*)a.work +
                            (int64_t)min(t.block + (i * 16 < t.rows ? i : 0), a.max_blocks - 1) * ops * wb * 64 + lane;
 #pragma unroll
-        for (int o = 0; o < Up::kOps; ++o)
+        for (int o = 0; o < Up::kHeld; ++o)
 #pragma unroll
             for (int b = 0; b < Up::kBlocks; ++b) tm[i][o][b] = src[(o * wb + b) * 64];
+        if constexpr (Up::kHeld < Up::kOps) {
+#pragma unroll
+            for (int b = 0; b < Up::kBlocks; ++b)
+                if (((i * Up::kBlocks + b) & 3) == w) low[(i * Up::kBlocks + b) * 64 + lane] = src[(Up::kHeld * wb + b) * 64];
+        }
     }
+    if constexpr (Up::kHeld < Up::kOps) __syncthreads();
     for (int b = 0; b < blocks; b += D) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
@@ -585,7 +607,7 @@ __device__ __forceinline__ void up_blocks(const LoraBatchArgs& a, const Tile& t,
             u.load_up(a, ad, col(min(b + d + 1, blocks - 1)));
             f32x4 acc[RBE][CB];
             float y[Up::kPieces][Up::kPer];
-            Up::products(lds, tm, acc);
+            Up::products(lds, tm, low, acc);
             Up::turn(lds, acc, y);
             Up::store(a, t, col(b + d), base[d], y);
             if (b + d + D < blocks) Up::load_base(a, t, col(b + d + D), base[d]);
@@ -593,11 +615,15 @@ __device__ __forceinline__ void up_blocks(const LoraBatchArgs& a, const Tile& t,
     }
 }
 
-// Up-projection of a tile of 16 RBE rows, `span` blocks of columns.
+// Up-projection of a tile of 16 RBE rows, `span` blocks of columns.  WAVES: waves a SIMD that the
+// registers must leave room for (32 rows, 32 columns a wave, rank 16: 97 registers leave room for
+// 4, one less for 5: 4096 x 3072 21.6 us in all, 22.3 with 4; tighter bounds elsewhere spill and
+// cost time).
+constexpr int up_waves(int RBE, int CB, int NB) { return RBE == 2 && CB == 2 && NB == 0 ? 5 : 1; }
 template <int RBE, int CB, int NB, bool BF16>
-__global__ __launch_bounds__(256) void lora_up_kernel(LoraBatchArgs a, int inner, int span) {
+__global__ __launch_bounds__(256, up_waves(RBE, CB, NB)) void lora_up_kernel(LoraBatchArgs a, int inner, int span) {
     using Up = UpTile<RBE, CB, NB, BF16>;
-    __shared__ uint4 lds[4][Up::kLds];
+    __shared__ uint4 lds[4][Up::kLds], low[Up::kHeld < Up::kOps ? RBE * Up::kBlocks * 64 : 1];
     int tile, part;
     tile_of<false>(blockIdx.x, inner, tile, part);
     const Tile t = find_tile<RBE>(a, tile);
@@ -617,11 +643,11 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraBatchArgs a, int inner
     }
     if constexpr (NB > 2) {
         if (ad.rank <= 64) {
-            up_blocks<RBE, CB, 2, BF16>(a, t, ad, first, blocks, lds[w]);
+            up_blocks<RBE, CB, 2, BF16>(a, t, ad, first, blocks, lds[w], low);
             return;
         }
     }
-    up_blocks<RBE, CB, NB, BF16>(a, t, ad, first, blocks, lds[w]);
+    up_blocks<RBE, CB, NB, BF16>(a, t, ad, first, blocks, lds[w], low);
 }
 
 // Both products for a tile of 16 rows x 256 columns, 32 columns to each of 8 waves: the waves
@@ -638,7 +664,7 @@ __global__ __launch_bounds__(512) void lora_few_rows_kernel(LoraBatchArgs a, int
     static_assert(kStage >= RB * 64, "the sums take the operands' place");
     __shared__ uint4 lds[W][kStage];
     f32x4* red = (f32x4*)lds;
-    __shared__ uint4 terms[ops_of(NB, BF16)][Up::kBlocks][64];
+    __shared__ uint4 terms[Up::kOps][Up::kBlocks][64];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, q = lane >> 4, r16 = lane & 15;
     int tile, part;
     tile_of<false>(blockIdx.x, inner, tile, part);
@@ -665,18 +691,18 @@ __global__ __launch_bounds__(512) void lora_few_rows_kernel(LoraBatchArgs a, int
         f32x4 v = red[w * 64 + lane];
 #pragma unroll
         for (int o = 1; o < W; ++o) v += red[(o * RB + w) * 64 + lane];
-        put_terms((uint2*)&terms[0][0][0], NB, BF16, j0, r16, v, ad.alpha, ad.rank - j0);
+        put_terms((uint2*)&terms[0][0][0], NB, j0, r16, v, ad.alpha, ad.rank - j0);
     }
     __syncthreads();
-    uint4 tm[1][Up::kOps][Up::kBlocks];
+    uint4 tm[1][Up::kHeld][Up::kBlocks];
 #pragma unroll
-    for (int o = 0; o < Up::kOps; ++o)
+    for (int o = 0; o < Up::kHeld; ++o)
 #pragma unroll
         for (int b = 0; b < Up::kBlocks; ++b) tm[0][o][b] = terms[o][b][lane];
     f32x4 out[1][2];
     float y[Up::kPieces][Up::kPer];
     u.stage_up(lds[w]);
-    Up::products(lds[w], tm, out);
+    Up::products(lds[w], tm, nullptr, out);
     Up::turn(lds[w], out, y);
     Up::store(a, t, c0, base, y);
 }
@@ -780,9 +806,9 @@ bool lora_batch_fits(int64_t M, int N, int n_segments) {
 
 int64_t lora_batch_workspace_bytes(int64_t M, int R, int n_segments) {
     if (n_segments == 0) return 0;
-    // the operands of t for an fp32 output, every block of 16 rows
+    // the operands of t, every block of 16 rows
     const int nb = rank_blocks(R);
-    return most_tiles(M, n_segments, 16) * ops_of(nb, false) * blocks_of(nb) * 1024;
+    return most_tiles(M, n_segments, 16) * ops_of(nb) * blocks_of(nb) * 1024;
 }
 
 void launch_lora_batch(const LoraBatchArgs& args, hipStream_t st) {

@@ -358,8 +358,11 @@ svdq_status svdq_merge_lora(const svdq_layer_cfg* cfg, int32_t r_lora, const voi
  *   out[m, n] = act(base[m, n] + alphas[s] sum_{j < rank_s} (sum_k x[m, k] lora_down[s, j, k])
  *                                                           lora_up[s, n, j])
  *
- * for every row m of segment i, s = seg_adapter[i].  All sums are fp32; the down-projection is
- * not rounded to 16 bits in between; the result is rounded once.
+ * for every row m of segment i, s = seg_adapter[i].  All sums are fp32; the down-projection
+ * enters the second product with all of its 24 bits, for a bf16 output too; the result is
+ * rounded once.  An infinite or NaN value in use spoils the elements that its products enter, as
+ * in fp32 arithmetic (infinity, or NaN for 0 times an infinity and for opposite infinities;
+ * NaN also where the down-projection's value at an infinite lora_up is below 2^-100).
  *
  *   x          [M, K] bf16, the linear's input (for an SVDQ layer the raw x, not smoothed),
  *              rows x_stride elements apart (x_stride >= K, a multiple of 8).
