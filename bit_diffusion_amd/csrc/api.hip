@@ -79,6 +79,11 @@ svdq_status check_ptr(const void* p, const char* name, size_t align) {
     return SVDQ_OK;
 }
 
+// As check_ptr for a buffer that may have no elements: NULL is an empty tensor's address.
+svdq_status check_buf(const void* p, const char* name, size_t align, bool empty) {
+    return empty && p == nullptr ? SVDQ_OK : check_ptr(p, name, align);
+}
+
 svdq_status check_cfg(const svdq_layer_cfg* cfg) {
     if (cfg == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "cfg is NULL");
     if (cfg->precision != SVDQ_PREC_INT4 && cfg->precision != SVDQ_PREC_NVFP4)
@@ -675,7 +680,7 @@ svdq_status svdq_lora_batch(int64_t M, int32_t K, int32_t N, int32_t max_rank, i
     SVDQ_TRY(check_act(act));
     SVDQ_TRY(check_dtype(out_dtype, "out_dtype"));
     const int64_t esz = out_dtype == SVDQ_DT_BF16 ? 2 : 4;
-    SVDQ_TRY(check_ptr(x, "x", 16));
+    SVDQ_TRY(check_buf(x, "x", 16, M == 0));
     SVDQ_TRY(check_stride(x_stride, K, "x_stride"));
     if (x_stride % 8 != 0)
         return fail(SVDQ_ERR_INVALID_ARG, "x_stride = %lld must be a multiple of 8", (long long)x_stride);
@@ -684,8 +689,8 @@ svdq_status svdq_lora_batch(int64_t M, int32_t K, int32_t N, int32_t max_rank, i
     SVDQ_TRY(check_ptr(alphas, "alphas", 4));
     if (ranks != nullptr && !aligned(ranks, 4)) return fail(SVDQ_ERR_INVALID_ARG, "ranks is not 4-byte aligned");
     SVDQ_TRY(check_ptr(seg_start, "seg_start", 4));
-    SVDQ_TRY(check_ptr(seg_adapter, "seg_adapter", 4));
-    SVDQ_TRY(check_ptr(out, "out", esz));
+    SVDQ_TRY(check_buf(seg_adapter, "seg_adapter", 4, n_segments == 0));
+    SVDQ_TRY(check_buf(out, "out", esz, M == 0));
     SVDQ_TRY(check_stride(out_stride, N, "out_stride"));
     if (base != nullptr) {
         SVDQ_TRY(check_ptr(base, "base", esz));
@@ -737,7 +742,8 @@ svdq_status svdq_group_norm(int64_t B, int64_t rows, int32_t C, int32_t groups, 
     SVDQ_TRY(check_act(act));
     const int64_t xsz = x_dtype == SVDQ_DT_BF16 ? 2 : 4, osz = out_dtype == SVDQ_DT_BF16 ? 2 : 4;
     const size_t msz = mod_dtype == SVDQ_DT_BF16 ? 2 : 4;
-    SVDQ_TRY(check_ptr(x, "x", xsz));
+    const bool none = B == 0 || rows == 0;
+    SVDQ_TRY(check_buf(x, "x", xsz, none));
     SVDQ_TRY(check_stride(x_stride, C, "x_stride"));
     if (weight != nullptr && !aligned(weight, 2)) return fail(SVDQ_ERR_INVALID_ARG, "weight is not 2-byte aligned");
     if (bias != nullptr && !aligned(bias, 2)) return fail(SVDQ_ERR_INVALID_ARG, "bias is not 2-byte aligned");
@@ -746,9 +752,9 @@ svdq_status svdq_group_norm(int64_t B, int64_t rows, int32_t C, int32_t groups, 
         if (mod_shift != nullptr) SVDQ_TRY(check_ptr(mod_shift, "mod_shift", msz));
         SVDQ_TRY(check_stride(mod_stride, C, "mod_stride"));
     }
-    SVDQ_TRY(check_ptr(out, "out", osz));
+    SVDQ_TRY(check_buf(out, "out", osz, none));
     SVDQ_TRY(check_stride(out_stride, C, "out_stride"));
-    if (x == out && (x_dtype != out_dtype || x_stride != out_stride))
+    if (x == out && x != nullptr && (x_dtype != out_dtype || x_stride != out_stride))
         return fail(SVDQ_ERR_INVALID_ARG, "x is out but their types or strides differ");
     SVDQ_TRY(check_workspace(workspace, workspace_bytes, svdq::group_norm_workspace_bytes(B, rows, C, groups)));
     SVDQ_TRY(check_current_device());

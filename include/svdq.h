@@ -389,7 +389,7 @@ svdq_status svdq_merge_lora(const svdq_layer_cfg* cfg, int32_t r_lora, const voi
  *              16-byte aligned, overwritten; calls that may overlap in time need one each.
  * K a positive multiple of 64 up to 2^24; max_rank a multiple of 16 up to 128; M up to 2^22 and
  * n_segments up to 2^16 (0 is valid and enqueues nothing), where (M / 16 + n_segments + 8)
- * ceil(N / 128) stays below 2^24.  The segments' arrays are read when the work
+ * ceil(N / 128) stays below 2^24; a buffer without elements may be NULL.  The segments' arrays are read when the work
  * runs, so a captured graph replays with what they hold then.  x, lora_down and lora_up must
  * be 16-byte aligned, base and out aligned to their type (16-byte aligned rows are faster).
  * All buffers are device memory on the current device.  Bit-reproducible from run to run. */
@@ -422,7 +422,7 @@ svdq_status svdq_lora_batch(int64_t M, int32_t K, int32_t N, int32_t max_rank, i
  *   workspace  svdq_group_norm_workspace_bytes(B, rows, C, groups) bytes at least, 16-byte
  *              aligned, overwritten; calls that may overlap in time need one each.
  * C a positive multiple of groups, up to 65536; eps positive and finite; B up to 65535; rows
- * up to 2^30 (B = 0 or rows = 0 enqueues nothing).  Buffers are aligned to their type; x and
+ * up to 2^30 (B = 0 or rows = 0 enqueues nothing; x and out may be NULL then).  Buffers are aligned to their type; x and
  * out that are 16-byte aligned with strides and C multiples of 8 are faster.  All buffers are
  * device memory on the current device.  Bit-reproducible from run to run. */
 svdq_status svdq_group_norm_workspace_bytes(int64_t B, int64_t rows, int32_t C, int32_t groups,
