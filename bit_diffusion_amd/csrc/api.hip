@@ -676,7 +676,9 @@ svdq_status svdq_lora_batch(int64_t M, int32_t K, int32_t N, int32_t max_rank, i
                             int32_t act, int32_t out_dtype, void* out, int64_t out_stride,
                             void* workspace, int64_t workspace_bytes, svdq_stream_t stream) {
     SVDQ_TRY(check_lora_batch(M, K, N, max_rank, n_segments));
-    if (n_adapters <= 0) return fail(SVDQ_ERR_INVALID_ARG, "n_adapters = %d must be positive", n_adapters);
+    if (n_adapters < 0) return fail(SVDQ_ERR_INVALID_ARG, "n_adapters = %d is negative", n_adapters);
+    if (n_adapters == 0 && (lora_down != nullptr || lora_up != nullptr || alphas != nullptr))
+        return fail(SVDQ_ERR_INVALID_ARG, "n_adapters = 0 but lora_down, lora_up or alphas is not NULL");
     SVDQ_TRY(check_act(act));
     SVDQ_TRY(check_dtype(out_dtype, "out_dtype"));
     const int64_t esz = out_dtype == SVDQ_DT_BF16 ? 2 : 4;
@@ -684,9 +686,9 @@ svdq_status svdq_lora_batch(int64_t M, int32_t K, int32_t N, int32_t max_rank, i
     SVDQ_TRY(check_stride(x_stride, K, "x_stride"));
     if (x_stride % 8 != 0)
         return fail(SVDQ_ERR_INVALID_ARG, "x_stride = %lld must be a multiple of 8", (long long)x_stride);
-    SVDQ_TRY(check_ptr(lora_down, "lora_down", 16));
-    SVDQ_TRY(check_ptr(lora_up, "lora_up", 16));
-    SVDQ_TRY(check_ptr(alphas, "alphas", 4));
+    SVDQ_TRY(check_buf(lora_down, "lora_down", 16, n_adapters == 0));
+    SVDQ_TRY(check_buf(lora_up, "lora_up", 16, n_adapters == 0));
+    SVDQ_TRY(check_buf(alphas, "alphas", 4, n_adapters == 0));
     if (ranks != nullptr && !aligned(ranks, 4)) return fail(SVDQ_ERR_INVALID_ARG, "ranks is not 4-byte aligned");
     SVDQ_TRY(check_ptr(seg_start, "seg_start", 4));
     SVDQ_TRY(check_buf(seg_adapter, "seg_adapter", 4, n_segments == 0));

@@ -822,7 +822,7 @@ void launch_lora_batch(const LoraBatchArgs& args, hipStream_t st) {
         a.bf16 ? few_rows<true>(a, st) : few_rows<false>(a, st);
         return;
     }
-    launch_down(a, st);
+    if (a.n_adapters > 0) launch_down(a, st);
     // 32 rows to a workgroup where that leaves 1024 of them (16384 x 4096, rank 128: 156 us in all,
     // with 16 178; 300 x 3072, rank 32: 9.4, with 16 9.1); t's third term for fp32 takes the
     // registers of the second 16 rows (30000 x 1024, rank 64: 90 us in all, 99 with 32 rows)

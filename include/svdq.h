@@ -369,6 +369,8 @@ svdq_status svdq_merge_lora(const svdq_layer_cfg* cfg, int32_t r_lora, const voi
  *   lora_down  [n_adapters, max_rank, K] bf16 and lora_up [n_adapters, N, max_rank] bf16: the
  *              pool, each adapter's A and B in the layout svdq_merge_lora takes.  Rows of A
  *              and columns of B at and past the adapter's rank are not used, whatever they hold.
+ *              An empty pool is n_adapters = 0 with NULL for lora_down, lora_up and alphas: no
+ *              segment has an adapter, out = act(base).
  *   alphas     [n_adapters] fp32: the adapter's scale.
  *   ranks      [n_adapters] int32 in [0, max_rank], or NULL: all max_rank.  A value outside is
  *              clamped; 0 is an adapter that adds nothing.
