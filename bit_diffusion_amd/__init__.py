@@ -61,11 +61,18 @@ def _dev_ptrs(names, tensors):
     return ptrs
 
 
+def _current_stream():
+    import torch
+    # the raw handle where this torch gives it: the Stream object around it costs 3 us a call
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None:
+        return raw(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        # torch.cuda.current_stream().cuda_stream, without the 3 us of the Stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
