@@ -31,7 +31,7 @@
 namespace svdq {
 namespace {
 
-constexpr int kSplitThreads = 256;
+constexpr int kThreads = 256;      // of every workgroup
 constexpr int kChunk = 8;         // rows of a thread's chunk in the statistics,
 constexpr int kApply = 4;         // and in the launch that only normalises
 // The one launch: vectors of a slab, at most (1 x 2048 x 256 channels, 8192 vectors: 6.8 us, in
@@ -173,24 +173,24 @@ struct Terms {
             return p == nullptr ? (kind == 0 ? 1.f : 0.f) : __uint_as_float(half ? u << 16 : u);
         }
     };
-    static __device__ __forceinline__ int channel() { return (threadIdx.x >> 8) * 64 + (threadIdx.x & 63); }
+    static __device__ __forceinline__ int channel() { return threadIdx.x & 63; }
     // starts the loads; what comes between this and put() need not wait for them
     static __device__ __forceinline__ Source load(const GroupNormArgs& a, int image, int c0, int width) {
-        const int kind = (threadIdx.x >> 6) & 3;
+        const int kind = threadIdx.x >> 6;
         Source s{kind == 0 ? a.weight : kind == 1 ? a.bias : kind == 2 ? a.mod_scale : a.mod_shift,
                  (kind < 2 ? 0 : (int64_t)image * a.mod_stride) + c0, kind, kind < 2 || a.mod_bf16 != 0, 0};
         if (s.p != nullptr && channel() < width) s.first = s.get(channel());
         return s;
     }
-    __device__ __forceinline__ void put(const Source& s, int width, int threads) {
+    __device__ __forceinline__ void put(const Source& s, int width) {
         if (channel() < width) v[s.kind][channel()] = s.value(s.first);
-        for (int ch = channel() + threads / 4; ch < width; ch += threads / 4)
+        for (int ch = channel() + kThreads / 4; ch < width; ch += kThreads / 4)
             v[s.kind][ch] = s.value(s.p == nullptr ? 0u : s.get(ch));
     }
     // v[0], v[1], v[2] become mean, A, D; cg: channels of a group in this slab
-    __device__ __forceinline__ void fold(const float* mean, const float* rstd, int width, int cg, int threads) {
+    __device__ __forceinline__ void fold(const float* mean, const float* rstd, int width, int cg) {
         const float inv = __builtin_amdgcn_rcpf((float)cg);
-        for (int ch = threadIdx.x; ch < width; ch += threads) {
+        for (int ch = threadIdx.x; ch < width; ch += kThreads) {
             const int g = quotient(ch, inv);
             const float m = 1.f + v[2][ch], A = rstd[g] * v[0][ch] * m, D = v[1][ch] * m + v[3][ch];
             v[0][ch] = mean[g];
@@ -303,11 +303,11 @@ enum Span { kWhole, kTwo, kAny };
 // groups in turn; where there are fewer groups than waves, several share a group's row lanes.
 // In the end stat[0][g] is group g's mean and stat[1][g] what `finish` makes of its M2, for every
 // thread.
-template <int VEC, Span SPAN, int BD>
+template <int VEC, Span SPAN>
 struct GroupJoin {
     static constexpr int EPV = SPAN == kWhole ? 1 : SPAN == kTwo ? 2 : VEC;
-    static constexpr int kWaves = BD / 64;
-    float n[BD * EPV], mean[BD * EPV], m2[BD * EPV];
+    static constexpr int kWaves = kThreads / 64;
+    float n[kThreads * EPV], mean[kThreads * EPV], m2[kThreads * EPV];
     float part[3][kWaves];
     float stat[2][kWide];
 
@@ -411,9 +411,9 @@ struct GroupJoin {
 // One launch: workgroup (tile, slab, image) normalises R rows a thread, which it keeps, and takes
 // the statistics of the whole slab, kChunk rows a thread at a time, in the same order as every
 // other workgroup of the slab, so that all get the same ones.
-template <int VEC, bool XBF, Span SPAN, int R, int BD>
-__global__ __launch_bounds__(BD) void norm_one_kernel(Shape p) {
-    __shared__ GroupJoin<VEC, SPAN, BD> lds;
+template <int VEC, bool XBF, Span SPAN, int R>
+__global__ __launch_bounds__(kThreads) void norm_one_kernel(Shape p) {
+    __shared__ GroupJoin<VEC, SPAN> lds;
     __shared__ Terms terms;
     const GroupNormArgs& a = p.a;
     const int tid = threadIdx.x, tile = blockIdx.y, b = blockIdx.z, rows = (int)a.rows;
@@ -434,10 +434,10 @@ __global__ __launch_bounds__(BD) void norm_one_kernel(Shape p) {
             if (tile * p.tile_rows + ty + i * p.ty < rows) own[i].load(a.x, own0 + i * step);
         st.template take<kChunk, XBF>(a.x, x0 + (int64_t)ty * a.x_stride, step, (rows - ty + p.ty - 1) / p.ty);
     }
-    terms.put(src, width, BD);
+    terms.put(src, width);
     const float inv = 1.f / ((float)rows * (float)p.cg);
     lds.join(p, p.cg, st, ty, tx, [&](float m2) { return 1.f / sqrtf(m2 * inv + a.eps); });
-    terms.fold(lds.stat[0], lds.stat[1], width, p.cg, BD);
+    terms.fold(lds.stat[0], lds.stat[1], width, p.cg);
     if (!on) return;
     float mean[VEC], A[VEC], D[VEC];
     terms.take(tx * VEC, mean, A, D);
@@ -462,8 +462,8 @@ __global__ __launch_bounds__(BD) void norm_one_kernel(Shape p) {
 // Two launches, the first: (mean, M2) of each group (or part of one) of a row tile to
 // work[b][group][part * tiles + tile].
 template <int VEC, bool XBF, Span SPAN, int R>
-__global__ __launch_bounds__(kSplitThreads) void norm_stats_kernel(Shape p) {
-    __shared__ GroupJoin<VEC, SPAN, kSplitThreads> lds;
+__global__ __launch_bounds__(kThreads) void norm_stats_kernel(Shape p) {
+    __shared__ GroupJoin<VEC, SPAN> lds;
     const GroupNormArgs& a = p.a;
     const int tid = threadIdx.x, tile = blockIdx.y, b = blockIdx.z;
     int c0, width, g0, part;
@@ -477,7 +477,7 @@ __global__ __launch_bounds__(kSplitThreads) void norm_stats_kernel(Shape p) {
     if (ty < p.ty && tx * VEC < width && first + ty < end)
         st.template take<R, XBF>(a.x, x0 + (first + ty) * a.x_stride, step, (end - first - ty + p.ty - 1) / p.ty);
     lds.join(p, p.parts == 1 ? p.cg : width, st, ty, tx, [](float m2) { return m2; });
-    for (int g = tid; g < p.gs; g += kSplitThreads)
+    for (int g = tid; g < p.gs; g += kThreads)
         ((float2*)a.work)[((int64_t)b * a.groups + g0 + g) * p.parts * p.tiles + part * p.tiles + tile] =
             make_float2(lds.stat[0][g], lds.stat[1][g]);
 }
@@ -487,7 +487,7 @@ __global__ __launch_bounds__(kSplitThreads) void norm_stats_kernel(Shape p) {
 // memory: 65536 x 512 channels 22 us (6.1 TB/s, part of x from the caches), 262144 x 256 channels
 // of fp32 to bf16 65 us (6.2 TB/s).
 template <int VEC, bool XBF, int R, bool STREAM>
-__global__ __launch_bounds__(kSplitThreads) void norm_apply_kernel(Shape p) {
+__global__ __launch_bounds__(kThreads) void norm_apply_kernel(Shape p) {
     __shared__ float stat[2][kWide];
     __shared__ Terms terms;
     const GroupNormArgs& a = p.a;
@@ -515,7 +515,7 @@ __global__ __launch_bounds__(kSplitThreads) void norm_apply_kernel(Shape p) {
     // `lanes` lanes to a group, so that a wave's loads for several groups are in flight together
     int lanes = 64;
     while (lanes > 1 && lanes >= 2 * q_all) lanes /= 2;
-    for (int g = (w * 64 + lane) / lanes; g < p.gs; g += kSplitThreads / lanes) {
+    for (int g = (w * 64 + lane) / lanes; g < p.gs; g += kThreads / lanes) {
         const float2* src = (const float2*)a.work + ((int64_t)b * a.groups + g0 + g) * q_all;
         Moments m{0.f, 0.f, 0.f};
         for (int q = lane & (lanes - 1); q < q_all; q += lanes) {
@@ -530,9 +530,9 @@ __global__ __launch_bounds__(kSplitThreads) void norm_apply_kernel(Shape p) {
             stat[1][g] = 1.f / sqrtf(m.m2 * inv + a.eps);
         }
     }
-    terms.put(src, width, kSplitThreads);
+    terms.put(src, width);
     __syncthreads();
-    terms.fold(stat[0], stat[1], width, p.parts == 1 ? p.cg : width, kSplitThreads);
+    terms.fold(stat[0], stat[1], width, p.parts == 1 ? p.cg : width);
     if (!on) return;
     float mean[VEC], A[VEC], D[VEC];
     terms.take(tx * VEC, mean, A, D);
@@ -594,7 +594,7 @@ Shape split_plan(const GroupNormArgs& a, int v) {
     // slabs of 64 channels make whole cache lines (33.5 million values: 47 us, with 32 61 us), of 32
     // more workgroups (1.3 million: 12.1 us, with 64 12.5 us)
     Shape p = plan(a, v, a.B * a.rows * a.C < (1 << 22) ? 32 : 64);
-    p.ty = kSplitThreads / p.vpt;
+    p.ty = kThreads / p.vpt;
     const int64_t step = (int64_t)p.ty * kChunk;
     const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kMaxTiles, 1024 / std::max<int64_t>(1, a.B * p.slabs)));
     const int64_t per = std::max<int64_t>(1, (a.rows + want * step - 1) / (want * step)) * step;
@@ -607,21 +607,21 @@ template <int VEC, bool XBF, Span SPAN>
 void split(const GroupNormArgs& a, hipStream_t st) {
     const Shape p = split_plan(a, VEC);
     const dim3 grid((unsigned)p.slabs, (unsigned)p.tiles, (unsigned)a.B);
-    hipLaunchKernelGGL((norm_stats_kernel<VEC, XBF, SPAN, kChunk>), grid, dim3(kSplitThreads), 0, st, p);
+    hipLaunchKernelGGL((norm_stats_kernel<VEC, XBF, SPAN, kChunk>), grid, dim3(kThreads), 0, st, p);
     // 33.5 million values of bf16 (64 MB): 37.5 us with streaming stores, 47.6 without, and no less
     // with a reader of out behind them; 1.3 million: 12.5 us both ways, but the reader 1.2 us slower
     if (a.B * a.rows * a.C * (XBF ? 2 : 4) >= kStreamBytes)
-        hipLaunchKernelGGL((norm_apply_kernel<VEC, XBF, kApply, true>), grid, dim3(kSplitThreads), 0, st, p);
-    else hipLaunchKernelGGL((norm_apply_kernel<VEC, XBF, kApply, false>), grid, dim3(kSplitThreads), 0, st, p);
+        hipLaunchKernelGGL((norm_apply_kernel<VEC, XBF, kApply, true>), grid, dim3(kThreads), 0, st, p);
+    else hipLaunchKernelGGL((norm_apply_kernel<VEC, XBF, kApply, false>), grid, dim3(kThreads), 0, st, p);
 }
 
-template <int VEC, bool XBF, Span SPAN, int R, int BD>
+template <int VEC, bool XBF, Span SPAN, int R>
 void one(Shape p, hipStream_t st) {
-    p.ty = BD / p.vpt;
+    p.ty = kThreads / p.vpt;
     p.tile_rows = p.ty * R;
     p.tiles = (int)((p.a.rows + p.tile_rows - 1) / p.tile_rows);
     const dim3 grid((unsigned)p.slabs, (unsigned)p.tiles, (unsigned)p.a.B);
-    hipLaunchKernelGGL((norm_one_kernel<VEC, XBF, SPAN, R, BD>), grid, dim3(BD), 0, st, p);
+    hipLaunchKernelGGL((norm_one_kernel<VEC, XBF, SPAN, R>), grid, dim3(kThreads), 0, st, p);
 }
 
 template <int VEC, bool XBF, Span SPAN>
@@ -631,14 +631,14 @@ void run(const GroupNormArgs& a, hipStream_t st) {
     const int64_t vectors = p.vpt * a.rows, all = vectors * p.slabs * a.B;   // of a slab, of x
     // one row a thread while that takes 256 workgroups at most, else four (2 x 64 x 1280 channels:
     // 4.6 us, with four 4.85; 8 x 64 x 1280: 5.1 us, with one 5.4)
-    const bool few = vectors <= 256 || all <= 256 * 256;
-    const int own = 256 / p.vpt * (few ? 1 : 4);             // rows of a workgroup
+    const bool few = vectors <= kThreads || all <= 256 * kThreads;
+    const int own = kThreads / p.vpt * (few ? 1 : 4);             // rows of a workgroup
     const int64_t tiles = (a.rows + own - 1) / own;          // each reads the whole slab
     // in place, a slab's second workgroup would overwrite rows that the first still reads
     if (p.parts > 1 || vectors > kOneVectors || all * tiles > kOneReads || (a.x == a.out && tiles > 1))
         split<VEC, XBF, SPAN>(a, st);
-    else if (few) one<VEC, XBF, SPAN, 1, 256>(p, st);
-    else one<VEC, XBF, SPAN, 4, 256>(p, st);
+    else if (few) one<VEC, XBF, SPAN, 1>(p, st);
+    else one<VEC, XBF, SPAN, 4>(p, st);
 }
 
 template <int VEC, bool XBF>
