@@ -722,9 +722,16 @@ void down(const LoraBatchArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((lora_down_kernel<RB, W, U>), dim3(grid_of(tiles, inner, true)), dim3(W * 64), 0, st, a, inner);
 }
 
-// Rows from which A is staged once a workgroup: 4096 x 1024, rank 64, fp32: 34.6 us in all, 38.9
-// without; 3500 x 3072, rank 64: 31.4 us with, 24.9 without (its tiles leave CUs idle).
-constexpr int64_t kWideRows = 4096;
+// Rows from which A is staged once a workgroup, for ranks past 32.  Such a workgroup walks all of K
+// alone, where the narrow kernel's waves share it, so a longer K takes more workgroups to hide (us
+// in all, wide and narrow.  Rank 64, K = 1024: 3500 rows 23.7 and 21.6, 4500 25.8 and 26.4; 2048:
+// 4096 25.6 and 24.1, 7000 31.6 and 32.6; 3072: 6000 41.3 and 37.9, 9000 61.9 and 62.4, 16384 92.6
+// and 101.9; 12288: 6000 103 and 85, 12000 140 and 154.  Rank 128, K = 1024: 2000 23.7 and 21.2,
+// 3000 28.8 and 29.7; 2048: 3000 28.2 and 28.1, 5000 36.4 and 37.8; 3072: 5000 50.5 and 49.0, 7000
+// 63.1 and 67.8; 12288: 5000 133 and 111, 8192 171 and 180).
+int64_t wide_rows(const LoraBatchArgs& a) {
+    return a.nb == 4 ? std::clamp<int64_t>(2 * (int64_t)a.K, 2304, 6144) : std::clamp<int64_t>(3 * (int64_t)a.K, 4096, 8192);
+}
 
 template <int TB, int NRB, int RW, int KW, int D, int OCC>
 void down_wide(const LoraBatchArgs& a, hipStream_t st) {
@@ -735,7 +742,7 @@ void down_wide(const LoraBatchArgs& a, hipStream_t st) {
 }
 
 void launch_down(const LoraBatchArgs& a, hipStream_t st) {
-    if (a.nb >= 2 && a.M >= kWideRows) {
+    if (a.nb >= 2 && a.M >= wide_rows(a)) {
         // the lowest tiles that need one round of 256 CUs at most: a workgroup has a CU's LDS and
         // registers nearly to itself, and a few tiles too many cost another round (16384 x 4096,
         // rank 128, 16 segments: 152 us in all, with 64 rows to a tile 184; 12000 x 3072, rank 64:

@@ -91,3 +91,10 @@ def test_in_place_takes_two_launches_where_a_slab_has_several_workgroups(trace):
 def test_an_empty_pool_has_no_down_projection(trace):
     _, (full, empty) = trace(["lora 9000 64 64 64 2 3 1", "lora 9000 64 64 64 2 0 1"])
     assert len(full) == 2 and len(empty) == 1 and empty[0] == full[1]
+
+
+@pytest.mark.parametrize("K,R,rows", [(512, 64, 4096), (2048, 64, 6144), (4096, 64, 8192), (12288, 48, 8192),
+                                      (512, 128, 2304), (2048, 128, 4096), (4096, 112, 6144), (12288, 128, 6144)])
+def test_rows_from_which_the_wide_down_projection_is_taken(trace, K, R, rows):
+    _, (narrow, wide) = trace([f"lora {m} {K} 1024 {R} 4 3 1" for m in (rows - 1, rows)])
+    assert narrow[0].startswith("lora_down_kernel<") and wide[0].startswith("lora_down_wide_kernel<")
