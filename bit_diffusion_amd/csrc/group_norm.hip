@@ -610,7 +610,7 @@ void split(const GroupNormArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((norm_stats_kernel<VEC, XBF, SPAN, kChunk>), grid, dim3(kThreads), 0, st, p);
     // 33.5 million values of bf16 (64 MB): 37.5 us with streaming stores, 47.6 without, and no less
     // with a reader of out behind them; 1.3 million: 12.5 us both ways, but the reader 1.2 us slower
-    if (a.B * a.rows * a.C * (XBF ? 2 : 4) >= kStreamBytes)
+    if (a.B * a.rows * a.C >= kStreamBytes / (XBF ? 2 : 4))
         hipLaunchKernelGGL((norm_apply_kernel<VEC, XBF, kApply, true>), grid, dim3(kThreads), 0, st, p);
     else hipLaunchKernelGGL((norm_apply_kernel<VEC, XBF, kApply, false>), grid, dim3(kThreads), 0, st, p);
 }
