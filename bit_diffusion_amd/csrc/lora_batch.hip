@@ -4,8 +4,8 @@
 // s = seg_adapter[i] of a pool, or none:
 //   out[m, n] = act(base[m, n] + sum_{j < rank_s} t[m, j] B_s[n, j]),
 //   t[m, j]   = alpha_s sum_k x[m, k] A_s[j, k].
-// Both products are bound by memory (x once; base and out once): 2 R flops per byte of x,
-// R / 2 per byte of bf16 base and out.  Many rows take two launches, the down-projection
+// Both products are bound by memory (x once; base and out once): R flops per byte of x, R / 2 per
+// byte of bf16 base and out (past rank 64 by LDS and registers first).  Many rows take two launches, the down-projection
 // (t to the workspace) and the up-projection (t, base -> out); few rows take one, in which
 // every workgroup forms its rows' t itself.
 //
@@ -653,9 +653,9 @@ __global__ __launch_bounds__(256, up_waves(RBE, CB, NB)) void lora_up_kernel(Lor
 // Both products for a tile of 16 rows x 256 columns, 32 columns to each of 8 waves: the waves
 // share the steps of K, and the rows' t goes through LDS.  Every workgroup of a tile reads its
 // rows and A again (from the L2s), which costs less than a second launch while they are few
-// and fit one round of CUs: 2 rows, 3072 -> 18432, rank 16: 6.7 us, two launches 8.3; 1237 rows,
-// rank 64, in 332 workgroups: 15.0 us, in two launches 12.8.  Bound by the launch and the
-// latency of K / 1024 steps.
+// and fit one round of CUs: 2 rows, 3072 -> 18432, rank 16: 6.8 us, two launches 8.1; 1237 rows,
+// rank 64, in 332 workgroups: 14.3 us, in two launches 11.3.  Bound by a chain of dependent
+// latencies: the launch, the segment, its adapter, K / 1024 steps, the join of the waves' sums.
 template <int RB, bool BF16, int U>
 __global__ __launch_bounds__(512) void lora_few_rows_kernel(LoraBatchArgs a, int inner) {
     constexpr int W = 8, NB = RB / 2;
@@ -771,7 +771,7 @@ void up(const LoraBatchArgs& a, hipStream_t st) {
     const int64_t tiles = most_tiles(a.M, a.n_segments, RBE * 16);
     const int blocks = (a.N + 64 * CB - 1) / (64 * CB);
     // up to 2 blocks a workgroup, so that neighbours work on the rest of the same rows at a time;
-    // 8 where t is large (16384 x 4096: rank 32 105 us in all, 122 with 8; rank 128 157, 165 with 2)
+    // 8 where t is large (16384 x 4096: rank 32 96 us in all, 108 with 8; rank 128 155, 168 with 2)
     constexpr int kMost = NB == 4 ? 8 : 2;
     int span = 1;
     while (span < kMost && span < blocks && tiles * ((blocks + 2 * span - 1) / (2 * span)) >= 1024) span *= 2;
@@ -783,7 +783,8 @@ void up(const LoraBatchArgs& a, hipStream_t st) {
 template <int RBE, bool BF16>
 void up_rank(const LoraBatchArgs& a, hipStream_t st) {
     // columns of a wave: 64 cover whole cache lines of out, 32 make more and smaller workgroups
-    // (rank 16: 16384 x 4096 73 us in all with 64, 79 with 32; 4096 x 3072 22.4 and 21.2)
+    // (16384 x 4096: rank 16 88.5 us in all with 64, 93.0 with 32; rank 32 96.4 and 101.7;
+    // 4096 x 3072, rank 16 22.5 and 21.4)
     const bool wide = most_tiles(a.M, a.n_segments, RBE * 16) * ((a.N + 255) / 256) >= 2048;
     switch (a.nb) {
         case 0: wide ? up<RBE, 4, 0, BF16>(a, st) : up<RBE, 2, 0, BF16>(a, st); break;
@@ -823,16 +824,19 @@ void launch_lora_batch(const LoraBatchArgs& args, hipStream_t st) {
     a.nb = rank_blocks(a.R);
     a.max_blocks = (int)most_tiles(a.M, a.n_segments, 16);
     const int64_t inner = (a.N + kColTile - 1) / kColTile;
-    // one launch while A is small (4 rows, one and two launches: rank 32, K = 4096 8.1 and 9.1 us,
-    // 8192 11.8 and 11.6; rank 64, K = 2048 8.2 and 8.1, 3072 10.1 and 8.7)
-    if (a.R <= 64 && a.max_blocks * inner <= 256 && (int64_t)a.R * a.K <= (a.R <= 32 ? 1 << 18 : 1 << 17)) {
+    // one launch while A is small (one and two launches, us: rank 16, K = 16384, 4 rows 14.2 and
+    // 16.4; rank 32, K = 4096, 100 rows 8.5 and 9.0, K = 6144 11.0 and 10.4; rank 64, K = 1536, one
+    // row 7.4 and 7.6, K = 2048 8.3 and 7.7)
+    if (a.R <= 64 && a.max_blocks * inner <= 256 &&
+        (int64_t)a.R * a.K <= (a.R <= 16 ? 1 << 18 : a.R <= 32 ? 1 << 17 : 3 << 15)) {
         a.bf16 ? few_rows<true>(a, st) : few_rows<false>(a, st);
         return;
     }
     if (a.n_adapters > 0) launch_down(a, st);
-    // 32 rows to a workgroup where that leaves 1024 of them (16384 x 4096, rank 128: 156 us in all,
-    // with 16 178; 300 x 3072, rank 32: 9.4, with 16 9.1); t's third term for fp32 takes the
-    // registers of the second 16 rows (30000 x 1024, rank 64: 90 us in all, 99 with 32 rows)
+    // 32 rows to a workgroup where that leaves 1024 of them (16384 x 4096: rank 128 156 us in all,
+    // with 16 173, rank 32 96 and 100; 300 x 3072, rank 32: 9.1, with 16 8.7); an fp32 output's
+    // base takes the registers of the second 16 rows (30000 x 1024, rank 64: 90 us in all, 99 with
+    // 32 rows)
     if (!a.bf16) up_rank<1, false>(a, st);
     else if ((a.M / 32) * inner >= 1024) up_rank<2, true>(a, st);
     else up_rank<1, true>(a, st);

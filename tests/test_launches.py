@@ -98,3 +98,9 @@ def test_an_empty_pool_has_no_down_projection(trace):
 def test_rows_from_which_the_wide_down_projection_is_taken(trace, K, R, rows):
     _, (narrow, wide) = trace([f"lora {m} {K} 1024 {R} 4 3 1" for m in (rows - 1, rows)])
     assert narrow[0].startswith("lora_down_kernel<") and wide[0].startswith("lora_down_wide_kernel<")
+
+
+@pytest.mark.parametrize("R,K", [(16, 16384), (32, 4096), (48, 2048), (64, 1536)])
+def test_longest_k_of_one_launch(trace, R, K):
+    _, (one, two) = trace([f"lora 4 {k} 1024 {R} 1 3 1" for k in (K, K + 64)])
+    assert len(one) == 1 and len(two) == 2
