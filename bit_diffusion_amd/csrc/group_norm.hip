@@ -7,7 +7,7 @@
 //   out  = act(((x - mean) r w_c + b_c) (1 + scale_bc) + shift_bc)
 // with the channel's terms folded to (x - mean) A_c + D_c, A = r w (1 + scale),
 // D = b (1 + scale) + shift.  All of it in fp32; squares are summed about a mean, never about
-// zero, so a large common offset costs nothing.
+// zero, so a large common offset costs no more than the rounding of the mean, 2^-24 of it.
 //
 // Bound: memory, x once and out once.  A workgroup works on a slab: a range of channels that
 // is whole groups (or, for a group too wide, a part of one), so neighbouring lanes read
@@ -36,7 +36,7 @@ constexpr int kChunk = 8;         // rows of a thread's chunk in the statistics,
 constexpr int kApply = 4;         // and in the launch that only normalises
 // The one launch: vectors of a slab, at most (1 x 2048 x 256 channels, 8192 vectors: 6.8 us, in
 // two launches 8.6; 2 x 2048 x 320 fp32, 10240: 14.8 us, 9.3), and vectors that all its
-// workgroups read (2 x 1024 x 640, 0.8 million: 8.9 us, in two launches 10.9; 8 images, 3.3
+// workgroups read (2 x 1024 x 640, 0.8 million: 9.1 us, in two launches 10.9; 8 images, 3.3
 // million: 18.5 us, 14.7).
 constexpr int kOneVectors = 8192;
 constexpr int64_t kOneReads = 1 << 20;
@@ -409,7 +409,7 @@ struct GroupJoin {
 };
 
 // Bound by the launch, the latency of its loads and the joins: 2 x 64 x 1280 channels 4.6 us in a
-// graph, 2 x 1024 x 640 8.9 us.
+// graph, 2 x 1024 x 640 9.1 us.
 //
 // One launch: workgroup (tile, slab, image) normalises R rows a thread, which it keeps, and takes
 // the statistics of the whole slab, kChunk rows a thread at a time, in the same order as every
@@ -591,8 +591,8 @@ Shape plan(const GroupNormArgs& a, int v, int least) {
     return p;
 }
 
-// The cut of the two launches: about 1024 workgroups, each at least one chunk (2 x 65536 x 256
-// channels: 38.8 us; with 512 38.9, with 2048 43.6).
+// The cut of the two launches: about 1024 workgroups (kMaxTiles at most for a slab of one image),
+// each at least one chunk (2 x 65536 x 256 channels: 38.8 us; with 512 38.9, with 2048 43.6).
 Shape split_plan(const GroupNormArgs& a, int v) {
     // slabs of 64 channels make whole cache lines (33.5 million values: 47 us, with 32 61 us), of 32
     // more workgroups (1.3 million: 12.1 us, with 64 12.5 us)

@@ -257,8 +257,8 @@ __device__ __forceinline__ void tile_of(int id, int inner, int& tile, int& part)
 // Down-projection of a tile of 16 rows, RB rank blocks: the W waves take the steps of K in turn
 // and their sums are added in wave order through LDS.  16 waves of one step at a time (64
 // registers) leave room for a second workgroup on the CU, which the few tiles past 256 need:
-// 4096 x 3072, rank 16: 9.5 us (2.6 TB/s of x); 12.9 with two steps at a time and one workgroup
-// a CU.  Bound by the latency of its few steps; 16384 x 4096 takes 38 us (3.5 TB/s).
+// 4096 x 3072, rank 16: 9.3 us (2.7 TB/s of x); 12.9 with two steps at a time and one workgroup
+// a CU.  Bound by the latency of its few steps; 16384 x 4096 takes 37 us (3.6 TB/s).
 template <int RB, int W, int U>
 __global__ __launch_bounds__(W * 64) void lora_down_kernel(LoraBatchArgs a, int inner) {
     constexpr int kSums = W * RB * 64, kStage = W * 256;
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(W * 64) void lora_down_kernel(LoraBatchArgs a, int 
 // adapter's A are staged once for the workgroup, 128 channels at a time, and each wave has RW
 // row blocks x KW rank blocks over all of K.  D steps are in flight in registers (OCC: waves a
 // SIMD that the registers must leave room for).  Bound by the CU's LDS and its barriers: 1.5 us
-// a step of 96 rows x 128 ranks, of which LDS moves 216 KB; 16384 x 4096 at rank 128 takes 65 us
+// a step of 96 rows x 128 ranks, of which LDS moves 216 KB; 16384 x 4096 at rank 128 takes 63 us
 // (2.1 TB/s of x).  At rank 32 the narrow kernel is faster: 8192 x 12288 86 us in all, so 104.
 // Steps are counted from another one in each tile, round the end of K: rows of x and A lie K
 // elements apart, a distance that falls on few memory channels, and workgroups that walk K in
@@ -564,7 +564,7 @@ struct UpTile {
 };
 
 // Up-projection, bound by memory (base and out once) and, at rank 128, by the registers that t
-// takes: 16384 x 4096 at rank 16 takes 52 us (5.2 TB/s), at rank 128 97 us (2.8 TB/s).
+// takes: 16384 x 4096 at rank 16 takes 52 us (5.2 TB/s), at rank 128 95 us (2.9 TB/s).
 //
 // A workgroup's rows x `blocks` blocks of 64 CB columns, 16 CB columns to each of 4 waves: t
 // stays in registers; base is loaded two blocks ahead, B as soon as the block before has its own
