@@ -101,3 +101,66 @@ def test_most_rows_and_segments_of_adapters(n, R, bf):
         ok = (out[s].double() - ref).abs() <= e + half * (ref.abs() + e) + 1e-37
         none = row_id[s] == -2
         assert bool(ok[~none].all()) and torch.equal(out[s][none], before[s][none])
+
+
+# the most channels: one group in 128 parts, a group a channel, groups of an odd width in 205 parts
+@pytest.mark.parametrize("B,rows,C,G,xd", [(1, 33, 65536, 1, BF), (2, 3, 65536, 65536, F32), (1, 700, 65536, 16384, BF), (1, 7, 65535, 5, F32)])
+def test_most_channels(B, rows, C, G, xd):
+    """Joins over the parts of a group come on top of the rows': 128 or 205 parts of 64 or more
+    channels, each lane joins 4 of them at most, within the 256 roundings that the bound counts."""
+    c = Norm(33, B, rows, C, G, xd=xd, act=2)
+    got = c.call()
+    torch.cuda.synchronize()
+    c.check(got)
+
+
+def test_longest_k():
+    """K = 2^24: rows with three nonzeros, the first channel, one in the middle and the last, so that t
+    is a sum of three exact products: 2 roundings, alpha's, three added products and the output's,
+    8 u of the absolute sums in all."""
+    M, K, N, R = 3, 1 << 24, 40, 16
+    g = torch.Generator(device=DEV).manual_seed(8)
+    x = torch.zeros(M, K, dtype=BF, device=DEV)
+    at = torch.tensor([0, (1 << 23) + 5, K - 1], device=DEV)
+    x[:, at] = torch.randn(M, 3, generator=g, device=DEV).to(BF)
+    down = torch.randn(1, R, K, generator=g, device=DEV, dtype=BF)
+    up = torch.randn(1, N, R, generator=g, device=DEV).to(BF)
+    alpha, out = torch.tensor([0.3], device=DEV), torch.zeros(M, N, device=DEV)
+    starts, ids = torch.tensor([0, M], dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    nb = bd.svdq_lora_batch_workspace_bytes(M, K, N, R, 1)
+    ws = torch.empty(nb, dtype=torch.uint8, device=DEV)
+    bd.svdq_lora_batch(M, K, N, R, 1, 1, x, K, down, up, alpha, None, starts, ids, None, 0, 0, DT[F32], out, N, ws, nb)
+    torch.cuda.synchronize()
+    xs, A, B = x[:, at].double(), down[0][:, at].double(), up[0].double()
+    al = alpha.double()
+    ref = (al * (xs @ A.t().contiguous())) @ B.t().contiguous()
+    size = (al * (xs.abs() @ A.abs().t().contiguous())) @ B.abs().t().contiguous()
+    # and the sums over 16 ranks, three terms each, counted twice
+    assert bool(((out.double() - ref).abs() <= (8 + 2 * (3 * R + 4)) * U * size).all())
+
+
+def test_widest_output():
+    """N = 2^27: offsets in lora_up pass 2^31 elements.  Rank 1, so an element is base + t B."""
+    M, K, N, R = 2, 64, 1 << 27, 16
+    g = torch.Generator(device=DEV).manual_seed(9)
+    x, down = torch.randn(M, K, generator=g, device=DEV).to(BF), torch.randn(1, R, K, generator=g, device=DEV).to(BF)
+    up = torch.empty(1, N, R, dtype=BF, device=DEV)
+    for part in up[0].split(1 << 24):
+        part.copy_(torch.randn(part.shape, generator=g, device=DEV))
+    alpha, ranks = torch.tensor([1.5], device=DEV), torch.ones(1, dtype=torch.int32, device=DEV)
+    base = torch.randn(M, N, generator=g, device=DEV).to(BF)
+    out = torch.empty_like(base)
+    starts, ids = torch.tensor([0, M], dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    nb = bd.svdq_lora_batch_workspace_bytes(M, K, N, R, 1)
+    ws = torch.empty(nb, dtype=torch.uint8, device=DEV)
+    bd.svdq_lora_batch(M, K, N, R, 1, 1, x, K, down, up, alpha, ranks, starts, ids, base, N, 0, DT[BF], out, N, ws, nb)
+    torch.cuda.synchronize()
+    t = 1.5 * (x.double() * down[0, 0].double()).sum(1)
+    D = 1.5 * (x.double() * down[0, 0].double()).abs().sum(1)
+    for lo in range(0, N, 1 << 24):
+        s = slice(lo, lo + (1 << 24))
+        B = up[0, s, 0].double()
+        for m in range(M):
+            ref = base[m, s].double() + t[m] * B
+            e = (2 * (K + 16) * U * D[m] + 8 * U * t[m].abs()) * B.abs() + 4 * U * (base[m, s].double().abs() + ref.abs())
+            assert bool(((out[m, s].double() - ref).abs() <= e + 2.0 ** -8 * (ref.abs() + e) + 1e-37).all())
