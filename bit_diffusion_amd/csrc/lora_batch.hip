@@ -5,9 +5,9 @@
 //   out[m, n] = act(base[m, n] + sum_{j < rank_s} t[m, j] B_s[n, j]),
 //   t[m, j]   = alpha_s sum_k x[m, k] A_s[j, k].
 // Both products are bound by memory (x once; base and out once): R flops per byte of x, R / 2 per
-// byte of bf16 base and out (past rank 64 by LDS and registers first).  Many rows take two launches, the down-projection
-// (t to the workspace) and the up-projection (t, base -> out); few rows take one, in which
-// every workgroup forms its rows' t itself.
+// byte of bf16 base and out; past rank 32 LDS, barriers and registers bind first.  Many rows take
+// two launches, the down-projection (t to the workspace) and the up-projection (t, base -> out);
+// few rows take one, in which every workgroup forms its rows' t itself.
 //
 // Tiles.  A workgroup owns rows of one segment only, so its adapter is uniform.  The
 // offsets live in device memory (a captured graph replays with other offsets), so the grid
@@ -615,11 +615,12 @@ __device__ __forceinline__ void up_blocks(const LoraBatchArgs& a, const Tile& t,
     }
 }
 
-// Up-projection of a tile of 16 RBE rows, `span` blocks of columns.  WAVES: waves a SIMD that the
-// registers must leave room for (32 rows, 32 columns a wave, rank 16: 97 registers leave room for
-// 4, one less for 5: 4096 x 3072 21.6 us in all, 22.3 with 4; tighter bounds elsewhere spill and
-// cost time).
+// Waves a SIMD that the up-projection's registers must leave room for: at 32 rows, 32 columns a wave
+// and rank 16 the compiler takes 97 unasked, one more than leaves room for 5 (4096 x 3072 21.6 us
+// in all, 22.3 with 4 waves); tighter bounds elsewhere spill and cost time.
 constexpr int up_waves(int RBE, int CB, int NB) { return RBE == 2 && CB == 2 && NB == 0 ? 5 : 1; }
+
+// Up-projection of a tile of 16 RBE rows, `span` blocks of columns.
 template <int RBE, int CB, int NB, bool BF16>
 __global__ __launch_bounds__(256, up_waves(RBE, CB, NB)) void lora_up_kernel(LoraBatchArgs a, int inner, int span) {
     using Up = UpTile<RBE, CB, NB, BF16>;
