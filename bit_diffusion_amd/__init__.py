@@ -13,7 +13,8 @@ from . import _abi
 from ._abi import (SVDQ_OK, SVDQ_ERR_INVALID_ARG, SVDQ_ERR_UNSUPPORTED_DEVICE,  # noqa: F401
                    SVDQ_ERR_UNSUPPORTED_CONFIG, SVDQ_ERR_LAUNCH, SVDQ_PREC_INT4, SVDQ_PREC_NVFP4,
                    SVDQ_DT_F32, SVDQ_DT_BF16, SVDQ_ACT_NONE, SVDQ_ACT_GELU_TANH,
-                   SVDQ_ACT_SILU, LayerCfg, SvdqError, lib, LIB_PATH)
+                   SVDQ_ACT_SILU, SVDQ_MASK_NONE, SVDQ_MASK_CAUSAL, SVDQ_ROTARY_INTERLEAVED,
+                   SVDQ_ROTARY_HALVES, LayerCfg, SvdqError, lib, LIB_PATH)
 
 __all__ = [
     "svdq_quantize_act", "svdq_gemm_w4a4", "awq_gemm_w4a16", "svdq_check_device",
@@ -26,7 +27,8 @@ __all__ = [
     "svdq_quantize_next_workspace_bytes", "svdq_peak_mfma", "svdq_peak_copy",
     "svdq_gemm_w4a4_packed_noalloc", "svdq_peak_read",
     "svdq_lora_batch_workspace_bytes", "svdq_lora_batch", "svdq_group_norm_workspace_bytes",
-    "svdq_group_norm", "svdq_check_arch", "svdq_status_string", "svdq_last_error", "svdq_version", "LayerCfg",
+    "svdq_group_norm", "svdq_layer_norm", "svdq_rotary", "svdq_attention_workspace_bytes",
+    "svdq_attention", "svdq_check_arch", "svdq_status_string", "svdq_last_error", "svdq_version", "LayerCfg",
     "SvdqError", "lib", "LIB_PATH",
 ]
 
@@ -273,6 +275,54 @@ def svdq_group_norm(B, rows, C, groups, eps, x_dtype, x, x_stride, weight, bias,
     return _check(lib().svdq_group_norm(B, rows, C, groups, eps, x_dtype, x, x_stride, w, b, mod_dtype, ms, mt,
                                         mod_stride, act, out_dtype, ou, out_stride, ws, workspace_bytes,
                                         _stream(stream)))
+
+
+_LAYER_NORM = ("x", "y", "weight", "bias", "seg_start", "mod_gate", "mod_scale", "mod_shift", "x_out", "out")
+
+
+def svdq_layer_norm(M, C, n_segments, eps, x_dtype, x, x_stride, y_dtype, y, y_stride, weight, bias, seg_start,
+                    mod_dtype, mod_gate, mod_scale, mod_shift, mod_stride, x_out, x_out_stride, out_dtype, out,
+                    out_stride, stream=None):
+    x, y, w, b, st, mg, ms, mt, xo, ou = _dev_ptrs(
+        _LAYER_NORM, (x, y, weight, bias, seg_start, mod_gate, mod_scale, mod_shift, x_out, out))
+    return _check(lib().svdq_layer_norm(M, C, n_segments, eps, x_dtype, x, x_stride, y_dtype, y, y_stride, w, b, st,
+                                        mod_dtype, mg, ms, mt, mod_stride, xo, x_out_stride, out_dtype, ou,
+                                        out_stride, _stream(stream)))
+
+
+_ROTARY = ("positions", "freqs", "q_weight", "k_weight", "q", "k", "q_out", "k_out")
+
+
+def svdq_rotary(M, n_q_heads, n_k_heads, head_dim, axis_pairs, pairing, positions, pos_stride, freqs, eps, q_weight,
+                k_weight, x_dtype, q, q_stride, k, k_stride, out_dtype, q_out, q_out_stride, k_out, k_out_stride,
+                stream=None):
+    """axis_pairs: a sequence of whole numbers, n_axes of the C call is its length."""
+    po, fr, qw, kw, q, k, qo, ko = _dev_ptrs(
+        _ROTARY, (positions, freqs, q_weight, k_weight, q, k, q_out, k_out))
+    pairs = (ctypes.c_int32 * len(axis_pairs))(*axis_pairs)
+    return _check(lib().svdq_rotary(M, n_q_heads, n_k_heads, head_dim, len(axis_pairs), pairs, pairing, po,
+                                    pos_stride, fr, eps, qw, kw, x_dtype, q, q_stride, k, k_stride, out_dtype, qo,
+                                    q_out_stride, ko, k_out_stride, _stream(stream)))
+
+
+def svdq_attention_workspace_bytes(Mq, Mkv, n_heads, n_kv_heads, head_dim, n_segments):
+    n = ctypes.c_int64(0)
+    _check(lib().svdq_attention_workspace_bytes(int(Mq), int(Mkv), int(n_heads), int(n_kv_heads), int(head_dim),
+                                                int(n_segments), ctypes.byref(n)))
+    return n.value
+
+
+_ATTENTION = ("q_start", "kv_start", "prefix", "slopes", "q", "k", "v", "out", "workspace")
+
+
+def svdq_attention(Mq, Mkv, n_heads, n_kv_heads, head_dim, n_segments, scale, cap, mask, q_start, kv_start, prefix,
+                   slopes, q, q_stride, k, k_stride, v, v_stride, out, out_stride, workspace, workspace_bytes,
+                   stream=None):
+    qs, ks, pr, sl, q, k, v, ou, ws = _dev_ptrs(
+        _ATTENTION, (q_start, kv_start, prefix, slopes, q, k, v, out, workspace))
+    return _check(lib().svdq_attention(Mq, Mkv, n_heads, n_kv_heads, head_dim, n_segments, scale, cap, mask, qs, ks,
+                                       pr, sl, q, q_stride, k, k_stride, v, v_stride, ou, out_stride, ws,
+                                       workspace_bytes, _stream(stream)))
 
 
 def svdq_peak_mfma(kind, iters, out, stream=None):

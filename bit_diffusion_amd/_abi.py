@@ -21,6 +21,10 @@ SVDQ_DT_BF16 = 1
 SVDQ_ACT_NONE = 0
 SVDQ_ACT_GELU_TANH = 1
 SVDQ_ACT_SILU = 2
+SVDQ_MASK_NONE = 0
+SVDQ_MASK_CAUSAL = 1
+SVDQ_ROTARY_INTERLEAVED = 0
+SVDQ_ROTARY_HALVES = 1
 
 # Every symbol include/*.h declares.
 EXPORTS = ("svdq_quantize_act", "svdq_gemm_w4a4", "awq_gemm_w4a16", "svdq_check_device",
@@ -33,7 +37,8 @@ EXPORTS = ("svdq_quantize_act", "svdq_gemm_w4a4", "awq_gemm_w4a16", "svdq_check_
            "svdq_gemm_w4a4_packed_workspace_bytes", "svdq_gemm_w4a4_packed_ws",
            "svdq_quantize_next_workspace_bytes", "svdq_peak_mfma", "svdq_peak_copy",
            "svdq_gemm_w4a4_packed_noalloc", "svdq_peak_read", "svdq_lora_batch_workspace_bytes",
-           "svdq_lora_batch", "svdq_group_norm_workspace_bytes", "svdq_group_norm")
+           "svdq_lora_batch", "svdq_group_norm_workspace_bytes", "svdq_group_norm", "svdq_layer_norm",
+           "svdq_rotary", "svdq_attention_workspace_bytes", "svdq_attention")
 
 
 class LayerCfg(ctypes.Structure):
@@ -107,6 +112,14 @@ def lib():
                                                       ctypes.POINTER(ctypes.c_int64)]
         L.svdq_group_norm.argtypes = [I64, I64, I32, I32, F, I32, P, I64, P, P, I32, P, P, I64, I32,
                                       I32, P, I64, P, I64, P]
+        L.svdq_layer_norm.argtypes = [I64, I32, I32, F, I32, P, I64, I32, P, I64, P, P, P, I32, P, P, P, I64, P,
+                                      I64, I32, P, I64, P]
+        L.svdq_rotary.argtypes = [I64, I32, I32, I32, I32, P, I32, P, I64, P, F, P, P, I32, P, I64, P, I64, I32,
+                                  P, I64, P, I64, P]
+        L.svdq_attention_workspace_bytes.argtypes = [I64, I64, I32, I32, I32, I32,
+                                                     ctypes.POINTER(ctypes.c_int64)]
+        L.svdq_attention.argtypes = [I64, I64, I32, I32, I32, I32, F, F, I32, P, P, P, P, P, I64, P, I64, P, I64,
+                                     P, I64, P, I64, P]
         L.svdq_check_device.argtypes = [ctypes.c_int]
         L.svdq_check_arch.argtypes = [ctypes.c_char_p]
         L.svdq_status_string.argtypes = [ctypes.c_int]
@@ -125,7 +138,8 @@ def lib():
                      "svdq_quantize_next_workspace_bytes", "svdq_peak_mfma", "svdq_peak_copy",
                      "svdq_gemm_w4a4_packed_noalloc", "svdq_peak_read",
                      "svdq_lora_batch_workspace_bytes", "svdq_lora_batch",
-                     "svdq_group_norm_workspace_bytes", "svdq_group_norm"):
+                     "svdq_group_norm_workspace_bytes", "svdq_group_norm", "svdq_layer_norm",
+                     "svdq_rotary", "svdq_attention_workspace_bytes", "svdq_attention"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib

@@ -35,6 +35,12 @@ svdq_status fail(svdq_status st, const char* fmt, ...) {
     return st;
 }
 
+#define SVDQ_TRY(expr)                     \
+    do {                                   \
+        svdq_status _s = (expr);           \
+        if (_s != SVDQ_OK) return _s;      \
+    } while (0)
+
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_dev_state[kMaxDevices];   // 0 unknown, 1 gfx950, 2 other
 
@@ -173,17 +179,56 @@ svdq_status check_group_norm(int64_t B, int64_t rows, int32_t C, int32_t groups)
     return SVDQ_OK;
 }
 
+svdq_status check_optional(const void* p, const char* name, size_t align) {
+    if (p != nullptr && !aligned(p, align))
+        return fail(SVDQ_ERR_INVALID_ARG, "%s is not %zu-byte aligned", name, align);
+    return SVDQ_OK;
+}
+
+svdq_status check_segments(int32_t n_segments) {
+    if (n_segments < 0) return fail(SVDQ_ERR_INVALID_ARG, "n_segments = %d is negative", n_segments);
+    if (n_segments > 1 << 16)
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "n_segments = %d exceeds the supported maximum 2^16", n_segments);
+    return SVDQ_OK;
+}
+
+svdq_status check_attention(int64_t Mq, int64_t Mkv, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                            int32_t n_segments) {
+    if (Mq < 0) return fail(SVDQ_ERR_INVALID_ARG, "Mq = %lld is negative", (long long)Mq);
+    if (Mkv < 0) return fail(SVDQ_ERR_INVALID_ARG, "Mkv = %lld is negative", (long long)Mkv);
+    if (n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0)
+        return fail(SVDQ_ERR_INVALID_ARG, "n_heads %d must be a positive multiple of n_kv_heads %d", n_heads, n_kv_heads);
+    if (head_dim <= 0 || head_dim % 8 != 0)
+        return fail(SVDQ_ERR_INVALID_ARG, "head_dim %d must be a positive multiple of 8", head_dim);
+    if (head_dim > 128)
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "head_dim %d exceeds the supported maximum 128", head_dim);
+    SVDQ_TRY(check_segments(n_segments));
+    if (n_heads > 1 << 16)
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "n_heads %d exceeds the supported maximum 2^16", n_heads);
+    if (Mkv > (int64_t)1 << 30 || Mq > (int64_t)1 << 24 ||
+        !svdq::attention_fits(Mq, n_heads, n_kv_heads, n_segments))
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "Mq = %lld, Mkv = %lld, n_heads = %d, n_segments = %d too large for one launch",
+                    (long long)Mq, (long long)Mkv, n_heads, n_segments);
+    return SVDQ_OK;
+}
+
+// Rows of an attention operand: 16-byte aligned, and offsets in a tile within 32 bits.
+svdq_status check_head_rows(const void* p, const char* name, int64_t stride, const char* stride_name, int64_t least,
+                            bool empty) {
+    SVDQ_TRY(check_buf(p, name, 16, empty));
+    SVDQ_TRY(check_stride(stride, least, stride_name));
+    if (stride % 8 != 0)
+        return fail(SVDQ_ERR_INVALID_ARG, "%s = %lld must be a multiple of 8", stride_name, (long long)stride);
+    if (stride > 1 << 24)
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "%s = %lld exceeds the supported maximum 2^24", stride_name, (long long)stride);
+    return SVDQ_OK;
+}
+
 svdq_status after_launch(const char* what) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(SVDQ_ERR_LAUNCH, "%s launch failed: %s", what, hipGetErrorString(e));
     return SVDQ_OK;
 }
-
-#define SVDQ_TRY(expr)                     \
-    do {                                   \
-        svdq_status _s = (expr);           \
-        if (_s != SVDQ_OK) return _s;      \
-    } while (0)
 
 }  // namespace
 
@@ -775,6 +820,214 @@ svdq_status svdq_group_norm(int64_t B, int64_t rows, int32_t C, int32_t groups, 
     a.vec = aligned(x, 16) && aligned(out, 16) && x_stride * xsz % 16 == 0 && out_stride * osz % 16 == 0;
     svdq::launch_group_norm(a, reinterpret_cast<hipStream_t>(stream));
     return after_launch("svdq_group_norm");
+}
+
+svdq_status svdq_layer_norm(int64_t M, int32_t C, int32_t n_segments, float eps, int32_t x_dtype, const void* x,
+                            int64_t x_stride, int32_t y_dtype, const void* y, int64_t y_stride,
+                            const void* weight, const void* bias, const int32_t* seg_start,
+                            int32_t mod_dtype, const void* mod_gate, const void* mod_scale,
+                            const void* mod_shift, int64_t mod_stride, void* x_out, int64_t x_out_stride,
+                            int32_t out_dtype, void* out, int64_t out_stride, svdq_stream_t stream) {
+    if (M < 0) return fail(SVDQ_ERR_INVALID_ARG, "M = %lld is negative", (long long)M);
+    if (M > (int64_t)1 << 30)
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "M = %lld too large for one launch", (long long)M);
+    if (C <= 0) return fail(SVDQ_ERR_INVALID_ARG, "C %d must be positive", C);
+    if (C > 16384) return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "C %d exceeds the supported maximum 16384", C);
+    SVDQ_TRY(check_segments(n_segments));
+    if (!(std::isfinite(eps) && eps > 0.0f))
+        return fail(SVDQ_ERR_INVALID_ARG, "eps = %g must be finite and positive", (double)eps);
+    SVDQ_TRY(check_dtype(x_dtype, "x_dtype"));
+    SVDQ_TRY(check_dtype(mod_dtype, "mod_dtype"));
+    SVDQ_TRY(check_dtype(out_dtype, "out_dtype"));
+    const size_t xsz = x_dtype == SVDQ_DT_BF16 ? 2 : 4, osz = out_dtype == SVDQ_DT_BF16 ? 2 : 4;
+    const size_t msz = mod_dtype == SVDQ_DT_BF16 ? 2 : 4;
+    size_t ysz = 4;
+    SVDQ_TRY(check_buf(x, "x", xsz, M == 0));
+    SVDQ_TRY(check_stride(x_stride, C, "x_stride"));
+    if (y != nullptr) {
+        SVDQ_TRY(check_dtype(y_dtype, "y_dtype"));
+        ysz = y_dtype == SVDQ_DT_BF16 ? 2 : 4;
+        SVDQ_TRY(check_ptr(y, "y", ysz));
+        SVDQ_TRY(check_stride(y_stride, C, "y_stride"));
+    } else if (M > 0 && (mod_gate != nullptr || x_out != nullptr)) {
+        return fail(SVDQ_ERR_INVALID_ARG, "y is NULL but mod_gate or x_out is not");
+    }
+    SVDQ_TRY(check_optional(weight, "weight", 2));
+    SVDQ_TRY(check_optional(bias, "bias", 2));
+    if (seg_start == nullptr) {
+        if (n_segments != 1)
+            return fail(SVDQ_ERR_INVALID_ARG, "seg_start is NULL but n_segments is %d, not 1", n_segments);
+    } else {
+        SVDQ_TRY(check_ptr(seg_start, "seg_start", 4));
+    }
+    SVDQ_TRY(check_optional(mod_gate, "mod_gate", msz));
+    SVDQ_TRY(check_optional(mod_scale, "mod_scale", msz));
+    SVDQ_TRY(check_optional(mod_shift, "mod_shift", msz));
+    if (mod_gate != nullptr || mod_scale != nullptr || mod_shift != nullptr)
+        SVDQ_TRY(check_stride(mod_stride, C, "mod_stride"));
+    if (x_out != nullptr) {
+        SVDQ_TRY(check_ptr(x_out, "x_out", xsz));
+        SVDQ_TRY(check_stride(x_out_stride, C, "x_out_stride"));
+        if (x_out == x && x_out_stride != x_stride)
+            return fail(SVDQ_ERR_INVALID_ARG, "x_out is x but their strides differ");
+        if (x_out == y && (x_out_stride != y_stride || x_dtype != y_dtype))
+            return fail(SVDQ_ERR_INVALID_ARG, "x_out is y but their types or strides differ");
+        if (x_out == out) return fail(SVDQ_ERR_INVALID_ARG, "x_out is out");
+    }
+    SVDQ_TRY(check_buf(out, "out", osz, M == 0));
+    SVDQ_TRY(check_stride(out_stride, C, "out_stride"));
+    if (out != nullptr && out == x && (out_dtype != x_dtype || out_stride != x_stride))
+        return fail(SVDQ_ERR_INVALID_ARG, "out is x but their types or strides differ");
+    if (out != nullptr && out == y && (out_dtype != y_dtype || out_stride != y_stride))
+        return fail(SVDQ_ERR_INVALID_ARG, "out is y but their types or strides differ");
+    const auto fours = [](const void* p, int64_t stride, size_t esz) {
+        return p == nullptr || (aligned(p, 4 * esz) && stride % 4 == 0);
+    };
+    const bool vec = C % 4 == 0 && fours(x, x_stride, xsz) && fours(y, y_stride, ysz) && fours(weight, 0, 2) &&
+                     fours(bias, 0, 2) && fours(mod_gate, mod_stride, msz) && fours(mod_scale, mod_stride, msz) &&
+                     fours(mod_shift, mod_stride, msz) && fours(x_out, x_out_stride, xsz) && fours(out, out_stride, osz);
+    if (!vec && C > 8192)
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "C %d exceeds 8192, the maximum for rows that do not take accesses of "
+                                                 "4 elements", C);
+    SVDQ_TRY(check_current_device());
+    if (M == 0 || n_segments == 0) return SVDQ_OK;
+    svdq::LayerNormArgs a{};
+    a.M = M; a.C = C; a.n_segments = n_segments; a.eps = eps;
+    a.x_bf16 = x_dtype == SVDQ_DT_BF16 ? 1 : 0;
+    a.x = x; a.x_stride = x_stride;
+    a.y_bf16 = y != nullptr && y_dtype == SVDQ_DT_BF16 ? 1 : 0;
+    a.y = y; a.y_stride = y_stride;
+    a.weight = weight; a.bias = bias;
+    a.starts = seg_start;
+    a.mod_bf16 = mod_dtype == SVDQ_DT_BF16 ? 1 : 0;
+    a.mod_gate = mod_gate; a.mod_scale = mod_scale; a.mod_shift = mod_shift; a.mod_stride = mod_stride;
+    a.x_out = x_out; a.x_out_stride = x_out_stride;
+    a.out_bf16 = out_dtype == SVDQ_DT_BF16 ? 1 : 0;
+    a.out = out; a.out_stride = out_stride;
+    a.vec = vec;
+    svdq::launch_layer_norm(a, reinterpret_cast<hipStream_t>(stream));
+    return after_launch("svdq_layer_norm");
+}
+
+svdq_status svdq_rotary(int64_t M, int32_t n_q_heads, int32_t n_k_heads, int32_t head_dim, int32_t n_axes,
+                        const int32_t* axis_pairs, int32_t pairing, const float* positions, int64_t pos_stride,
+                        const double* freqs, float eps, const void* q_weight, const void* k_weight,
+                        int32_t x_dtype, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        int32_t out_dtype, void* q_out, int64_t q_out_stride, void* k_out,
+                        int64_t k_out_stride, svdq_stream_t stream) {
+    if (M < 0) return fail(SVDQ_ERR_INVALID_ARG, "M = %lld is negative", (long long)M);
+    if (n_q_heads < 0 || n_k_heads < 0)
+        return fail(SVDQ_ERR_INVALID_ARG, "n_q_heads %d and n_k_heads %d must not be negative", n_q_heads, n_k_heads);
+    if (M > (int64_t)1 << 24 || n_q_heads > 1 << 16 || n_k_heads > 1 << 16)
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "M = %lld, n_q_heads = %d, n_k_heads = %d too large for one launch",
+                    (long long)M, n_q_heads, n_k_heads);
+    if (head_dim <= 0 || head_dim % 2 != 0)
+        return fail(SVDQ_ERR_INVALID_ARG, "head_dim %d must be a positive multiple of 2", head_dim);
+    if (head_dim > 256)
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "head_dim %d exceeds the supported maximum 256", head_dim);
+    if (n_axes < 1) return fail(SVDQ_ERR_INVALID_ARG, "n_axes %d must be positive", n_axes);
+    if (n_axes > 4) return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "n_axes %d exceeds the supported maximum 4", n_axes);
+    SVDQ_TRY(check_ptr(axis_pairs, "axis_pairs", 4));
+    svdq::RotaryArgs a{};
+    int64_t pairs = 0;
+    for (int i = 0; i < 4; ++i) {
+        if (i < n_axes) {
+            if (axis_pairs[i] < 0) return fail(SVDQ_ERR_INVALID_ARG, "axis_pairs[%d] = %d is negative", i, axis_pairs[i]);
+            pairs += axis_pairs[i];
+        }
+        a.ends[i] = i < n_axes - 1 && pairs < head_dim / 2 ? (int)pairs : head_dim / 2;
+    }
+    if (pairs != head_dim / 2)
+        return fail(SVDQ_ERR_INVALID_ARG, "axis_pairs sum to %lld, not to head_dim / 2 = %d", (long long)pairs, head_dim / 2);
+    if (pairing != SVDQ_ROTARY_INTERLEAVED && pairing != SVDQ_ROTARY_HALVES)
+        return fail(SVDQ_ERR_INVALID_ARG, "pairing %d is not a svdq_rotary_pairing value", pairing);
+    SVDQ_TRY(check_buf(positions, "positions", 4, M == 0));
+    SVDQ_TRY(check_stride(pos_stride, n_axes, "pos_stride"));
+    SVDQ_TRY(check_ptr(freqs, "freqs", 8));
+    SVDQ_TRY(check_optional(q_weight, "q_weight", 2));
+    SVDQ_TRY(check_optional(k_weight, "k_weight", 2));
+    if ((q_weight != nullptr || k_weight != nullptr) && !(std::isfinite(eps) && eps > 0.0f))
+        return fail(SVDQ_ERR_INVALID_ARG, "eps = %g must be finite and positive", (double)eps);
+    SVDQ_TRY(check_dtype(x_dtype, "x_dtype"));
+    SVDQ_TRY(check_dtype(out_dtype, "out_dtype"));
+    const int64_t xsz = x_dtype == SVDQ_DT_BF16 ? 2 : 4, osz = out_dtype == SVDQ_DT_BF16 ? 2 : 4;
+    bool vec = head_dim % (pairing == SVDQ_ROTARY_HALVES ? 16 : 8) == 0;
+    const auto rows = [&](const void* in, int64_t stride, const void* to, int64_t to_stride, int64_t heads, const char* in_name,
+                          const char* stride_name, const char* to_name, const char* to_stride_name) -> svdq_status {
+        if (heads == 0) return SVDQ_OK;
+        SVDQ_TRY(check_buf(in, in_name, xsz, M == 0));
+        SVDQ_TRY(check_stride(stride, heads * head_dim, stride_name));
+        SVDQ_TRY(check_buf(to, to_name, osz, M == 0));
+        SVDQ_TRY(check_stride(to_stride, heads * head_dim, to_stride_name));
+        if (in != nullptr && in == to && (x_dtype != out_dtype || stride != to_stride))
+            return fail(SVDQ_ERR_INVALID_ARG, "%s is %s but their types or strides differ", to_name, in_name);
+        vec = vec && aligned(in, 16) && aligned(to, 16) && stride * xsz % 16 == 0 && to_stride * osz % 16 == 0;
+        return SVDQ_OK;
+    };
+    SVDQ_TRY(rows(q, q_stride, q_out, q_out_stride, n_q_heads, "q", "q_stride", "q_out", "q_out_stride"));
+    SVDQ_TRY(rows(k, k_stride, k_out, k_out_stride, n_k_heads, "k", "k_stride", "k_out", "k_out_stride"));
+    SVDQ_TRY(check_current_device());
+    if (M == 0 || n_q_heads + n_k_heads == 0) return SVDQ_OK;
+    a.M = M; a.q_heads = n_q_heads; a.k_heads = n_k_heads; a.D = head_dim; a.n_axes = n_axes;
+    a.halves = pairing == SVDQ_ROTARY_HALVES ? 1 : 0;
+    a.pos = positions; a.pos_stride = pos_stride; a.freqs = freqs;
+    a.eps = eps; a.q_weight = q_weight; a.k_weight = k_weight;
+    a.x_bf16 = x_dtype == SVDQ_DT_BF16 ? 1 : 0;
+    a.q = q; a.q_stride = q_stride; a.k = k; a.k_stride = k_stride;
+    a.out_bf16 = out_dtype == SVDQ_DT_BF16 ? 1 : 0;
+    a.q_out = q_out; a.q_out_stride = q_out_stride; a.k_out = k_out; a.k_out_stride = k_out_stride;
+    a.vec = vec;
+    svdq::launch_rotary(a, reinterpret_cast<hipStream_t>(stream));
+    return after_launch("svdq_rotary");
+}
+
+svdq_status svdq_attention_workspace_bytes(int64_t Mq, int64_t Mkv, int32_t n_heads, int32_t n_kv_heads,
+                                           int32_t head_dim, int32_t n_segments, int64_t* bytes) {
+    SVDQ_TRY(check_attention(Mq, Mkv, n_heads, n_kv_heads, head_dim, n_segments));
+    if (bytes == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = svdq::attention_workspace_bytes(Mq, Mkv, n_heads, n_kv_heads, head_dim, n_segments);
+    return SVDQ_OK;
+}
+
+svdq_status svdq_attention(int64_t Mq, int64_t Mkv, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                           int32_t n_segments, float scale, float cap, int32_t mask, const int32_t* q_start,
+                           const int32_t* kv_start, const int32_t* prefix, const float* slopes, const void* q,
+                           int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           void* out, int64_t out_stride, void* workspace, int64_t workspace_bytes,
+                           svdq_stream_t stream) {
+    SVDQ_TRY(check_attention(Mq, Mkv, n_heads, n_kv_heads, head_dim, n_segments));
+    if (!(std::isfinite(scale) && scale > 0.0f))
+        return fail(SVDQ_ERR_INVALID_ARG, "scale = %g must be finite and positive", (double)scale);
+    if (!(std::isfinite(cap) && cap >= 0.0f))
+        return fail(SVDQ_ERR_INVALID_ARG, "cap = %g must be finite and not negative", (double)cap);
+    if (mask != SVDQ_MASK_NONE && mask != SVDQ_MASK_CAUSAL)
+        return fail(SVDQ_ERR_INVALID_ARG, "mask %d is not a svdq_mask value", mask);
+    if (prefix != nullptr && mask != SVDQ_MASK_CAUSAL)
+        return fail(SVDQ_ERR_INVALID_ARG, "prefix is not NULL but mask is not SVDQ_MASK_CAUSAL");
+    SVDQ_TRY(check_ptr(q_start, "q_start", 4));
+    SVDQ_TRY(check_ptr(kv_start, "kv_start", 4));
+    SVDQ_TRY(check_optional(prefix, "prefix", 4));
+    SVDQ_TRY(check_optional(slopes, "slopes", 4));
+    const int64_t qw = (int64_t)n_heads * head_dim, kw = (int64_t)n_kv_heads * head_dim;
+    SVDQ_TRY(check_head_rows(q, "q", q_stride, "q_stride", qw, Mq == 0));
+    SVDQ_TRY(check_head_rows(k, "k", k_stride, "k_stride", kw, Mkv == 0));
+    SVDQ_TRY(check_head_rows(v, "v", v_stride, "v_stride", kw, Mkv == 0));
+    SVDQ_TRY(check_head_rows(out, "out", out_stride, "out_stride", qw, Mq == 0));
+    SVDQ_TRY(check_workspace(workspace, workspace_bytes,
+                             svdq::attention_workspace_bytes(Mq, Mkv, n_heads, n_kv_heads, head_dim, n_segments)));
+    SVDQ_TRY(check_current_device());
+    if (Mq == 0 || n_segments == 0) return SVDQ_OK;
+    svdq::AttentionArgs a{};
+    a.Mq = Mq; a.Mk = Mkv;
+    a.H = n_heads; a.G = n_kv_heads; a.D = head_dim; a.n = n_segments;
+    a.scale = scale; a.cap = cap;
+    a.causal = mask == SVDQ_MASK_CAUSAL ? 1 : 0;
+    a.q_start = q_start; a.kv_start = kv_start; a.prefix = prefix; a.slopes = slopes;
+    a.q = q; a.q_stride = q_stride; a.k = k; a.k_stride = k_stride; a.v = v; a.v_stride = v_stride;
+    a.out = out; a.out_stride = out_stride;
+    a.work = workspace;
+    svdq::launch_attention(a, reinterpret_cast<hipStream_t>(stream));
+    return after_launch("svdq_attention");
 }
 
 svdq_status svdq_peak_mfma(int32_t kind, int32_t iters, float* out, int64_t* ops,

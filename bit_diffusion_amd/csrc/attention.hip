@@ -1,0 +1,509 @@
+// attention.hip -- softmax attention of packed requests: rows of segment i see the keys of segment
+// i, in grouped heads (H heads share G kv heads, H / G = rep to one).
+//
+//   s_ij = scale q_i . k_j,  capped:  s = cap tanh(s / cap),  biased:  s -= slope_h |i + off - j|,
+//   out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(s_ij - max_j s_ij) over the keys j that i sees:
+//   all of the segment, or j < max(prefix, i + off + 1), off = keys - rows of the segment.
+//
+// One pass over the keys with the running maximum and sum of each row (fp32), tiles of 64 keys.
+//
+// Rows.  A workgroup owns up to 128 rows of one segment and one kv head: position major, the rep
+// heads that share the kv head within (so single tokens fill rep rows of a tile, and its keys are
+// read once for all of them).  Each of its 4 waves takes 32 rows and all keys.  The grid is the
+// most tiles any cut of the rows can need; every workgroup finds its own by a prefix sum over the
+// offsets in device memory.
+//
+// Products.  Both are 32x32x16 bf16 MFMAs, transposed: S^T = K Q^T and O^T = V^T P^T, so that a lane
+// holds scores of one row only: row maximum and sum stay in the lane but for its other half (the
+// lane 32 further), and what the first product leaves in registers is already the second one's
+// operand, keys in the order 4 h to 4 h + 3, 8 + 4 h to 8 + 4 h + 3 of every 16 (h the lane's
+// half).  V^T comes out of LDS in that order by the transposing read ds_read_b64_tr_b16.  P is
+// rounded to bf16 (2^-9 of each weight at most, against V's own 2^-9), its sum is of the unrounded
+// values; O, maxima and sums are fp32.
+//
+// Maximum.  O is rescaled only where a row's maximum grew by more than 2^8 since the last time
+// (always at its first key): weights are at most 2^8 then, far from fp32's and bf16's ends, and
+// most tiles skip the 16 multiplications a lane and block of 32 channels.
+//
+// LDS.  K and V tiles, rows of 64 or 128 channels, twice each: the next tile's copies (LDS DMA,
+// 16 bytes a lane) fly while this one is multiplied, one barrier a tile.  The 16-byte slots of a
+// row are exclusive-ored with the row (K: for 16 rows of one channel slot; V: for 4 rows of 32
+// channels), which the copies do by their source addresses.
+//
+// Masks.  A row sees the keys below its limit, so only a wave's tiles between its least and its
+// largest limit are masked.  There, and in a segment's last tile, values of V that are not finite
+// must not meet a weight 0: they are multiplied as 0, and counted in a second product over who sees
+// them (poison below).
+//
+// Few rows: the keys of a tile are split over several workgroups, whose maxima, sums and O go to
+// the workspace and are joined by a second launch.
+#include "common.hpp"
+#include "launch.hpp"
+#include "segments.hpp"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace svdq {
+namespace {
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kRows = 32 * kWaves;   // rows of a workgroup
+constexpr int kKeys = 64;            // keys of a tile
+constexpr int kCus = 256;            // of the GPU
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGrow = 8.f;         // growth of a maximum, in powers of two, that O is rescaled for
+
+enum Mod { kPlain = 0, kCap = 1, kBias = 2, kBoth = 3 };
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) const bf16x8 lds_bf16x8;
+
+// Tile `want` of the segments' tiles of kRows rows (rep to a position), in order; the first row in
+// its segment, and the segment.  seg < 0: no such tile.
+struct Tile {
+    int seg, q0, len, row0;   // segment, its first row of q, its positions, the tile's first packed row
+};
+__device__ __forceinline__ int wave_scan(int v) {
+    v += dpp<kShr + 1>(0, v);
+    v += dpp<kShr + 2>(0, v);
+    v += dpp<kShr + 4>(0, v);
+    v += dpp<kShr + 8>(0, v);
+    v += dpp<kBcast15, 0xa>(0, v);
+    v += dpp<kBcast31, 0xc>(0, v);
+    return v;
+}
+__device__ __forceinline__ Tile find_tile(const AttentionArgs& a, int rep, int want) {
+    const int lane = threadIdx.x & 63, M = (int)a.Mq;
+    int before = 0;
+    for (int c = 0; c < a.n; c += 64) {
+        const int i = c + lane;
+        int r0 = 0, len = 0;
+        if (i < a.n) {
+            r0 = min(max(a.q_start[i], 0), M);
+            len = max(min(max(a.q_start[i + 1], 0), M) - r0, 0);
+        }
+        const int nt = (len * rep + kRows - 1) / kRows, sum = wave_scan(nt);
+        const unsigned long long past = __ballot(before + sum > want);
+        if (past != 0) {
+            const int src = __ffsll(past) - 1;
+            const int off = want - before - __builtin_amdgcn_readlane(sum - nt, src);
+            return Tile{c + src, __builtin_amdgcn_readlane(r0, src), __builtin_amdgcn_readlane(len, src), off * kRows};
+        }
+        before += __builtin_amdgcn_readlane(sum, 63);
+    }
+    return Tile{-1, 0, 0, 0};
+}
+
+__device__ __forceinline__ f32x16 mfma32(bf16x8 x, bf16x8 y, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, c, 0, 0, 0);
+}
+
+// The larger of the two halves' values, in both; NaN where either is.
+__device__ __forceinline__ float both_max(float v) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __builtin_elementwise_maximum(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ __forceinline__ float both_sum(float v) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+
+__device__ __forceinline__ uint64_t uniform_ptr(const void* p) {
+    const uint64_t v = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return ((uint64_t)hi << 32) | lo;
+}
+// Global -> LDS copy: each lane that is on moves the 16 bytes at base + off to LDS address lds +
+// 16 lane.  In asm so that the compiler does not wait for every copy in flight before each LDS
+// read; wait_copies does.  An LDS copy that reads M0 right after its write needs one wait state.
+__device__ __forceinline__ void copy16(uint64_t base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :: "v"(off), "s"(base), "s"(lds) : "memory");
+}
+// Every copy of this wave has landed, and every LDS access before is done.
+__device__ __forceinline__ void wait_copies() { __builtin_amdgcn_s_waitcnt(0x0070); }
+__device__ __forceinline__ void barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// NB: blocks of 32 channels (D <= 32 NB, the rest counts as zero).
+template <int NB>
+struct Lds {
+    static constexpr int kRow = NB <= 2 ? 128 : 256;             // bytes of a row
+    static constexpr int kSlots = kRow / 16;
+    static constexpr int kTile = kKeys * kRow;
+    // 16-byte slot of channel slot `s` in row `r`
+    static __device__ __forceinline__ int k_slot(int r, int s) { return s ^ (kSlots == 16 ? r & 15 : (r >> 1) & 7); }
+    static __device__ __forceinline__ int v_slot(int r, int s) { return s ^ (kSlots == 16 ? (r & 3) << 2 : ((r >> 1) & 1) << 2); }
+};
+
+// One wave's rows.
+template <int NB, int MOD>
+struct Rows {
+    f32x16 O[NB];      // O^T: lane (h, row) has channels 32 b + 8 (i / 4) + 4 h + i % 4
+    bf16x8 Q[2 * NB];  // channels 16 c + 8 h to + 7 of the lane's row
+    float m, l;        // maximum of the row's scores (MOD = kPlain: unscaled; else times log2 e), this half's sum
+    int limit;         // keys that the row sees
+    int at;            // the key at distance 0
+    float slope;       // times log2 e
+    float c0, c1, c2;  // kPlain, kBias: c0 = scale log2 e; with cap: 2 scale log2 e / cap, cap log2 e, 2 cap log2 e
+
+    // scores of 32 keys from key0 on to the exponent's domain
+    template <bool MASK>
+    __device__ __forceinline__ void score(f32x16& s, int key0, int h) const {
+        const float far = (float)(key0 + 4 * h - at);
+        const int seen = limit - key0 - 4 * h;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int key = 8 * (i >> 2) + (i & 3);   // from the lane's first one on
+            float x = s[i];
+            if constexpr ((MOD & kCap) != 0)
+                x = c1 - c2 * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * c0) + 1.f);
+            else if constexpr (MOD == kBias) x *= c0;
+            if constexpr ((MOD & kBias) != 0) x = fmaf(-slope, fabsf(far + (float)key), x);
+            if constexpr (MASK) x = key < seen ? x : -INFINITY;
+            s[i] = x;
+        }
+    }
+};
+
+// Words of two bf16: those that are not finite become 0.
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+    const uint32_t lo = (w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu;
+    return ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u) | lo;
+}
+// Of a bf16: 1 for infinity, 2^8 for minus infinity, 2^16 for a NaN, else 0, as bf16.
+__device__ __forceinline__ uint32_t kind16(uint32_t v) {
+    const uint32_t bad = (v & 0x7F80u) == 0x7F80u;
+    const uint32_t k = (v & 0x7Fu) != 0 ? 0x4780u : (v & 0x8000u) != 0 ? 0x4380u : 0x3F80u;
+    return bad ? k : 0u;
+}
+
+template <int NB>
+__device__ __forceinline__ uint4 v_operand(uint32_t vbase, int b, int kc) {
+    // keys 16 kc + 4 h to + 3 and 8 further of the lane's channel in block b
+    using L = Lds<NB>;
+    const uint32_t at = (vbase ^ (uint32_t)(b * 64)) + kc * 16 * L::kRow;
+    const uint2 x = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_u8*)(uintptr_t)at));
+    const uint2 y = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_u8*)(uintptr_t)(at + 8 * L::kRow)));
+    return make_uint4(x.x, x.y, y.x, y.y);
+}
+
+// A tile of 64 keys from key0 on: kb, vb the lane's read addresses in this tile's buffers.
+template <int NB, int MOD, bool MASK>
+__device__ __forceinline__ void step(Rows<NB, MOD>& w, int key0, uint32_t kb, uint32_t vb) {
+    using L = Lds<NB>;
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    f32x16 s[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[u][i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2 * NB; ++c) {
+            const bf16x8 k = *(lds_bf16x8*)(lds_u8*)(uintptr_t)((kb ^ (uint32_t)(c * 32)) + u * 32 * L::kRow);
+            s[u] = mfma32(k, w.Q[c], s[u]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+        if (MASK || MOD != kPlain) w.template score<MASK>(s[u], key0 + 32 * u, h);
+    float top = s[0][0];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = __builtin_elementwise_maximum(top, s[u][i]);
+    top = both_max(top);
+    const float unit = MOD == kPlain ? w.c0 : 1.f;
+    if (__any((top - w.m) * unit > kGrow)) {
+        const float m = __builtin_elementwise_maximum(w.m, top);
+        const float keep = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((w.m - m) * unit);
+        w.m = m;
+        w.l *= keep;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w.O[b][i] *= keep;
+    }
+    const float base = w.m == -INFINITY ? 0.f : -w.m * unit;
+    uint4 P[4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            s[u][i] = __builtin_amdgcn_exp2f(fmaf(s[u][i], unit, base));
+            w.l += s[u][i];
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            P[2 * u + c] = make_uint4(pack_bf16(s[u][8 * c], s[u][8 * c + 1]), pack_bf16(s[u][8 * c + 2], s[u][8 * c + 3]),
+                                      pack_bf16(s[u][8 * c + 4], s[u][8 * c + 5]), pack_bf16(s[u][8 * c + 6], s[u][8 * c + 7]));
+    }
+    uint32_t bad = 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            uint4 v = v_operand<NB>(vb, b, c);
+            if constexpr (MASK) {
+                const uint4 f = make_uint4(finite_only(v.x), finite_only(v.y), finite_only(v.z), finite_only(v.w));
+                bad |= (f.x ^ v.x) | (f.y ^ v.y) | (f.z ^ v.z) | (f.w ^ v.w);
+                v = f;
+            }
+            w.O[b] = mfma32(as_bf16x8(v), as_bf16x8(P[c]), w.O[b]);
+        }
+    if constexpr (MASK) {
+        // who sees how many infinities, minus infinities and NaN (at most 64 of each: exact in fp32)
+        if (__any(bad != 0)) {
+#pragma unroll 1
+            for (int b = 0; b < NB; ++b) {
+                f32x16 n;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) n[i] = 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 v = v_operand<NB>(vb, b, c);
+                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t e[4], one[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        e[j] = kind16(vw[j] & 0xFFFFu) | kind16(vw[j] >> 16) << 16;
+                        const int key = key0 + 16 * c + 8 * (j >> 1) + 4 * h + 2 * (j & 1);
+                        one[j] = (key < w.limit ? 0x3F80u : 0u) | (key + 1 < w.limit ? 0x3F800000u : 0u);
+                    }
+                    n = mfma32(as_bf16x8(make_uint4(e[0], e[1], e[2], e[3])), as_bf16x8(make_uint4(one[0], one[1], one[2], one[3])), n);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int k = (int)n[i];
+                    const bool up = (k & 0xFF) != 0, down = (k & 0xFF00) != 0;
+                    const float add = k >= 1 << 16 || (up && down) ? NAN : up ? INFINITY : down ? -INFINITY : 0.f;
+#pragma unroll
+                    for (int bb = 0; bb < NB; ++bb)
+                        if (bb == b) w.O[bb][i] += add;
+                }
+            }
+        }
+    }
+}
+
+// Where a split's O, maximum and sum of row (position m, head h) stand in the workspace.
+__device__ __forceinline__ int64_t part_row(const AttentionArgs& a, int split, int64_t m, int h) {
+    return ((int64_t)split * a.Mq + m) * a.H + h;
+}
+
+template <int NB, int MOD>
+__global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a) {
+    using L = Lds<NB>;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * L::kTile];   // K, V, K, V
+    const int lane = threadIdx.x & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rep = a.H / a.G, D = a.D;
+
+    // consecutive workgroups go to the 8 XCDs in turn: give each XCD whole runs of a kv head's tiles
+    const int total = (int)gridDim.x;
+    const int xcd = blockIdx.x & 7, lo = total >> 3, more = total & 7;
+    const int item = xcd * lo + min(xcd, more) + (int)(blockIdx.x >> 3);
+    const int split = item % a.splits, gt = item / a.splits, g = gt / a.tiles;
+    // last rows first: with a causal mask they have the most keys
+    const Tile t = find_tile(a, rep, a.causal ? a.tiles - 1 - (gt - g * a.tiles) : gt - g * a.tiles);
+    if (t.seg < 0) return;
+    const int Mk = (int)a.Mk, k0 = min(max(a.kv_start[t.seg], 0), Mk);
+    const int klen = max(min(max(a.kv_start[t.seg + 1], 0), Mk) - k0, 0);
+    const int rows = min(kRows, t.len * rep - t.row0);
+    const int prefix = a.prefix == nullptr ? 0 : min(max(a.prefix[t.seg], 0), klen), off = klen - t.len;
+    auto limit_of = [&](int row) {
+        return a.causal ? min(max(max(prefix, row / rep + off + 1), 0), klen) : klen;
+    };
+
+    // the lane's row, or the last one's again
+    const bool active = wave * 32 < rows;
+    const int row = t.row0 + min(wave * 32 + (lane & 31), rows - 1);
+    const int pos = row / rep, head = g * rep + row - pos * rep;
+    Rows<NB, MOD> w;
+    w.m = -INFINITY;
+    w.l = 0.f;
+    w.limit = limit_of(row);
+    w.at = pos + off;
+    w.slope = (MOD & kBias) != 0 ? a.slopes[head] * kLog2e : 0.f;
+    w.c0 = a.scale * kLog2e;
+    w.c1 = a.cap * kLog2e;
+    w.c2 = 2.f * w.c1;
+    if ((MOD & kCap) != 0) w.c0 *= 2.f / a.cap;
+    const uint16_t* qp = (const uint16_t*)a.q + (t.q0 + pos) * a.q_stride + (int64_t)head * D;
+#pragma unroll
+    for (int c = 0; c < 2 * NB; ++c) {
+        const int ch = 16 * c + 8 * h;
+        w.Q[c] = as_bf16x8(ch < D ? *(const uint4*)(qp + ch) : make_uint4(0u, 0u, 0u, 0u));
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w.O[b][i] = 0.f;
+
+    // tiles of the workgroup, and the wave's tiles without a mask (to least) and with keys (to most)
+    const int least = limit_of(t.row0 + min(wave * 32, rows - 1));
+    const int most = limit_of(t.row0 + min(wave * 32 + 31, rows - 1));
+    const int tiles = (limit_of(t.row0 + rows - 1) + kKeys - 1) / kKeys, per = (tiles + a.splits - 1) / a.splits;
+    const int first = split * per, last = min(first + per, tiles);
+
+    // copies: an instruction fills 1 KB, kRow of them a row
+    constexpr int kLanes = L::kSlots, kStep = 64 / kLanes;   // lanes of a row, rows of an instruction
+    constexpr int kCopies = kKeys / kStep / kWaves;          // of a wave, for each of K and V
+    const int crow = wave * kCopies * kStep + lane / kLanes, cslot = lane % kLanes;
+    const uint32_t smem0 = (uint32_t)(uintptr_t)(lds_u8*)smem;
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(smem0 + wave * kCopies * 1024);
+    const uint32_t kbytes = (uint32_t)(a.k_stride * 2), vbytes = (uint32_t)(a.v_stride * 2);
+    const char* kp = (const char*)a.k + ((int64_t)k0 * a.k_stride + (int64_t)g * D) * 2;
+    const char* vp = (const char*)a.v + ((int64_t)k0 * a.v_stride + (int64_t)g * D) * 2;
+    auto copy_tile = [&](int tile, int buf) {
+        const uint64_t kt = uniform_ptr(kp + (int64_t)tile * kKeys * kbytes), vt = uniform_ptr(vp + (int64_t)tile * kKeys * vbytes);
+        const int most_row = klen - 1 - tile * kKeys;   // keys past the segment's: its last again
+#pragma unroll
+        for (int j = 0; j < kCopies; ++j) {
+            const int r = crow + j * kStep, from = min(r, most_row);
+            const int ks = L::k_slot(r, cslot), vs = L::v_slot(r, cslot);
+            const uint32_t to = lds0 + buf * 2 * L::kTile + j * 1024;
+            if (ks * 8 < D) copy16(kt, from * kbytes + ks * 16, to);
+            if (vs * 8 < D) copy16(vt, from * vbytes + vs * 16, to + L::kTile);
+        }
+    };
+    // channels past D: zeros, which no copy overwrites
+    if (D < L::kRow / 2) {
+        for (int i = threadIdx.x; i < 4 * L::kTile / 16; i += kThreads) *(uint4*)(smem + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+    }
+    // the lane's reads of K (row lane % 32, slot h of every 2) and of V (4 lanes to a row of 16 channels)
+    const uint32_t kr = (lane & 31) * L::kRow + L::k_slot(lane & 31, h) * 16;
+    const int vrow = 4 * h + ((lane >> 2) & 3);
+    const uint32_t vr = vrow * L::kRow + L::v_slot(vrow, ((lane >> 4) & 1) * 2 + ((lane >> 1) & 1)) * 16 + (lane & 1) * 8;
+
+    if (first < last) copy_tile(first, 0);
+    for (int tile = first; tile < last; ++tile) {
+        const int buf = (tile - first) & 1;
+        wait_copies();
+        barrier();   // this tile is there, and the other buffer has been read
+        if (tile + 1 < last) copy_tile(tile + 1, buf ^ 1);
+        const uint32_t at = smem0 + buf * 2 * L::kTile;
+        if (active && tile * kKeys < most) {
+            if (tile * kKeys + kKeys <= least) step<NB, MOD, false>(w, tile * kKeys, at + kr, at + L::kTile + vr);
+            else step<NB, MOD, true>(w, tile * kKeys, at + kr, at + L::kTile + vr);
+        }
+    }
+    if (!active || wave * 32 + (lane & 31) >= rows) return;
+    w.l = both_sum(w.l);
+    if (a.splits > 1) {
+        const int64_t at = part_row(a, split, t.q0 + pos, head), all = (int64_t)a.splits * a.Mq * a.H;
+        float* ml = (float*)a.work + all * D + at * 2;
+        if (h == 0) {
+            ml[0] = MOD == kPlain ? w.m * w.c0 : w.m;
+            ml[1] = w.l;
+        }
+        float* o = (float*)a.work + at * D;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const int ch = 32 * b + 2 * i + 4 * h;
+                if (ch < D) *(float4*)(o + ch) = make_float4(w.O[b][i], w.O[b][i + 1], w.O[b][i + 2], w.O[b][i + 3]);
+            }
+        return;
+    }
+    const float inv = w.l == 0.f ? 0.f : 1.f / w.l;   // a row that sees no key gives zeros
+    uint16_t* op = (uint16_t*)a.out + (t.q0 + pos) * a.out_stride + (int64_t)head * D;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const int ch = 32 * b + 2 * i + 4 * h;
+            if (ch < D)
+                *(uint2*)(op + ch) = make_uint2(pack_bf16(w.O[b][i] * inv, w.O[b][i + 1] * inv),
+                                                pack_bf16(w.O[b][i + 2] * inv, w.O[b][i + 3] * inv));
+        }
+}
+
+// Joins the splits of one row (position, head) a wave, in their order; lane: channels 2 lane, 2 lane + 1.
+__global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t r = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6), m = r / a.H;
+    if (m >= a.Mq) return;
+    const int head = (int)(r - m * a.H);
+    const int seg = find_segment(a.q_start, a.n, (int)m);
+    if (seg < 0 || a.q_start[seg + 1] <= m) return;
+    const int64_t all = (int64_t)a.splits * a.Mq * a.H;
+    const float* o = (const float*)a.work;
+    const float* ml = o + all * a.D;
+    float top = -INFINITY;
+    for (int s = 0; s < a.splits; ++s) top = __builtin_elementwise_maximum(top, ml[part_row(a, s, m, head) * 2]);
+    float l = 0.f, x = 0.f, y = 0.f;
+    for (int s = 0; s < a.splits; ++s) {
+        const int64_t at = part_row(a, s, m, head);
+        const float ms = ml[at * 2];
+        if (ms == -INFINITY) continue;
+        const float f = __builtin_amdgcn_exp2f(ms - top);
+        l = fmaf(ml[at * 2 + 1], f, l);
+        if (2 * lane < a.D) {
+            const float2 v = *(const float2*)(o + at * a.D + 2 * lane);
+            x = fmaf(v.x, f, x);
+            y = fmaf(v.y, f, y);
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (2 * lane < a.D)
+        *(uint32_t*)((uint16_t*)a.out + m * a.out_stride + (int64_t)head * a.D + 2 * lane) = pack_bf16(x * inv, y * inv);
+}
+
+// The most tiles that any cut of Mq positions into n segments can need.
+int64_t max_tiles(int64_t Mq, int rep, int n) {
+    return std::min(Mq * ((rep + kRows - 1) / kRows), (Mq * rep + (int64_t)n * (kRows - 1)) / kRows);
+}
+
+// Parts of a tile's keys: enough for two workgroups a CU, each at least 4 tiles of keys of the longest
+// segment there may be.
+int split_count(int64_t Mq, int64_t Mk, int H, int G, int n) {
+    const int64_t items = max_tiles(Mq, H / G, n) * G;
+    if (items == 0) return 1;
+    const int64_t want = 2 * kCus / items, least = Mk / (4 * kKeys);
+    return (int)std::max<int64_t>(1, std::min(want, least));
+}
+
+template <int NB>
+void launch(const AttentionArgs& a, hipStream_t st) {
+    const dim3 grid((unsigned)(a.tiles * (int64_t)a.G * a.splits)), block(kThreads);
+    if (a.cap != 0.f && a.slopes != nullptr) hipLaunchKernelGGL((attention_kernel<NB, kBoth>), grid, block, 0, st, a);
+    else if (a.cap != 0.f) hipLaunchKernelGGL((attention_kernel<NB, kCap>), grid, block, 0, st, a);
+    else if (a.slopes != nullptr) hipLaunchKernelGGL((attention_kernel<NB, kBias>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((attention_kernel<NB, kPlain>), grid, block, 0, st, a);
+}
+
+}  // namespace
+
+bool attention_fits(int64_t Mq, int H, int G, int n) {
+    return max_tiles(Mq, H / G, n) * G < (int64_t)1 << 23 && Mq * H < (int64_t)1 << 25;
+}
+
+int64_t attention_workspace_bytes(int64_t Mq, int64_t Mk, int H, int G, int D, int n) {
+    const int splits = split_count(Mq, Mk, H, G, n);
+    return splits <= 1 ? 0 : splits * Mq * H * (D + 2) * 4;
+}
+
+void launch_attention(const AttentionArgs& in, hipStream_t st) {
+    AttentionArgs a = in;
+    a.tiles = (int)max_tiles(a.Mq, a.H / a.G, a.n);
+    a.splits = split_count(a.Mq, a.Mk, a.H, a.G, a.n);
+    if (a.D <= 32) launch<1>(a, st);
+    else if (a.D <= 64) launch<2>(a, st);
+    else if (a.D <= 96) launch<3>(a, st);
+    else launch<4>(a, st);
+    if (a.splits > 1) {
+        const int64_t rows = a.Mq * a.H;
+        hipLaunchKernelGGL(attention_join_kernel, dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a);
+    }
+}
+
+}  // namespace svdq

@@ -122,6 +122,78 @@ struct GroupNormArgs {
     int vec;                 // x and out take 16-byte accesses
 };
 
+struct LayerNormArgs {
+    int64_t M;
+    int C, n_segments;
+    float eps;
+    int x_bf16;              // type of x and x_out: 0 fp32, 1 bf16
+    const void* x;           // [M, C]
+    int64_t x_stride;
+    int y_bf16;
+    const void* y;           // [M, C] or NULL
+    int64_t y_stride;
+    const void* weight;      // bf16 [C] or NULL
+    const void* bias;
+    const int* starts;       // [n_segments + 1], or NULL: all rows are segment 0
+    int mod_bf16;
+    const void* mod_gate;    // [n_segments, C] each, or NULL
+    const void* mod_scale;
+    const void* mod_shift;
+    int64_t mod_stride;
+    void* x_out;             // [M, C] or NULL
+    int64_t x_out_stride;
+    int out_bf16;
+    void* out;
+    int64_t out_stride;
+    int vec;                 // every row takes accesses of 4 elements
+};
+
+struct RotaryArgs {
+    int64_t M;
+    int q_heads, k_heads, D;
+    int n_axes;
+    int ends[4];             // pairs up to and with axis a (n_axes to 3: D / 2)
+    int halves;              // pairs (i, i + D / 2) and not (2 i, 2 i + 1)
+    const float* pos;        // [M, n_axes]
+    int64_t pos_stride;
+    const double* freqs;     // [D / 2]
+    float eps;
+    const void* q_weight;    // bf16 [D] or NULL: no norm
+    const void* k_weight;
+    int x_bf16;
+    const void* q;           // [M, q_heads D]
+    int64_t q_stride;
+    const void* k;
+    int64_t k_stride;
+    int out_bf16;
+    void* q_out;
+    int64_t q_out_stride;
+    void* k_out;
+    int64_t k_out_stride;
+    int vec;                 // rows take 16-byte accesses of 8 channels (pairs of 4)
+};
+
+struct AttentionArgs {
+    int64_t Mq, Mk;
+    int H, G, D, n;          // heads, kv heads, head dimension, segments
+    float scale, cap;        // cap 0: none
+    int causal;
+    const int* q_start;      // [n + 1]
+    const int* kv_start;
+    const int* prefix;       // [n] or NULL
+    const float* slopes;     // [H] or NULL
+    const void* q;           // bf16 [Mq, H D]
+    int64_t q_stride;
+    const void* k;           // bf16 [Mk, G D]
+    int64_t k_stride;
+    const void* v;
+    int64_t v_stride;
+    void* out;               // bf16 [Mq, H D]
+    int64_t out_stride;
+    void* work;
+    int splits, tiles;       // parts of a tile's keys, and the most row tiles (set by the launcher)
+};
+
 // Largest workspace the K split of svdq_gemm_w4a4_packed uses (its split count is capped so
 // that the partial tiles fit).
 constexpr int64_t kSplitWorkspaceMax = (int64_t)64 << 20;
@@ -161,6 +233,17 @@ void launch_lora_batch(const LoraBatchArgs& a, hipStream_t st);
 // group normalisation of channels-last images (group_norm.hip)
 int64_t group_norm_workspace_bytes(int64_t B, int64_t rows, int C, int groups);
 void launch_group_norm(const GroupNormArgs& a, hipStream_t st);
+
+// residual, layer norm and modulation of packed rows (layer_norm.hip)
+void launch_layer_norm(const LayerNormArgs& a, hipStream_t st);
+
+// rotary positions with several axes (rotary.hip)
+void launch_rotary(const RotaryArgs& a, hipStream_t st);
+
+// attention of packed requests (attention.hip)
+bool attention_fits(int64_t Mq, int H, int G, int n);   // one launch's grid
+int64_t attention_workspace_bytes(int64_t Mq, int64_t Mk, int H, int G, int D, int n);
+void launch_attention(const AttentionArgs& a, hipStream_t st);
 
 // offline weight quantization (weights.hip)
 void launch_calib_absmax(int64_t M, int K, const void* x, float* absmax, hipStream_t st);

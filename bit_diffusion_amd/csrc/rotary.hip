@@ -1,0 +1,255 @@
+// rotary.hip -- the q and k heads of a fused q, k, v linear made ready for attention: an optional
+// RMS norm over each head's D channels, then every channel pair (a, b) turned by its angle,
+//   (a cos t - b sin t, a sin t + b cos t),  t = positions[row, axis of the pair] freqs[pair],
+// the pairs dealt over up to four axes (time, height, width, ...) in order.
+//
+// Angles.  t reaches 1e6 and more where frames lie far from the first, and a float holds it to
+// 2^-24 of that only.  So the product is formed in binary64, in turns, its whole turns are taken
+// off there, and the rest, at most half a turn, goes to sincospif.  One angle serves all heads of
+// its row: a workgroup fills a table of kRows rows x D / 2 pairs in LDS once and takes all heads
+// through it.
+//
+// Bound: memory, q and k once in and once out.  Aligned heads: a lane holds 8 channels (16 bytes
+// of bf16) in adjacent pairs, or 8 from either half, and a head is a group of 8, 16 or 32 lanes of
+// one wave, so the norm's sum needs no LDS; kItems heads a lane are in flight at a time.  Other
+// head widths and alignments: a wave takes a head, a lane single pairs.
+#include "common.hpp"
+#include "launch.hpp"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace svdq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kCus = 256;    // of the GPU
+constexpr int kMaxPairs = 128;
+constexpr int kRows = 4;     // rows of a workgroup, at most
+constexpr int kItems = 4;    // heads of a lane in flight
+
+// cos and sin of `rows` rows' angles: table[row][pair].
+__device__ __forceinline__ void fill_table(const RotaryArgs& a, int64_t row0, int rows, float2* table) {
+    const int P = a.D >> 1;
+    for (int i = threadIdx.x; i < rows * P; i += kThreads) {
+        const int r = i / P, p = i - r * P;
+        const int axis = (p >= a.ends[0]) + (p >= a.ends[1]) + (p >= a.ends[2]);
+        const double turns = (double)a.pos[(row0 + r) * a.pos_stride + axis] * a.freqs[p] * 0.15915494309189533577;
+        float s, c;
+        sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+        table[i] = make_float2(c, s);
+    }
+    __syncthreads();
+}
+
+// The sum over each LANES (8, 16, 32, 64) neighbouring lanes, in all of them.
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v) {
+    v += dpp<0xB1>(0.f, v);     // the neighbour
+    v += dpp<0x4E>(0.f, v);     // the other two of four
+    v += dpp<0x141>(0.f, v);    // the other half of eight, mirrored
+    if constexpr (LANES > 8) v += dpp<0x140>(0.f, v);
+    if constexpr (LANES > 16) v += __shfl_xor(v, 16, kWave);
+    if constexpr (LANES > 32) v += __shfl_xor(v, 32, kWave);
+    return v;
+}
+
+// 8 channels as loaded.
+template <bool BF16>
+struct Vec {
+    uint4 u[BF16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void* p, int64_t at) {
+        const uint4* s = (const uint4*)((const char*)p + at * (BF16 ? 2 : 4));
+        u[0] = s[0];
+        if constexpr (!BF16) u[1] = s[1];
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[BF16 ? 0 : 1].x, u[BF16 ? 0 : 1].y, u[BF16 ? 0 : 1].z, u[BF16 ? 0 : 1].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            x[j] = __uint_as_float(!BF16 ? w[j] : (j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+    }
+};
+
+template <bool BF16>
+__device__ __forceinline__ void store8(void* p, int64_t at, const float (&x)[8]) {
+    if constexpr (BF16) {
+        *(uint4*)((uint16_t*)p + at) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    } else {
+        float4* d = (float4*)((float*)p + at);
+        d[0] = make_float4(x[0], x[1], x[2], x[3]);
+        d[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+}
+
+// LANES: lanes of a head, a power of two; those past its vectors idle.
+template <int LANES, bool HALVES, bool XBF, bool OBF>
+__global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int per) {
+    __shared__ float2 table[kRows * kMaxPairs];
+    const int64_t row0 = (int64_t)blockIdx.x * per;
+    const int rows = (int)min((int64_t)per, a.M - row0), P = a.D >> 1;
+    fill_table(a, row0, rows, table);
+
+    constexpr int NV = HALVES ? 2 : 1, kHeads = kThreads / LANES;   // heads at a time
+    const int l = threadIdx.x % LANES, first = threadIdx.x / LANES;
+    const bool on = l * 8 < (HALVES ? P : a.D);
+    const int ch[2] = {l * 8, P + l * 8};
+    const int heads = a.q_heads + a.k_heads, items = rows * heads;
+    const float inv_d = 1.f / (float)a.D;
+    float wq[NV][8], wk[NV][8];
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) wq[n][j] = wk[n][j] = 1.f;
+    if (on) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (a.q_weight != nullptr) wq[n][j] = bf16_to_f32(((const uint16_t*)a.q_weight)[ch[n] + j]);
+                if (a.k_weight != nullptr) wk[n][j] = bf16_to_f32(((const uint16_t*)a.k_weight)[ch[n] + j]);
+            }
+    }
+    for (int i0 = first; i0 < items; i0 += kItems * kHeads) {
+        Vec<XBF> v[kItems][NV];
+#pragma unroll
+        for (int u = 0; u < kItems; ++u) {
+            const int i = i0 + u * kHeads, r = i / heads, h = i - r * heads;
+            if (i < items && on) {
+                const bool q = h < a.q_heads;
+                const int64_t at = (row0 + r) * (q ? a.q_stride : a.k_stride) + (int64_t)(q ? h : h - a.q_heads) * a.D;
+#pragma unroll
+                for (int n = 0; n < NV; ++n) v[u][n].load(q ? a.q : a.k, at + ch[n]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kItems; ++u) {
+            const int i = i0 + u * kHeads, r = i / heads, h = i - r * heads;
+            const bool q = h < a.q_heads, mine = i < items && on;
+            float x[NV][8];
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[n][j] = 0.f;
+                if (mine) v[u][n].get(x[n]);
+            }
+            if (a.q_weight != nullptr || a.k_weight != nullptr) {
+                float s = 0.f;
+#pragma unroll
+                for (int n = 0; n < NV; ++n)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s = fmaf(x[n][j], x[n][j], s);
+                s = __builtin_amdgcn_rsqf(fmaf(group_sum<LANES>(s), inv_d, a.eps));
+                if ((q ? a.q_weight : a.k_weight) != nullptr) {
+#pragma unroll
+                    for (int n = 0; n < NV; ++n)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[n][j] *= s * (q ? wq[n][j] : wk[n][j]);
+                }
+            }
+            if (!mine) continue;
+            const float2* t = table + r * P + (HALVES ? l * 8 : l * 4);
+            float y[NV][8];
+#pragma unroll
+            for (int p = 0; p < (HALVES ? 8 : 4); ++p) {
+                const float2 cs = t[p];
+                float& ya = y[0][HALVES ? p : 2 * p];
+                float& yb = y[NV - 1][HALVES ? p : 2 * p + 1];
+                const float xa = x[0][HALVES ? p : 2 * p], xb = x[NV - 1][HALVES ? p : 2 * p + 1];
+                ya = fmaf(xa, cs.x, -xb * cs.y);
+                yb = fmaf(xa, cs.y, xb * cs.x);
+            }
+            const int64_t at = (row0 + r) * (q ? a.q_out_stride : a.k_out_stride) + (int64_t)(q ? h : h - a.q_heads) * a.D;
+#pragma unroll
+            for (int n = 0; n < NV; ++n) store8<OBF>(q ? a.q_out : a.k_out, at + ch[n], y[n]);
+        }
+    }
+}
+
+// Any even D and any alignment: a wave takes a head, a lane the pairs lane and lane + 64.
+template <bool XBF, bool OBF>
+__global__ __launch_bounds__(kThreads) void rotary_pairs_kernel(RotaryArgs a, int per) {
+    __shared__ float2 table[kRows * kMaxPairs];
+    const int64_t row0 = (int64_t)blockIdx.x * per;
+    const int rows = (int)min((int64_t)per, a.M - row0), P = a.D >> 1;
+    fill_table(a, row0, rows, table);
+    const int lane = threadIdx.x & 63, heads = a.q_heads + a.k_heads;
+    for (int i = threadIdx.x >> 6; i < rows * heads; i += kThreads / 64) {
+        const int r = i / heads, h = i - r * heads;
+        const bool q = h < a.q_heads;
+        const int hh = q ? h : h - a.q_heads;
+        const int64_t at = (row0 + r) * (q ? a.q_stride : a.k_stride) + (int64_t)hh * a.D;
+        const int64_t to = (row0 + r) * (q ? a.q_out_stride : a.k_out_stride) + (int64_t)hh * a.D;
+        const void* src = q ? a.q : a.k;
+        void* dst = q ? a.q_out : a.k_out;
+        const uint16_t* w = (const uint16_t*)(q ? a.q_weight : a.k_weight);
+        float x[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int p = lane + u * 64, c = a.halves ? p + j * P : 2 * p + j;
+                if (p < P) x[u][j] = XBF ? bf16_to_f32(((const uint16_t*)src)[at + c]) : ((const float*)src)[at + c];
+            }
+        if (w != nullptr) {
+            float s = x[0][0] * x[0][0];
+            s = fmaf(x[0][1], x[0][1], s);
+            s = fmaf(x[1][0], x[1][0], s);
+            s = fmaf(x[1][1], x[1][1], s);
+            s = __builtin_amdgcn_rsqf(fmaf(group_sum<64>(s), 1.f / (float)a.D, a.eps));
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int p = lane + u * 64, c = a.halves ? p + j * P : 2 * p + j;
+                    if (p < P) x[u][j] *= s * bf16_to_f32(w[c]);
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int p = lane + u * 64;
+            if (p >= P) continue;
+            const float2 cs = table[r * P + p];
+            const float y[2] = {fmaf(x[u][0], cs.x, -x[u][1] * cs.y), fmaf(x[u][0], cs.y, x[u][1] * cs.x)};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int c = a.halves ? p + j * P : 2 * p + j;
+                if (OBF) ((uint16_t*)dst)[to + c] = (uint16_t)f32_to_bf16(y[j]);
+                else ((float*)dst)[to + c] = y[j];
+            }
+        }
+    }
+}
+
+template <bool XBF, bool OBF>
+void launch(const RotaryArgs& a, hipStream_t st) {
+    // whole rounds of CUs before a workgroup takes several rows
+    const int per = (int)std::min<int64_t>(kRows, std::max<int64_t>(1, a.M / (2 * kCus)));
+    const dim3 grid((unsigned)((a.M + per - 1) / per)), block(kThreads);
+    if (!a.vec) {
+        hipLaunchKernelGGL((rotary_pairs_kernel<XBF, OBF>), grid, block, 0, st, a, per);
+        return;
+    }
+    const int vecs = (a.halves ? a.D / 2 : a.D) / 8;
+    auto go = [&](auto lanes) {
+        if constexpr (lanes.value < 32) {
+            if (a.halves) {
+                hipLaunchKernelGGL((rotary_kernel<lanes.value, true, XBF, OBF>), grid, block, 0, st, a, per);
+                return;
+            }
+        }
+        hipLaunchKernelGGL((rotary_kernel<lanes.value, false, XBF, OBF>), grid, block, 0, st, a, per);
+    };
+    if (vecs <= 8) go(std::integral_constant<int, 8>{});
+    else if (vecs <= 16) go(std::integral_constant<int, 16>{});
+    else go(std::integral_constant<int, 32>{});   // never pairs of halves, which have 16 vectors at most
+}
+
+}  // namespace
+
+void launch_rotary(const RotaryArgs& a, hipStream_t st) {
+    if (a.x_bf16) a.out_bf16 ? launch<true, true>(a, st) : launch<true, false>(a, st);
+    else a.out_bf16 ? launch<false, true>(a, st) : launch<false, false>(a, st);
+}
+
+}  // namespace svdq

@@ -22,7 +22,9 @@
  *                       (optionally GELU-tanh), fp32 or bf16 output.
  * and the modulation layers as one call, awq_gemm_w4a16.  Beside a linear stand the adapters
  * of a batch's requests (svdq_lora_batch), before it the group norm of channels-last images
- * (svdq_group_norm).
+ * (svdq_group_norm), and between the linears of a transformer block, for the packed rows of many
+ * requests, the gated residual with layer norm and modulation (svdq_layer_norm), rotary positions
+ * with the q and k norm (svdq_rotary) and the attention itself (svdq_attention).
  *
  * Conventions shared by every entry point
  *   - Ownership: the caller allocates and owns every buffer (device memory unless stated).
@@ -62,6 +64,11 @@ typedef enum { SVDQ_PREC_INT4 = 0, SVDQ_PREC_NVFP4 = 1 } svdq_precision;
 typedef enum { SVDQ_DT_F32 = 0, SVDQ_DT_BF16 = 1 } svdq_dtype;
 /* SVDQ_ACT_SILU is taken by svdq_lora_batch and svdq_group_norm only. */
 typedef enum { SVDQ_ACT_NONE = 0, SVDQ_ACT_GELU_TANH = 1, SVDQ_ACT_SILU = 2 } svdq_act;
+
+/* What a row of svdq_attention sees: its segment's keys, or those up to its own position. */
+typedef enum { SVDQ_MASK_NONE = 0, SVDQ_MASK_CAUSAL = 1 } svdq_mask;
+/* Channel pairs of svdq_rotary: (2 i, 2 i + 1), or (i, i + head_dim / 2). */
+typedef enum { SVDQ_ROTARY_INTERLEAVED = 0, SVDQ_ROTARY_HALVES = 1 } svdq_rotary_pairing;
 
 /* The quantization fields a checkpoint's config.json records for one layer
  * ([ainews] paragraph 2: method, precision, group size, low-rank rank). */
@@ -435,6 +442,124 @@ svdq_status svdq_group_norm(int64_t B, int64_t rows, int32_t C, int32_t groups, 
                             const void* mod_shift, int64_t mod_stride, int32_t act,
                             int32_t out_dtype, void* out, int64_t out_stride, void* workspace,
                             int64_t workspace_bytes, svdq_stream_t stream);
+
+/* Between two linears of a transformer block: the branch's output through its gate onto the
+ * residual stream, and the stream's layer norm with each request's scale and shift.  For every row
+ * m of segment i (request i), over its C values
+ *
+ *   h = x[m] + mod_gate[i] y[m],   mean = sum h / C,   var = sum (h - mean)^2 / C,
+ *   x_out[m] = h,
+ *   out[m]   = ((h - mean) / sqrt(var + eps) weight + bias) (1 + mod_scale[i]) + mod_shift[i]
+ *
+ * in fp32, each result rounded once and the norm taken of the unrounded h (the sums of a row's
+ * values and of their squares about the mean must stay in fp32's range).
+ *   x          [M, C] of x_dtype, rows x_stride elements apart (>= C).
+ *   y          [M, C] of y_dtype, rows y_stride apart, or NULL: h = x (mod_gate and x_out must be
+ *              NULL then, y_dtype and y_stride are not looked at).
+ *   weight, bias  [C] bf16, or NULL: 1 and 0.
+ *   seg_start  [n_segments + 1] int32, not decreasing: segment i is rows seg_start[i] to
+ *              seg_start[i + 1] - 1.  Rows of no segment are not touched.  Where offsets decrease,
+ *              rows may be left or given another segment's terms, but nothing outside the buffers
+ *              is read or written.  NULL with n_segments = 1: all rows are segment 0.
+ *   mod_gate, mod_scale, mod_shift  [n_segments, C] of mod_dtype, rows mod_stride apart (>= C; one
+ *              stride for the three), or NULL each: 1, 0 and 0.  Column ranges of the rows that
+ *              awq_gemm_w4a16 writes for a modulation layer.
+ *   x_out      [M, C] of x_dtype, rows x_out_stride apart, or NULL: h is not kept.
+ *   out        [M, C] of out_dtype, rows out_stride apart.
+ * x_out may be x or y, and out may be x or y, where types and strides are the same (not both the
+ * same buffer); otherwise no input may overlap a result, nor one result the other.
+ * C up to 16384 where C and the strides in use are multiples of 4 and the buffers aligned to 4
+ * elements (which is faster too), else up to 8192; M up to 2^30, n_segments up to 2^16 (0 of
+ * either enqueues nothing).  Buffers are aligned to their type, all device memory on the current
+ * device; the offsets are read when the work runs, so a captured graph replays with what they hold
+ * then.  Bit-reproducible from run to run. */
+svdq_status svdq_layer_norm(int64_t M, int32_t C, int32_t n_segments, float eps, int32_t x_dtype, const void* x,
+                            int64_t x_stride, int32_t y_dtype, const void* y, int64_t y_stride,
+                            const void* weight, const void* bias, const int32_t* seg_start,
+                            int32_t mod_dtype, const void* mod_gate, const void* mod_scale,
+                            const void* mod_shift, int64_t mod_stride, void* x_out, int64_t x_out_stride,
+                            int32_t out_dtype, void* out, int64_t out_stride, svdq_stream_t stream);
+
+/* Rotary positions with several axes (time, height, width, ...) for the q and k heads that a fused
+ * q, k, v linear writes, after an optional RMS norm of each head.  For every row m, head x of q
+ * (of k with k_weight) and channel pair j = 0 to head_dim / 2 - 1 with channels (a, b)
+ *
+ *   x      = x / sqrt(sum x^2 / head_dim + eps) weight        (where the weight is not NULL)
+ *   angle  = positions[m, axis of pair j] freqs[j]
+ *   x'[a]  = x[a] cos(angle) - x[b] sin(angle),   x'[b] = x[a] sin(angle) + x[b] cos(angle)
+ *
+ * The angle is formed and reduced in binary64, so far positions keep their precision; the rest is
+ * fp32, rounded once (the sum of a head's squares must stay in fp32's range).
+ *   n_axes     1 to 4; axis_pairs [n_axes] int32 in HOST memory, read during the call: the first
+ *              axis_pairs[0] pairs belong to axis 0, the next axis_pairs[1] to axis 1, ...; none
+ *              negative, their sum head_dim / 2.
+ *   pairing    svdq_rotary_pairing: pair j is channels (2 j, 2 j + 1) or (j, j + head_dim / 2).
+ *   positions  [M, n_axes] fp32 (they may be fractions or negative), rows pos_stride apart.
+ *   freqs      [head_dim / 2] fp64: the angle, in radians, of one step along the pair's axis (often
+ *              theta^(-i / axis_pairs[a]) for the i-th pair of axis a; 0 leaves a pair as it is).
+ *   q_weight, k_weight  [head_dim] bf16, or NULL: no norm of those heads (eps is not looked at
+ *              where both are NULL).
+ *   q          [M, n_q_heads head_dim] of x_dtype, rows q_stride elements apart; k
+ *              [M, n_k_heads head_dim], rows k_stride apart: column ranges of the linear's output.
+ *              Of 0 heads the pointers and strides are not looked at.
+ *   q_out, k_out  as q and k, of out_dtype.  q_out == q or k_out == k is allowed where types and
+ *              strides are the same (in place); otherwise no input may overlap a result.
+ * head_dim even, up to 256; M up to 2^24, heads up to 2^16 (M = 0, or no heads, enqueues nothing).
+ * Buffers are aligned to their type; 16-byte aligned rows and head_dim a multiple of 8
+ * (interleaved) or 16 (halves) are faster.  All but axis_pairs are device memory on the current
+ * device.  Bit-reproducible from run to run. */
+svdq_status svdq_rotary(int64_t M, int32_t n_q_heads, int32_t n_k_heads, int32_t head_dim, int32_t n_axes,
+                        const int32_t* axis_pairs, int32_t pairing, const float* positions, int64_t pos_stride,
+                        const double* freqs, float eps, const void* q_weight, const void* k_weight,
+                        int32_t x_dtype, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        int32_t out_dtype, void* q_out, int64_t q_out_stride, void* k_out,
+                        int64_t k_out_stride, svdq_stream_t stream);
+
+/* Softmax attention of a packed batch: every row sees the keys of its own segment (request) only.
+ * For position i (from 0) of segment s and head h, over the keys j (from 0) that it sees,
+ *
+ *   t_ij = scale q[i, h] . k[j, h'],   h' = h n_kv_heads / n_heads (grouped heads),
+ *   t_ij = cap tanh(t_ij / cap)                     where cap > 0,
+ *   t_ij = t_ij - slopes[h] |i + d - j|             where slopes is not NULL,
+ *   out[i, h] = sum_j exp(t_ij) v[j, h'] / sum_j exp(t_ij),
+ *
+ * d = keys of s - rows of s, which puts the last row at the last key.  A row that sees no key gives
+ * zeros.  q, k and v are bf16; scores, the running maximum, sum and result are fp32, the weights
+ * exp(t_ij - max) rounded to bf16 for their product with v.
+ *   scale      finite and positive.  cap finite, 0: none.
+ *   mask       svdq_mask: SVDQ_MASK_NONE all keys of the segment (rows of an image see one another);
+ *              SVDQ_MASK_CAUSAL keys j <= i + d, and all j < prefix[s] (a prompt in front of it, or
+ *              the rows of an image that see one another).
+ *   q_start, kv_start  [n_segments + 1] int32, not decreasing: segment s has the rows q_start[s] to
+ *              q_start[s + 1] - 1 of q and kv_start[s] to kv_start[s + 1] - 1 of k and v (the same
+ *              pointer where they are the same rows).  Rows of q in no segment are not touched.
+ *              Values are clamped to [0, Mq] and [0, Mkv]; where they decrease, rows of out may be
+ *              left or written with other results, but nothing outside the buffers is read or
+ *              written.
+ *   prefix     [n_segments] int32 or NULL: 0; only with SVDQ_MASK_CAUSAL; clamped to the keys.
+ *   slopes     [n_heads] fp32 or NULL: no bias.
+ *   q, out     [Mq, n_heads head_dim] bf16, rows q_stride and out_stride elements apart; k, v
+ *              [Mkv, n_kv_heads head_dim] bf16: column ranges of wider matrices.  No input may
+ *              overlap out.
+ *   workspace  svdq_attention_workspace_bytes(Mq, Mkv, n_heads, n_kv_heads, head_dim, n_segments)
+ *              bytes at least (0 unless the rows are few), 16-byte aligned, overwritten; calls that
+ *              may overlap in time need one each.
+ * What a row does not see does not change its result, infinities and NaN among it.  A NaN score
+ * that a row sees makes the row NaN.
+ * head_dim a multiple of 8 up to 128; n_heads a positive multiple of n_kv_heads; Mq up to 2^24 and
+ * Mq n_heads below 2^25, Mkv up to 2^30, n_segments up to 2^16 (Mq = 0 or n_segments = 0 enqueues
+ * nothing; a buffer without elements may be NULL).  q, k, v and out must be 16-byte aligned, their
+ * strides multiples of 8 up to 2^24.  All buffers are device memory on the current device; offsets
+ * and prefixes are read when the work runs, so a captured graph replays with what they hold then.
+ * Bit-reproducible from run to run. */
+svdq_status svdq_attention_workspace_bytes(int64_t Mq, int64_t Mkv, int32_t n_heads, int32_t n_kv_heads,
+                                           int32_t head_dim, int32_t n_segments, int64_t* bytes);
+svdq_status svdq_attention(int64_t Mq, int64_t Mkv, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                           int32_t n_segments, float scale, float cap, int32_t mask, const int32_t* q_start,
+                           const int32_t* kv_start, const int32_t* prefix, const float* slopes, const void* q,
+                           int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           void* out, int64_t out_stride, void* workspace, int64_t workspace_bytes,
+                           svdq_stream_t stream);
 
 /* SVDQ_OK when HIP device `device` is a gfx950 GPU, else SVDQ_ERR_UNSUPPORTED_DEVICE
  * (or SVDQ_ERR_INVALID_ARG for a bad ordinal).  Results are cached per device. */
