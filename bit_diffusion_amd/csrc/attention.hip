@@ -18,7 +18,7 @@
 // lane 32 further), and what the first product leaves in registers is already the second one's
 // operand, keys in the order 4 h to 4 h + 3, 8 + 4 h to 8 + 4 h + 3 of every 16 (h the lane's
 // half).  V^T comes out of LDS in that order by the transposing read ds_read_b64_tr_b16.  P is
-// rounded to bf16 (2^-9 of each weight at most, against V's own 2^-9), its sum is of the unrounded
+// rounded to bf16 (2^-8 of each weight at most, as V's own values were), its sum is of the unrounded
 // values; O, maxima and sums are fp32.
 //
 // Maximum.  O is rescaled only where a row's maximum grew by more than 2^8 since the last time

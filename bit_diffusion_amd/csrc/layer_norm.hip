@@ -180,11 +180,12 @@ __global__ __launch_bounds__(kThreads) void layer_norm_kernel(LayerNormArgs a, i
             sum(0, m);
             __syncthreads();
             total(0, m);
-            // about that mean, the squares and what its rounding left: equal values give exactly 0
+            // about that mean, the squares and what its rounding left.  Equal values differ from it by
+            // a few ulp, all the same: their sum is exact, its C-th part (divided, not multiplied) too
             float e[kRows];
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
-                m[r] *= inv;
+                m[r] /= (float)C;   // a product would be contracted into h - m and never be rounded
                 q[r] = e[r] = 0.f;
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
@@ -204,7 +205,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_kernel(LayerNormArgs a, i
             total(2, q);
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
-                const float off = e[r] * inv;
+                const float off = e[r] / (float)C;
                 const float var = fmaxf(fmaf(-off, off, q[r] * inv), 0.f);
                 const float rstd = __builtin_amdgcn_rsqf(var + a.eps);
 #pragma unroll
