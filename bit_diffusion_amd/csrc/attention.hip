@@ -117,12 +117,14 @@ __device__ __forceinline__ uint64_t uniform_ptr(const void* p) {
     const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
     return ((uint64_t)hi << 32) | lo;
 }
-// Global -> LDS copy: each lane that is on moves the 16 bytes at base + off to LDS address lds +
-// 16 lane.  In asm so that the compiler does not wait for every copy in flight before each LDS
-// read; wait_copies does.  An LDS copy that reads M0 right after its write needs one wait state.
-__device__ __forceinline__ void copy16(uint64_t base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-                 :: "v"(off), "s"(base), "s"(lds) : "memory");
+// Global -> LDS copy: each lane whose bit is set in `on` moves the 16 bytes at base + off to LDS
+// address lds + 16 lane.  In asm so that the compiler does not wait for every copy in flight before
+// each LDS read; wait_copies does.  An LDS copy that reads M0 right after its write needs one wait
+// state.
+__device__ __forceinline__ void copy16(uint64_t base, uint32_t off, uint32_t lds, uint64_t on) {
+    uint64_t saved;
+    asm volatile("s_mov_b32 m0, %2\n\ts_and_saveexec_b64 %0, %4\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %3\n\ts_mov_b64 exec, %0"
+                 : "=&s"(saved) : "v"(off), "s"(lds), "s"(base), "s"(on) : "memory", "scc");
 }
 // Every copy of this wave has landed, and every LDS access before is done.
 __device__ __forceinline__ void wait_copies() { __builtin_amdgcn_s_waitcnt(0x0070); }
@@ -173,10 +175,12 @@ struct Rows {
     }
 };
 
-// Words of two bf16: those that are not finite become 0.
-__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
-    const uint32_t lo = (w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu;
-    return ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u) | lo;
+// All ones in the halves of a word of two bf16 that are not finite (their exponent bits plus one
+// reach the sign's place).
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+    typedef short s16x2 __attribute__((ext_vector_type(2)));
+    const s16x2 t = __builtin_bit_cast(s16x2, (w & 0x7F807F80u) + 0x00800080u);
+    return __builtin_bit_cast(uint32_t, t >> 15);
 }
 // Of a bf16: 1 for infinity, 2^8 for minus infinity, 2^16 for a NaN, else 0, as bf16.
 __device__ __forceinline__ uint32_t kind16(uint32_t v) {
@@ -203,14 +207,22 @@ __device__ __forceinline__ void step(Rows<NB, MOD>& w, int key0, uint32_t kb, ui
     f32x16 s[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
+        bf16x8 k[2 * NB];
+#pragma unroll
+        for (int c = 0; c < 2 * NB; ++c)
+            k[c] = *(lds_bf16x8*)(lds_u8*)(uintptr_t)((kb ^ (uint32_t)(c * 32)) + u * 32 * L::kRow);
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[u][i] = 0.f;
 #pragma unroll
-        for (int c = 0; c < 2 * NB; ++c) {
-            const bf16x8 k = *(lds_bf16x8*)(lds_u8*)(uintptr_t)((kb ^ (uint32_t)(c * 32)) + u * 32 * L::kRow);
-            s[u] = mfma32(k, w.Q[c], s[u]);
-        }
+        for (int c = 0; c < 2 * NB; ++c) s[u] = mfma32(k[c], w.Q[c], s[u]);
     }
+    // the first half of V is on its way while the weights are formed
+    uint4 v[2][NB];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) v[c][b] = v_operand<NB>(vb, b, c);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int u = 0; u < 2; ++u)
         if (MASK || MOD != kPlain) w.template score<MASK>(s[u], key0 + 32 * u, h);
@@ -231,7 +243,7 @@ __device__ __forceinline__ void step(Rows<NB, MOD>& w, int key0, uint32_t kb, ui
 #pragma unroll
             for (int i = 0; i < 16; ++i) w.O[b][i] *= keep;
     }
-    const float base = w.m == -INFINITY ? 0.f : -w.m * unit;
+    const float base = MASK && w.m == -INFINITY ? 0.f : -w.m * unit;   // no key yet: all weights 0
     uint4 P[4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -247,46 +259,66 @@ __device__ __forceinline__ void step(Rows<NB, MOD>& w, int key0, uint32_t kb, ui
     }
     uint32_t bad = 0;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int half = 0; half < 2; ++half) {
+        uint4 next[2][NB];
+        if (half == 0) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            uint4 v = v_operand<NB>(vb, b, c);
-            if constexpr (MASK) {
-                const uint4 f = make_uint4(finite_only(v.x), finite_only(v.y), finite_only(v.z), finite_only(v.w));
-                bad |= (f.x ^ v.x) | (f.y ^ v.y) | (f.z ^ v.z) | (f.w ^ v.w);
-                v = f;
-            }
-            w.O[b] = mfma32(as_bf16x8(v), as_bf16x8(P[c]), w.O[b]);
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) next[c][b] = v_operand<NB>(vb, b, c + 2);
         }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                uint4 x = v[c][b];
+                if constexpr (MASK) {
+                    const uint4 n = make_uint4(not_finite(x.x), not_finite(x.y), not_finite(x.z), not_finite(x.w));
+                    bad |= n.x | n.y | n.z | n.w;
+                    x = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
+                }
+                w.O[b] = mfma32(as_bf16x8(x), as_bf16x8(P[2 * half + c]), w.O[b]);
+            }
+        if (half == 0) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) v[c][b] = next[c][b];
+        }
+    }
     if constexpr (MASK) {
         // who sees how many infinities, minus infinities and NaN (at most 64 of each: exact in fp32)
         if (__any(bad != 0)) {
-#pragma unroll 1
+            uint4 one[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t e[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int key = key0 + 16 * c + 8 * (j >> 1) + 4 * h + 2 * (j & 1);
+                    e[j] = (key < w.limit ? 0x3F80u : 0u) | (key + 1 < w.limit ? 0x3F800000u : 0u);
+                }
+                one[c] = make_uint4(e[0], e[1], e[2], e[3]);
+            }
+#pragma unroll
             for (int b = 0; b < NB; ++b) {
                 f32x16 n;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) n[i] = 0.f;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const uint4 v = v_operand<NB>(vb, b, c);
-                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t e[4], one[4];
+                    const uint4 x = v_operand<NB>(vb, b, c);
+                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t e[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        e[j] = kind16(vw[j] & 0xFFFFu) | kind16(vw[j] >> 16) << 16;
-                        const int key = key0 + 16 * c + 8 * (j >> 1) + 4 * h + 2 * (j & 1);
-                        one[j] = (key < w.limit ? 0x3F80u : 0u) | (key + 1 < w.limit ? 0x3F800000u : 0u);
-                    }
-                    n = mfma32(as_bf16x8(make_uint4(e[0], e[1], e[2], e[3])), as_bf16x8(make_uint4(one[0], one[1], one[2], one[3])), n);
+                    for (int j = 0; j < 4; ++j) e[j] = kind16(xw[j] & 0xFFFFu) | kind16(xw[j] >> 16) << 16;
+                    n = mfma32(as_bf16x8(make_uint4(e[0], e[1], e[2], e[3])), as_bf16x8(one[c]), n);
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int k = (int)n[i];
                     const bool up = (k & 0xFF) != 0, down = (k & 0xFF00) != 0;
-                    const float add = k >= 1 << 16 || (up && down) ? NAN : up ? INFINITY : down ? -INFINITY : 0.f;
-#pragma unroll
-                    for (int bb = 0; bb < NB; ++bb)
-                        if (bb == b) w.O[bb][i] += add;
+                    w.O[b][i] += k >= 1 << 16 || (up && down) ? NAN : up ? INFINITY : down ? -INFINITY : 0.f;
                 }
             }
         }
@@ -346,14 +378,14 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
 #pragma unroll
         for (int i = 0; i < 16; ++i) w.O[b][i] = 0.f;
 
-    // tiles of the workgroup, and the wave's tiles without a mask (to least) and with keys (to most)
-    const int least = limit_of(t.row0 + min(wave * 32, rows - 1));
-    const int most = limit_of(t.row0 + min(wave * 32 + 31, rows - 1));
+    // the workgroup's tiles, those that all its rows see whole, and the keys that the wave's last row sees
     const int tiles = (limit_of(t.row0 + rows - 1) + kKeys - 1) / kKeys, per = (tiles + a.splits - 1) / a.splits;
     const int first = split * per, last = min(first + per, tiles);
+    const int whole = min(max(limit_of(t.row0) / kKeys, first), last);
+    const int most = active ? limit_of(t.row0 + min(wave * 32 + 31, rows - 1)) : 0;
 
-    // copies: an instruction fills 1 KB, kRow of them a row
-    constexpr int kLanes = L::kSlots, kStep = 64 / kLanes;   // lanes of a row, rows of an instruction
+    // copies: an instruction fills 1 KB, kLanes lanes a row, kStep rows
+    constexpr int kLanes = L::kSlots, kStep = 64 / kLanes;
     constexpr int kCopies = kKeys / kStep / kWaves;          // of a wave, for each of K and V
     const int crow = wave * kCopies * kStep + lane / kLanes, cslot = lane % kLanes;
     const uint32_t smem0 = (uint32_t)(uintptr_t)(lds_u8*)smem;
@@ -361,16 +393,35 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
     const uint32_t kbytes = (uint32_t)(a.k_stride * 2), vbytes = (uint32_t)(a.v_stride * 2);
     const char* kp = (const char*)a.k + ((int64_t)k0 * a.k_stride + (int64_t)g * D) * 2;
     const char* vp = (const char*)a.v + ((int64_t)k0 * a.v_stride + (int64_t)g * D) * 2;
+    // where each copy reads, from the tile's first key on, and its lanes with a channel
+    uint32_t koff[kCopies], voff[kCopies];
+    uint64_t kon[kCopies], von;
+#pragma unroll
+    for (int j = 0; j < kCopies; ++j) {
+        const int r = crow + j * kStep, ks = L::k_slot(r, cslot), vs = L::v_slot(r, cslot);
+        koff[j] = r * kbytes + ks * 16;
+        voff[j] = r * vbytes + vs * 16;
+        kon[j] = __ballot(ks * 8 < D);
+        von = __ballot(vs * 8 < D);      // the same for all: kStep is a multiple of the rows it goes by
+    }
+    static_assert(kStep % 4 == 0, "v_slot goes by the row modulo 4");
     auto copy_tile = [&](int tile, int buf) {
         const uint64_t kt = uniform_ptr(kp + (int64_t)tile * kKeys * kbytes), vt = uniform_ptr(vp + (int64_t)tile * kKeys * vbytes);
-        const int most_row = klen - 1 - tile * kKeys;   // keys past the segment's: its last again
+        const uint32_t to = lds0 + buf * 2 * L::kTile;
+        const int past = tile * kKeys + kKeys - klen;        // keys past the segment's: its last again
+        if (past <= 0) {
 #pragma unroll
-        for (int j = 0; j < kCopies; ++j) {
-            const int r = crow + j * kStep, from = min(r, most_row);
-            const int ks = L::k_slot(r, cslot), vs = L::v_slot(r, cslot);
-            const uint32_t to = lds0 + buf * 2 * L::kTile + j * 1024;
-            if (ks * 8 < D) copy16(kt, from * kbytes + ks * 16, to);
-            if (vs * 8 < D) copy16(vt, from * vbytes + vs * 16, to + L::kTile);
+            for (int j = 0; j < kCopies; ++j) {
+                copy16(kt, koff[j], to + j * 1024, kon[j]);
+                copy16(vt, voff[j], to + j * 1024 + L::kTile, von);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kCopies; ++j) {
+                const int r = crow + j * kStep, back = max(r - (kKeys - 1 - past), 0);
+                copy16(kt, koff[j] - back * kbytes, to + j * 1024, kon[j]);
+                copy16(vt, voff[j] - back * vbytes, to + j * 1024 + L::kTile, von);
+            }
         }
     };
     // channels past D: zeros, which no copy overwrites
@@ -381,19 +432,23 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
     // the lane's reads of K (row lane % 32, slot h of every 2) and of V (4 lanes to a row of 16 channels)
     const uint32_t kr = (lane & 31) * L::kRow + L::k_slot(lane & 31, h) * 16;
     const int vrow = 4 * h + ((lane >> 2) & 3);
-    const uint32_t vr = vrow * L::kRow + L::v_slot(vrow, ((lane >> 4) & 1) * 2 + ((lane >> 1) & 1)) * 16 + (lane & 1) * 8;
+    const uint32_t vr = vrow * L::kRow + L::v_slot(vrow, ((lane >> 4) & 1) * 2 + ((lane >> 1) & 1)) * 16 + (lane & 1) * 8 + L::kTile;
 
     if (first < last) copy_tile(first, 0);
-    for (int tile = first; tile < last; ++tile) {
-        const int buf = (tile - first) & 1;
+    uint32_t at = smem0;
+    for (int tile = first; tile < whole; ++tile) {
         wait_copies();
         barrier();   // this tile is there, and the other buffer has been read
-        if (tile + 1 < last) copy_tile(tile + 1, buf ^ 1);
-        const uint32_t at = smem0 + buf * 2 * L::kTile;
-        if (active && tile * kKeys < most) {
-            if (tile * kKeys + kKeys <= least) step<NB, MOD, false>(w, tile * kKeys, at + kr, at + L::kTile + vr);
-            else step<NB, MOD, true>(w, tile * kKeys, at + kr, at + L::kTile + vr);
-        }
+        if (tile + 1 < last) copy_tile(tile + 1, (tile + 1 - first) & 1);
+        if (active) step<NB, MOD, false>(w, tile * kKeys, at + kr, at + vr);
+        at = smem0 + (((tile + 1 - first) & 1) * 2) * L::kTile;
+    }
+    for (int tile = whole; tile < last; ++tile) {
+        wait_copies();
+        barrier();
+        if (tile + 1 < last) copy_tile(tile + 1, (tile + 1 - first) & 1);
+        if (tile * kKeys < most) step<NB, MOD, true>(w, tile * kKeys, at + kr, at + vr);
+        at = smem0 + (((tile + 1 - first) & 1) * 2) * L::kTile;
     }
     if (!active || wave * 32 + (lane & 31) >= rows) return;
     w.l = both_sum(w.l);
