@@ -12,8 +12,9 @@
 // Bound: memory, every row once.  A workgroup owns all columns of its rows, a thread the same
 // columns of each, so A, D and gate stay in registers from row to row while the segment does not
 // change (as fp32 rows they are three times a bf16 row's bytes, which the caches would else have to
-// deliver with every row).  kRows rows go at a time: their loads are in flight together and two
-// barriers serve all of them.
+// deliver with every row).  A row at a time, the next one's loads in flight, and several workgroups a
+// CU that wait at different barriers: four rows at a time, with one pair of barriers for all, held
+// four times the registers and took 85 us where this takes 29 (4608 x 3072 bf16 with residual).
 #include "common.hpp"
 #include "launch.hpp"
 #include "segments.hpp"
@@ -27,6 +28,8 @@ namespace {
 constexpr int kCus = 256;    // of the GPU
 constexpr int kVec = 4;      // columns of a thread's access where rows are aligned
 constexpr int kWaves = 16;   // of the widest workgroup
+constexpr int kWavesCu = 18; // a CU's share of the rows goes over workgroups of so many waves in all (4608
+                             // rows of 6 waves: 28.7 us, with 12 waves 30.5, 24 29.4, 48 31.9)
 
 // The sum over the wave, in every lane.
 __device__ __forceinline__ float wave_sum(float v) {
@@ -39,21 +42,45 @@ __device__ __forceinline__ float wave_sum(float v) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// VEC columns at element `at`, as fp32 and back.
+// A barrier that waits for this wave's LDS accesses only: loads of the next row and stores of this
+// one stay in flight (__syncthreads would wait for them).
+__device__ __forceinline__ void sync() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// VEC columns at element `at`: as loaded, and as fp32.
+template <int VEC, bool BF16>
+struct Raw {
+    uint32_t u[VEC == 1 ? 1 : BF16 ? 2 : 4];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (uint32_t& w : u) w = 0;
+    }
+    __device__ __forceinline__ void load(const void* p, int64_t at) {
+        if constexpr (VEC == 1) {
+            u[0] = BF16 ? ((const uint16_t*)p)[at] : ((const uint32_t*)p)[at];
+        } else if constexpr (BF16) {
+            const uint2 w = *(const uint2*)((const uint16_t*)p + at);
+            u[0] = w.x; u[1] = w.y;
+        } else {
+            const uint4 w = *(const uint4*)((const uint32_t*)p + at);
+            u[0] = w.x; u[1] = w.y; u[2] = w.z; u[3] = w.w;
+        }
+    }
+    __device__ __forceinline__ float get(int j) const {
+        if constexpr (!BF16) return __uint_as_float(u[j]);
+        else return __uint_as_float((j & 1) ? u[j >> 1] & 0xFFFF0000u : u[j >> 1] << 16);
+    }
+};
+
 template <int VEC>
 __device__ __forceinline__ void load(const void* p, int64_t at, bool bf16, float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        v[0] = bf16 ? bf16_to_f32(((const uint16_t*)p)[at]) : ((const float*)p)[at];
-    } else if (bf16) {
-        const uint2 u = *(const uint2*)((const uint16_t*)p + at);
-        v[0] = __uint_as_float(u.x << 16);
-        v[1] = __uint_as_float(u.x & 0xFFFF0000u);
-        v[2] = __uint_as_float(u.y << 16);
-        v[3] = __uint_as_float(u.y & 0xFFFF0000u);
-    } else {
-        const float4 f = *(const float4*)((const float*)p + at);
-        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-    }
+    Raw<VEC, true> b;
+    Raw<VEC, false> f;
+    if (bf16) b.load(p, at);
+    else f.load(p, at);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) v[j] = bf16 ? b.get(j) : f.get(j);
 }
 
 template <int VEC>
@@ -68,17 +95,33 @@ __device__ __forceinline__ void store(void* p, int64_t at, bool bf16, const floa
     }
 }
 
-// V vectors of VEC columns a thread, kRows rows at a time; `per` rows a workgroup.  The last column
-// vector may reach past C only where VEC is 1 (C is a multiple of VEC).
-template <int VEC, int V, int kRows, int kThreads, bool XBF, bool YBF, bool OBF>
+// V vectors of VEC columns a thread; `per` rows a workgroup.  C is a multiple of VEC.  The next row is
+// loaded while this one is normalised, but in the widest rows, which have no registers left for it.
+template <int VEC, int V, int kThreads, bool XBF, bool YBF, bool OBF>
 __global__ __launch_bounds__(kThreads) void layer_norm_kernel(LayerNormArgs a, int per) {
-    __shared__ float part[3][kWaves][kRows];
+    __shared__ float part[3][kWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
     const int C = a.C, T = blockDim.x;
-    const float inv = 1.f / (float)C;
+    const float c_count = (float)C;
+    constexpr bool kAhead = V < 8;
     int row = (int)blockIdx.x * per;
     const int stop = min(row + per, (int)a.M);
+    Raw<VEC, XBF> x[V];
+    Raw<VEC, YBF> y[V];
+    auto fetch = [&](int r) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = (v * T + tid) * VEC;
+            x[v].clear();
+            y[v].clear();
+            if (c < C) {
+                x[v].load(a.x, r * a.x_stride + c);
+                if (a.y != nullptr) y[v].load(a.y, r * a.y_stride + c);
+            }
+        }
+    };
     while (row < stop) {
+        if (kAhead) fetch(row);  // what comes up to its use need not wait for it
         int seg = 0, end = stop;
         if (a.starts != nullptr) {
             seg = find_segment(a.starts, a.n_segments, row);
@@ -114,122 +157,75 @@ __global__ __launch_bounds__(kThreads) void layer_norm_kernel(LayerNormArgs a, i
                 }
             }
         }
-        for (; row < end; row += kRows) {
-            const int live = min(kRows, end - row);
-            float h[kRows][V][VEC];
+        for (; row < end; ++row) {
+            if (!kAhead) fetch(row);
+            float h[V][VEC], m = 0.f;
 #pragma unroll
-            for (int r = 0; r < kRows; ++r)
+            for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const int c = (v * T + tid) * VEC;
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) h[r][v][j] = 0.f;
-                    if (c < C && r < live) load<VEC>(a.x, (row + r) * a.x_stride + c, XBF, h[r][v]);
+                for (int j = 0; j < VEC; ++j) {
+                    h[v][j] = a.y != nullptr ? fmaf(gate[v][j], y[v].get(j), x[v].get(j)) : x[v].get(j);
+                    m += h[v][j];
                 }
-            if (a.y != nullptr) {
-                float y[kRows][V][VEC];
-#pragma unroll
-                for (int r = 0; r < kRows; ++r)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const int c = (v * T + tid) * VEC;
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) y[r][v][j] = 0.f;
-                        if (c < C && r < live) load<VEC>(a.y, (row + r) * a.y_stride + c, YBF, y[r][v]);
-                    }
-#pragma unroll
-                for (int r = 0; r < kRows; ++r)
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) h[r][v][j] = fmaf(gate[v][j], y[r][v][j], h[r][v][j]);
-            }
+            if (kAhead && row + 1 < end) fetch(row + 1);
             if (a.x_out != nullptr) {
 #pragma unroll
-                for (int r = 0; r < kRows; ++r)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const int c = (v * T + tid) * VEC;
-                        if (c < C && r < live) store<VEC>(a.x_out, (row + r) * a.x_out_stride + c, XBF, h[r][v]);
-                    }
-            }
-            // the sum over the workgroup of each row's f, through part[at]
-            auto sum = [&](int at, const float (&s)[kRows]) {
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) {
-                    const float w = wave_sum(s[r]);
-                    if (lane == 0) part[at][wave][r] = w;
-                }
-            };
-            auto total = [&](int at, float (&s)[kRows]) {
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) s[r] = part[at][0][r];
-                for (int w = 1; w < waves; ++w)
-#pragma unroll
-                    for (int r = 0; r < kRows; ++r) s[r] += part[at][w][r];
-            };
-            float m[kRows], q[kRows];
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                m[r] = 0.f;
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) m[r] += h[r][v][j];
-            }
-            sum(0, m);
-            __syncthreads();
-            total(0, m);
-            // about that mean, the squares and what its rounding left.  Equal values differ from it by
-            // a few ulp, all the same: their sum is exact, its C-th part (divided, not multiplied) too
-            float e[kRows];
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                m[r] /= (float)C;   // a product would be contracted into h - m and never be rounded
-                q[r] = e[r] = 0.f;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const bool in = (v * T + tid) * VEC < C;
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        h[r][v][j] = in ? h[r][v][j] - m[r] : 0.f;
-                        e[r] += h[r][v][j];
-                        q[r] = fmaf(h[r][v][j], h[r][v][j], q[r]);
-                    }
-                }
-            }
-            sum(1, e);
-            sum(2, q);
-            __syncthreads();
-            total(1, e);
-            total(2, q);
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const float off = e[r] / (float)C;
-                const float var = fmaxf(fmaf(-off, off, q[r] * inv), 0.f);
-                const float rstd = __builtin_amdgcn_rsqf(var + a.eps);
-#pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const int c = (v * T + tid) * VEC;
-                    float z[VEC];
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) z[j] = fmaf((h[r][v][j] - off) * rstd, A[v][j], D[v][j]);
-                    if (c < C && r < live) store<VEC>(a.out, (row + r) * a.out_stride + c, OBF, z);
+                    if (c < C) store<VEC>(a.x_out, row * a.x_out_stride + c, XBF, h[v]);
                 }
             }
+            // the workgroup's sum of every wave's f, through part[at]
+            auto put = [&](int at, float f) {
+                f = wave_sum(f);
+                if (lane == 0) part[at][wave] = f;
+            };
+            auto total = [&](int at) {
+                float f = part[at][0];
+                for (int w = 1; w < waves; ++w) f += part[at][w];
+                return f;
+            };
+            put(0, m);
+            sync();
+            m = total(0) / c_count;   // a product would be contracted into h - m and never be rounded
+            // about that mean, the squares and what its rounding left.  Equal values differ from it by
+            // a few ulp, all the same: their sum is exact, its C-th part (divided, not multiplied) too
+            float e = 0.f, q = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const bool in = (v * T + tid) * VEC < C;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    h[v][j] = in ? h[v][j] - m : 0.f;
+                    e += h[v][j];
+                    q = fmaf(h[v][j], h[v][j], q);
+                }
+            }
+            put(1, e);
+            put(2, q);
+            sync();
+            const float off = total(1) / c_count;
+            const float var = fmaxf(fmaf(-off, off, total(2) / c_count), 0.f);
+            const float rstd = __builtin_amdgcn_rsqf(var + a.eps);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int c = (v * T + tid) * VEC;
+                float z[VEC];
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) z[j] = fmaf((h[v][j] - off) * rstd, A[v][j], D[v][j]);
+                if (c < C) store<VEC>(a.out, row * a.out_stride + c, OBF, z);
+            }
         }
-        row = end;
     }
 }
 
-template <int VEC, int V, int kRows, int kThreads>
+template <int VEC, int V, int kThreads>
 void launch(const LayerNormArgs& a, int threads, hipStream_t st) {
-    // a few workgroups a CU, each with whole sets of kRows rows
-    const int64_t want = (a.M + 4 * kCus - 1) / (4 * kCus);
-    const int per = (int)(want <= 1 ? 1 : (want + kRows - 1) / kRows * kRows);
+    const int64_t most = kCus * std::max(1, kWavesCu * 64 / threads);
+    const int per = (int)((a.M + most - 1) / most);
     const dim3 grid((unsigned)((a.M + per - 1) / per)), block(threads);
     auto go = [&](auto xb, auto yb, auto ob) {
-        hipLaunchKernelGGL((layer_norm_kernel<VEC, V, kRows, kThreads, xb.value, yb.value, ob.value>), grid, block, 0, st, a, per);
+        hipLaunchKernelGGL((layer_norm_kernel<VEC, V, kThreads, xb.value, yb.value, ob.value>), grid, block, 0, st, a, per);
     };
     auto with_out = [&](auto xb, auto yb) { a.out_bf16 ? go(xb, yb, std::true_type{}) : go(xb, yb, std::false_type{}); };
     auto with_y = [&](auto xb) { a.y_bf16 ? with_out(xb, std::true_type{}) : with_out(xb, std::false_type{}); };
@@ -240,20 +236,20 @@ void launch(const LayerNormArgs& a, int threads, hipStream_t st) {
 
 void launch_layer_norm(const LayerNormArgs& a, hipStream_t st) {
     const int n = a.vec ? (a.C + kVec - 1) / kVec : a.C;   // column vectors of a row
-    // vectors a thread so that a row's threads fit a workgroup: 256 of them, and for wide rows the
-    // most that leave each its registers
-    const int V = n <= 64 ? 1 : n <= 512 ? 2 : n <= 1024 ? 4 : 8;
+    // two vectors a thread up to 1024 (4608 rows of 768 vectors: 28.7 us, with one 40, with four 31),
+    // then as many as leave a row's threads in a workgroup their registers
+    const int V = n <= 64 ? 1 : n <= 1024 ? 2 : n <= 2048 ? 4 : 8;
     const int threads = ((n + V - 1) / V + 63) / 64 * 64;
     if (a.vec) {
-        if (V == 1) launch<kVec, 1, 4, 64>(a, threads, st);
-        else if (V == 2) launch<kVec, 2, 4, 256>(a, threads, st);
-        else if (V == 4) launch<kVec, 4, 4, 256>(a, threads, st);
-        else launch<kVec, 8, 1, 512>(a, threads, st);
+        if (V == 1) launch<kVec, 1, 64>(a, threads, st);
+        else if (V == 2) launch<kVec, 2, 512>(a, threads, st);
+        else if (V == 4) launch<kVec, 4, 512>(a, threads, st);
+        else launch<kVec, 8, 512>(a, threads, st);
     } else {
-        if (V == 1) launch<1, 1, 4, 64>(a, threads, st);
-        else if (V == 2) launch<1, 2, 4, 256>(a, threads, st);
-        else if (V == 4) launch<1, 4, 4, 256>(a, threads, st);
-        else launch<1, 8, 2, 1024>(a, threads, st);
+        if (V == 1) launch<1, 1, 64>(a, threads, st);
+        else if (V == 2) launch<1, 2, 512>(a, threads, st);
+        else if (V == 4) launch<1, 4, 512>(a, threads, st);
+        else launch<1, 8, 1024>(a, threads, st);
     }
 }
 
