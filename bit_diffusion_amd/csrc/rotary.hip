@@ -11,8 +11,9 @@
 //
 // Bound: memory, q and k once in and once out.  Aligned heads: a lane holds 8 channels (16 bytes
 // of bf16) in adjacent pairs, or 8 from either half, and a head is a group of 8, 16 or 32 lanes of
-// one wave, so the norm's sum needs no LDS; kItems heads a lane are in flight at a time.  Other
-// head widths and alignments: a wave takes a head, a lane single pairs.
+// one wave, so the norm's sum needs no LDS; the next head is loaded before this one is turned, the
+// first before the table is made.  Other head widths and alignments: a wave takes a head, a lane
+// single pairs.
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -25,8 +26,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kCus = 256;    // of the GPU
 constexpr int kMaxPairs = 128;
-constexpr int kRows = 4;     // rows of a workgroup, at most
-constexpr int kItems = 4;    // heads of a lane in flight
+constexpr int kRows = 16;    // rows of a workgroup, at most
+// Heads that a group of lanes takes: so many pay for the angle table and its start (4608 rows of 48
+// heads of 128: 27.5 us, with 4 heads 32.4; 6001 rows of 20 heads of 96, fp32: 17.8, with one row a
+// workgroup, 1 head, 39).
+constexpr int kPerGroup = 16;
 
 // cos and sin of `rows` rows' angles: table[row][pair].
 __device__ __forceinline__ void fill_table(const RotaryArgs& a, int64_t row0, int rows, float2* table) {
@@ -39,7 +43,10 @@ __device__ __forceinline__ void fill_table(const RotaryArgs& a, int64_t row0, in
         sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
         table[i] = make_float2(c, s);
     }
-    __syncthreads();
+}
+// A barrier that waits for this wave's LDS accesses only: loads stay in flight.
+__device__ __forceinline__ void sync() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 // The sum over each LANES (8, 16, 32, 64) neighbouring lanes, in all of them.
@@ -88,13 +95,11 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int per)
     __shared__ float2 table[kRows * kMaxPairs];
     const int64_t row0 = (int64_t)blockIdx.x * per;
     const int rows = (int)min((int64_t)per, a.M - row0), P = a.D >> 1;
-    fill_table(a, row0, rows, table);
-
     constexpr int NV = HALVES ? 2 : 1, kHeads = kThreads / LANES;   // heads at a time
     const int l = threadIdx.x % LANES, first = threadIdx.x / LANES;
     const bool on = l * 8 < (HALVES ? P : a.D);
     const int ch[2] = {l * 8, P + l * 8};
-    const int heads = a.q_heads + a.k_heads, items = rows * heads;
+    const int heads = a.q_heads + a.k_heads;
     const float inv_d = 1.f / (float)a.D;
     float wq[NV][8], wk[NV][8];
 #pragma unroll
@@ -110,59 +115,70 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int per)
                 if (a.k_weight != nullptr) wk[n][j] = bf16_to_f32(((const uint16_t*)a.k_weight)[ch[n] + j]);
             }
     }
-    for (int i0 = first; i0 < items; i0 += kItems * kHeads) {
-        Vec<XBF> v[kItems][NV];
-#pragma unroll
-        for (int u = 0; u < kItems; ++u) {
-            const int i = i0 + u * kHeads, r = i / heads, h = i - r * heads;
-            if (i < items && on) {
-                const bool q = h < a.q_heads;
-                const int64_t at = (row0 + r) * (q ? a.q_stride : a.k_stride) + (int64_t)(q ? h : h - a.q_heads) * a.D;
-#pragma unroll
-                for (int n = 0; n < NV; ++n) v[u][n].load(q ? a.q : a.k, at + ch[n]);
-            }
+    // the lane's items: head and row, kHeads items further each time
+    const int step_r = kHeads / heads, step_h = kHeads - step_r * heads;
+    struct Item {
+        int r, h;
+    };
+    auto next = [&](Item& t) {
+        t.r += step_r;
+        t.h += step_h;
+        if (t.h >= heads) {
+            t.h -= heads;
+            ++t.r;
         }
+    };
+    Vec<XBF> v[NV];
+    auto fetch = [&](const Item& t) {
+        if (t.r >= rows || !on) return;
+        const bool q = t.h < a.q_heads;
+        const int64_t at = (row0 + t.r) * (q ? a.q_stride : a.k_stride) + (int64_t)(q ? t.h : t.h - a.q_heads) * a.D;
 #pragma unroll
-        for (int u = 0; u < kItems; ++u) {
-            const int i = i0 + u * kHeads, r = i / heads, h = i - r * heads;
-            const bool q = h < a.q_heads, mine = i < items && on;
-            float x[NV][8];
+        for (int n = 0; n < NV; ++n) v[n].load(q ? a.q : a.k, at + ch[n]);
+    };
+    Item t{first / heads, first % heads}, ahead = t;
+    fetch(t);                   // on its way while the table is made
+    fill_table(a, row0, rows, table);
+    sync();
+    for (; __any(t.r < rows); t = ahead) {
+        const bool q = t.h < a.q_heads, mine = t.r < rows && on;
+        float x[NV][8];
 #pragma unroll
-            for (int n = 0; n < NV; ++n) {
+        for (int n = 0; n < NV; ++n) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[n][j] = 0.f;
-                if (mine) v[u][n].get(x[n]);
-            }
-            if (a.q_weight != nullptr || a.k_weight != nullptr) {
-                float s = 0.f;
+            for (int j = 0; j < 8; ++j) x[n][j] = 0.f;
+            if (mine) v[n].get(x[n]);
+        }
+        next(ahead);
+        fetch(ahead);
+        if (a.q_weight != nullptr || a.k_weight != nullptr) {
+            float s = 0.f;
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s = fmaf(x[n][j], x[n][j], s);
+            s = __builtin_amdgcn_rsqf(fmaf(group_sum<LANES>(s), inv_d, a.eps));
+            if ((q ? a.q_weight : a.k_weight) != nullptr) {
 #pragma unroll
                 for (int n = 0; n < NV; ++n)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s = fmaf(x[n][j], x[n][j], s);
-                s = __builtin_amdgcn_rsqf(fmaf(group_sum<LANES>(s), inv_d, a.eps));
-                if ((q ? a.q_weight : a.k_weight) != nullptr) {
-#pragma unroll
-                    for (int n = 0; n < NV; ++n)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) x[n][j] *= s * (q ? wq[n][j] : wk[n][j]);
-                }
+                    for (int j = 0; j < 8; ++j) x[n][j] *= s * (q ? wq[n][j] : wk[n][j]);
             }
-            if (!mine) continue;
-            const float2* t = table + r * P + (HALVES ? l * 8 : l * 4);
-            float y[NV][8];
-#pragma unroll
-            for (int p = 0; p < (HALVES ? 8 : 4); ++p) {
-                const float2 cs = t[p];
-                float& ya = y[0][HALVES ? p : 2 * p];
-                float& yb = y[NV - 1][HALVES ? p : 2 * p + 1];
-                const float xa = x[0][HALVES ? p : 2 * p], xb = x[NV - 1][HALVES ? p : 2 * p + 1];
-                ya = fmaf(xa, cs.x, -xb * cs.y);
-                yb = fmaf(xa, cs.y, xb * cs.x);
-            }
-            const int64_t at = (row0 + r) * (q ? a.q_out_stride : a.k_out_stride) + (int64_t)(q ? h : h - a.q_heads) * a.D;
-#pragma unroll
-            for (int n = 0; n < NV; ++n) store8<OBF>(q ? a.q_out : a.k_out, at + ch[n], y[n]);
         }
+        if (!mine) continue;
+        const float2* cs = table + t.r * P + (HALVES ? l * 8 : l * 4);
+        float y[NV][8];
+#pragma unroll
+        for (int p = 0; p < (HALVES ? 8 : 4); ++p) {
+            float& ya = y[0][HALVES ? p : 2 * p];
+            float& yb = y[NV - 1][HALVES ? p : 2 * p + 1];
+            const float xa = x[0][HALVES ? p : 2 * p], xb = x[NV - 1][HALVES ? p : 2 * p + 1];
+            ya = fmaf(xa, cs[p].x, -xb * cs[p].y);
+            yb = fmaf(xa, cs[p].y, xb * cs[p].x);
+        }
+        const int64_t at = (row0 + t.r) * (q ? a.q_out_stride : a.k_out_stride) + (int64_t)(q ? t.h : t.h - a.q_heads) * a.D;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) store8<OBF>(q ? a.q_out : a.k_out, at + ch[n], y[n]);
     }
 }
 
@@ -173,6 +189,7 @@ __global__ __launch_bounds__(kThreads) void rotary_pairs_kernel(RotaryArgs a, in
     const int64_t row0 = (int64_t)blockIdx.x * per;
     const int rows = (int)min((int64_t)per, a.M - row0), P = a.D >> 1;
     fill_table(a, row0, rows, table);
+    sync();
     const int lane = threadIdx.x & 63, heads = a.q_heads + a.k_heads;
     for (int i = threadIdx.x >> 6; i < rows * heads; i += kThreads / 64) {
         const int r = i / heads, h = i - r * heads;
@@ -223,14 +240,15 @@ __global__ __launch_bounds__(kThreads) void rotary_pairs_kernel(RotaryArgs a, in
 
 template <bool XBF, bool OBF>
 void launch(const RotaryArgs& a, hipStream_t st) {
-    // whole rounds of CUs before a workgroup takes several rows
-    const int per = (int)std::min<int64_t>(kRows, std::max<int64_t>(1, a.M / (2 * kCus)));
+    const int heads = a.q_heads + a.k_heads, vecs = (a.halves ? a.D / 2 : a.D) / 8;
+    const int at_once = !a.vec ? kThreads / 64 : kThreads / (vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32);
+    const int64_t rows = std::min<int64_t>(a.M / kCus, (kPerGroup * at_once + heads - 1) / heads);
+    const int per = (int)std::min<int64_t>(kRows, std::max<int64_t>(1, rows));
     const dim3 grid((unsigned)((a.M + per - 1) / per)), block(kThreads);
     if (!a.vec) {
         hipLaunchKernelGGL((rotary_pairs_kernel<XBF, OBF>), grid, block, 0, st, a, per);
         return;
     }
-    const int vecs = (a.halves ? a.D / 2 : a.D) / 8;
     auto go = [&](auto lanes) {
         if constexpr (lanes.value < 32) {
             if (a.halves) {
