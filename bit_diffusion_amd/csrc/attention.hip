@@ -18,12 +18,15 @@
 // lane 32 further), and what the first product leaves in registers is already the second one's
 // operand, keys in the order 4 h to 4 h + 3, 8 + 4 h to 8 + 4 h + 3 of every 16 (h the lane's
 // half).  V^T comes out of LDS in that order by the transposing read ds_read_b64_tr_b16.  P is
-// rounded to bf16 (2^-8 of each weight at most, as V's own values were), its sum is of the unrounded
-// values; O, maxima and sums are fp32.
+// rounded to bf16 (2^-8 of each weight at most, as V's own values were), and summed as rounded, which
+// takes their common error out again; O, maxima and sums are fp32.
 //
-// Maximum.  O is rescaled only where a row's maximum grew by more than 2^8 since the last time
-// (always at its first key): weights are at most 2^8 then, far from fp32's and bf16's ends, and
-// most tiles skip the 16 multiplications a lane and block of 32 channels.
+// Maximum.  What the weights are taken against need not be the largest score so far: 2^40 above it
+// bf16 and fp32 hold a weight as well as 1.  So a row keeps the maximum of its first tile, and only
+// where the weights' sum of a tile passes 2^40 are maximum, O and sum brought up to date and the tile's
+// weights formed again (finding the largest score of every tile: 251 -> 260 us at 4608 rows and 24
+// heads of 128).  With a bias by distance scores grow from tile to tile as a rule, and the largest is
+// sought in each; O is rescaled only where it grew by more than 2^8.
 //
 // LDS.  K and V tiles, rows of 64 or 128 channels, twice each: the next tile's copies (LDS DMA,
 // 16 bytes a lane) fly while this one is multiplied, one barrier a tile.  The 16-byte slots of a
@@ -53,6 +56,7 @@ constexpr int kKeys = 64;            // keys of a tile
 constexpr int kCus = 256;            // of the GPU
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;         // growth of a maximum, in powers of two, that O is rescaled for
+constexpr float kMost = 1.1e12f;     // sum of 32 weights past which a row gets a new maximum
 
 enum Mod { kPlain = 0, kCap = 1, kBias = 2, kBoth = 3 };
 
@@ -205,6 +209,7 @@ __device__ __forceinline__ void step(Rows<NB, MOD>& w, int key0, uint32_t kb, ui
     using L = Lds<NB>;
     const int lane = threadIdx.x & 63, h = lane >> 5;
     f32x16 s[2];
+    __builtin_amdgcn_s_setprio(1);   // the other wave's weights wait for these products, not these for them
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         bf16x8 k[2 * NB];
@@ -223,40 +228,60 @@ __device__ __forceinline__ void step(Rows<NB, MOD>& w, int key0, uint32_t kb, ui
 #pragma unroll
         for (int b = 0; b < NB; ++b) v[c][b] = v_operand<NB>(vb, b, c);
     __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(0);
 #pragma unroll
     for (int u = 0; u < 2; ++u)
         if (MASK || MOD != kPlain) w.template score<MASK>(s[u], key0 + 32 * u, h);
-    float top = s[0][0];
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = __builtin_elementwise_maximum(top, s[u][i]);
-    top = both_max(top);
+    // the weights against the maximum so far, and this half's sum of them
     const float unit = MOD == kPlain ? w.c0 : 1.f;
-    if (__any((top - w.m) * unit > kGrow)) {
-        const float m = __builtin_elementwise_maximum(w.m, top);
-        const float keep = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((w.m - m) * unit);
-        w.m = m;
+    uint4 P[4];
+    auto weigh = [&]() {
+        const float base = w.m == -INFINITY ? 0.f : -w.m * unit;   // no key yet: all weights are 0
+        const bf16x2 ones{(__bf16)1.f, (__bf16)1.f};
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t e[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = 8 * (c & 1) + 2 * j;
+                e[j] = pack_bf16(__builtin_amdgcn_exp2f(fmaf(s[c >> 1][i], unit, base)),
+                                 __builtin_amdgcn_exp2f(fmaf(s[c >> 1][i + 1], unit, base)));
+                sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, e[j]), ones, sum, false);
+            }
+            P[c] = make_uint4(e[0], e[1], e[2], e[3]);
+        }
+        return sum;
+    };
+    // brings what is there to the maximum with this tile's, where a row's grew by more than `by`
+    auto grow = [&](float by) {
+        float top = s[0][0];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = __builtin_elementwise_maximum(top, s[u][i]);
+        top = __builtin_elementwise_maximum(w.m, both_max(top));
+        if (!__any((top - w.m) * unit > by)) return;
+        const float keep = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((w.m - top) * unit);
+        w.m = top;
         w.l *= keep;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) w.O[b][i] *= keep;
-    }
-    const float base = MASK && w.m == -INFINITY ? 0.f : -w.m * unit;   // no key yet: all weights 0
-    uint4 P[4];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            s[u][i] = __builtin_amdgcn_exp2f(fmaf(s[u][i], unit, base));
-            w.l += s[u][i];
+    };
+    float sum;
+    if constexpr ((MOD & kBias) != 0) {
+        grow(kGrow);
+        sum = weigh();
+    } else {
+        sum = weigh();
+        if (__any(!(sum < kMost) || w.m == -INFINITY)) {
+            grow(0.f);
+            sum = weigh();
         }
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-            P[2 * u + c] = make_uint4(pack_bf16(s[u][8 * c], s[u][8 * c + 1]), pack_bf16(s[u][8 * c + 2], s[u][8 * c + 3]),
-                                      pack_bf16(s[u][8 * c + 4], s[u][8 * c + 5]), pack_bf16(s[u][8 * c + 6], s[u][8 * c + 7]));
     }
+    w.l += sum;
     uint32_t bad = 0;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
