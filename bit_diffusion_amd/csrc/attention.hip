@@ -42,7 +42,6 @@
 // the workspace and are joined by a second launch.
 #include "common.hpp"
 #include "launch.hpp"
-#include "segments.hpp"
 
 #include <algorithm>
 #include <type_traits>
@@ -65,11 +64,24 @@ typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) const bf16x8 lds_bf16x8;
 
-// Tile `want` of the segments' tiles of kRows rows (rep to a position), in order; the first row in
-// its segment, and the segment.  seg < 0: no such tile.
 struct Tile {
-    int seg, q0, len, row0;   // segment, its first row of q, its positions, the tile's first packed row
+    int seg;           // < 0: no such tile
+    int q0, len;       // the segment's first row of q and its positions,
+    int k0, keys;      // its first key and its keys
+    int row0;          // the tile's first packed row
 };
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ int max_dpp(int v) { return max(v, dpp<CTRL, ROWS>(v, v)); }
+// The largest over the wave, in every lane.
+__device__ __forceinline__ int wave_max(int v) {
+    v = max_dpp<kShr + 1>(v);
+    v = max_dpp<kShr + 2>(v);
+    v = max_dpp<kShr + 4>(v);
+    v = max_dpp<kShr + 8>(v);
+    v = max_dpp<kBcast15, 0xa>(v);
+    v = max_dpp<kBcast31, 0xc>(v);
+    return __builtin_amdgcn_readlane(v, 63);
+}
 __device__ __forceinline__ int wave_scan(int v) {
     v += dpp<kShr + 1>(0, v);
     v += dpp<kShr + 2>(0, v);
@@ -79,26 +91,59 @@ __device__ __forceinline__ int wave_scan(int v) {
     v += dpp<kBcast31, 0xc>(0, v);
     return v;
 }
+// Tile `want` of the segments' tiles of kRows rows (rep to a position).  Up to 64 segments: those
+// with the most keys first (by powers of two), so that no long tile starts when the others are done;
+// more: in order.  With a causal mask a segment's last rows first, which see the most.
 __device__ __forceinline__ Tile find_tile(const AttentionArgs& a, int rep, int want) {
-    const int lane = threadIdx.x & 63, M = (int)a.Mq;
-    int before = 0;
+    const int lane = threadIdx.x & 63, M = (int)a.Mq, Mk = (int)a.Mk;
+    int next[4];
+    auto fetch = [&](int i) {
+        const int at = min(i, a.n - 1);
+        next[0] = a.q_start[at];
+        next[1] = a.q_start[at + 1];
+        next[2] = a.kv_start[at];
+        next[3] = a.kv_start[at + 1];
+    };
+    fetch(lane);
     for (int c = 0; c < a.n; c += 64) {
-        const int i = c + lane;
-        int r0 = 0, len = 0;
-        if (i < a.n) {
-            r0 = min(max(a.q_start[i], 0), M);
-            len = max(min(max(a.q_start[i + 1], 0), M) - r0, 0);
+        const int q0 = min(max(next[0], 0), M), k0 = min(max(next[2], 0), Mk);
+        const int len = c + lane < a.n ? max(min(max(next[1], 0), M) - q0, 0) : 0;
+        const int keys = max(min(max(next[3], 0), Mk) - k0, 0);
+        if (c + 64 < a.n) fetch(c + 64 + lane);
+        const int nt = (len * rep + kRows - 1) / kRows;
+        // a lane's turn: the number of its keys' bits, one turn for all of many segments; -1: no tile
+        int turn = nt == 0 ? -1 : a.n > 64 ? 0 : 32 - __clz(keys);
+        for (int now = a.n > 64 ? 0 : wave_max(turn); now >= 0; now = a.n > 64 ? -1 : wave_max(turn)) {
+            const int mine = turn == now ? nt : 0, sum = wave_scan(mine);
+            const unsigned long long past = __ballot(sum > want);
+            if (past != 0) {
+                const int src = __ffsll(past) - 1;
+                const int off = want - __builtin_amdgcn_readlane(sum - mine, src);
+                const int tile = a.causal ? __builtin_amdgcn_readlane(nt, src) - 1 - off : off;
+                return Tile{c + src, __builtin_amdgcn_readlane(q0, src), __builtin_amdgcn_readlane(len, src),
+                            __builtin_amdgcn_readlane(k0, src), __builtin_amdgcn_readlane(keys, src), tile * kRows};
+            }
+            want -= __builtin_amdgcn_readlane(sum, 63);
+            if (turn == now) turn = -1;
         }
-        const int nt = (len * rep + kRows - 1) / kRows, sum = wave_scan(nt);
-        const unsigned long long past = __ballot(before + sum > want);
-        if (past != 0) {
-            const int src = __ffsll(past) - 1;
-            const int off = want - before - __builtin_amdgcn_readlane(sum - nt, src);
-            return Tile{c + src, __builtin_amdgcn_readlane(r0, src), __builtin_amdgcn_readlane(len, src), off * kRows};
-        }
-        before += __builtin_amdgcn_readlane(sum, 63);
     }
-    return Tile{-1, 0, 0, 0};
+    return Tile{-1, 0, 0, 0, 0, 0};
+}
+
+// The keys that packed row `row` of a segment sees: those below.
+struct Limit {
+    int causal, rep, keys, prefix, off;
+    __device__ __forceinline__ Limit(const AttentionArgs& a, int seg, int len, int keys_)
+        : causal(a.causal), rep(a.H / a.G), keys(keys_),
+          prefix(a.prefix == nullptr ? 0 : min(max(a.prefix[seg], 0), keys_)), off(keys_ - len) {}
+    __device__ __forceinline__ int of(int row) const {
+        return causal ? min(max(max(prefix, row / rep + off + 1), 0), keys) : keys;
+    }
+};
+
+// Tiles of keys that one of a row tile's workgroups takes, of `tiles` in all.
+__device__ __forceinline__ int part_tiles(const AttentionArgs& a, int tiles) {
+    return a.splits == 1 ? tiles : max(a.part, (tiles + a.splits - 1) / a.splits);
 }
 
 __device__ __forceinline__ f32x16 mfma32(bf16x8 x, bf16x8 y, f32x16 c) {
@@ -367,16 +412,13 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
     const int xcd = blockIdx.x & 7, lo = total >> 3, more = total & 7;
     const int item = xcd * lo + min(xcd, more) + (int)(blockIdx.x >> 3);
     const int split = item % a.splits, gt = item / a.splits, g = gt / a.tiles;
-    // last rows first: with a causal mask they have the most keys
-    const Tile t = find_tile(a, rep, a.causal ? a.tiles - 1 - (gt - g * a.tiles) : gt - g * a.tiles);
+    const Tile t = find_tile(a, rep, gt - g * a.tiles);
     if (t.seg < 0) return;
-    const int Mk = (int)a.Mk, k0 = min(max(a.kv_start[t.seg], 0), Mk);
-    const int klen = max(min(max(a.kv_start[t.seg + 1], 0), Mk) - k0, 0);
-    const int rows = min(kRows, t.len * rep - t.row0);
-    const int prefix = a.prefix == nullptr ? 0 : min(max(a.prefix[t.seg], 0), klen), off = klen - t.len;
-    auto limit_of = [&](int row) {
-        return a.causal ? min(max(max(prefix, row / rep + off + 1), 0), klen) : klen;
-    };
+    const int klen = t.keys, rows = min(kRows, t.len * rep - t.row0);
+    const Limit limit(a, t.seg, t.len, klen);
+    // the workgroup's tiles: its part of those that its last row sees
+    const int tiles = (limit.of(t.row0 + rows - 1) + kKeys - 1) / kKeys, per = part_tiles(a, tiles);
+    const int first = split * per, last = min(first + per, tiles);
 
     // the lane's row, or the last one's again
     const bool active = wave * 32 < rows;
@@ -385,8 +427,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
     Rows<NB, MOD> w;
     w.m = -INFINITY;
     w.l = 0.f;
-    w.limit = limit_of(row);
-    w.at = pos + off;
+    w.limit = limit.of(row);
+    w.at = pos + limit.off;
     w.slope = (MOD & kBias) != 0 ? a.slopes[head] * kLog2e : 0.f;
     w.c0 = a.scale * kLog2e;
     w.c1 = a.cap * kLog2e;
@@ -403,11 +445,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
 #pragma unroll
         for (int i = 0; i < 16; ++i) w.O[b][i] = 0.f;
 
-    // the workgroup's tiles, those that all its rows see whole, and the keys that the wave's last row sees
-    const int tiles = (limit_of(t.row0 + rows - 1) + kKeys - 1) / kKeys, per = (tiles + a.splits - 1) / a.splits;
-    const int first = split * per, last = min(first + per, tiles);
-    const int whole = min(max(limit_of(t.row0) / kKeys, first), last);
-    const int most = active ? limit_of(t.row0 + min(wave * 32 + 31, rows - 1)) : 0;
+    // of them those that all its rows see whole; and the keys that the wave's last row sees
+    const int whole = min(max(limit.of(t.row0) / kKeys, first), last);
+    const int most = active ? limit.of(t.row0 + min(wave * 32 + 31, rows - 1)) : 0;
 
     // copies: an instruction fills 1 KB, kLanes lanes a row, kStep rows
     constexpr int kLanes = L::kSlots, kStep = 64 / kLanes;
@@ -416,8 +456,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
     const uint32_t smem0 = (uint32_t)(uintptr_t)(lds_u8*)smem;
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(smem0 + wave * kCopies * 1024);
     const uint32_t kbytes = (uint32_t)(a.k_stride * 2), vbytes = (uint32_t)(a.v_stride * 2);
-    const char* kp = (const char*)a.k + ((int64_t)k0 * a.k_stride + (int64_t)g * D) * 2;
-    const char* vp = (const char*)a.v + ((int64_t)k0 * a.v_stride + (int64_t)g * D) * 2;
+    const char* kp = (const char*)a.k + ((int64_t)t.k0 * a.k_stride + (int64_t)g * D) * 2;
+    const char* vp = (const char*)a.v + ((int64_t)t.k0 * a.v_stride + (int64_t)g * D) * 2;
     // where each copy reads, from the tile's first key on, and its lanes with a channel
     uint32_t koff[kCopies], voff[kCopies];
     uint64_t kon[kCopies], von;
@@ -507,35 +547,54 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
         }
 }
 
-// Joins the splits of one row (position, head) a wave, in their order; lane: channels 2 lane, 2 lane + 1.
+// Joins the parts of rows (position, head), PER waves a row: each takes every PER-th part in their
+// order, then the waves' sums are added in theirs.  Lane: part `lane`'s maximum and sum, and channels
+// 2 lane, 2 lane + 1.  Rows between the first offset and the last are the segments'.
+template <int PER>
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t r = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6), m = r / a.H;
-    if (m >= a.Mq) return;
-    const int head = (int)(r - m * a.H);
-    const int seg = find_segment(a.q_start, a.n, (int)m);
-    if (seg < 0 || a.q_start[seg + 1] <= m) return;
-    const int64_t all = (int64_t)a.splits * a.Mq * a.H;
-    const float* o = (const float*)a.work;
-    const float* ml = o + all * a.D;
-    float top = -INFINITY;
-    for (int s = 0; s < a.splits; ++s) top = __builtin_elementwise_maximum(top, ml[part_row(a, s, m, head) * 2]);
-    float l = 0.f, x = 0.f, y = 0.f;
-    for (int s = 0; s < a.splits; ++s) {
-        const int64_t at = part_row(a, s, m, head);
-        const float ms = ml[at * 2];
-        if (ms == -INFINITY) continue;
-        const float f = __builtin_amdgcn_exp2f(ms - top);
-        l = fmaf(ml[at * 2 + 1], f, l);
-        if (2 * lane < a.D) {
-            const float2 v = *(const float2*)(o + at * a.D + 2 * lane);
-            x = fmaf(v.x, f, x);
-            y = fmaf(v.y, f, y);
+    __shared__ float2 sums[kWaves][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t all = a.Mq * a.H, r = std::min((int64_t)blockIdx.x * (kWaves / PER) + wave / PER, all - 1);
+    const int64_t m = r / a.H, head = r - m * a.H;
+    const float* o = (const float*)a.work + r * a.D;
+    const float2* ml = (const float2*)((const float*)a.work + all * a.splits * a.D) + r;
+    const float2 mine = lane < a.splits ? ml[all * lane] : make_float2(-INFINITY, 0.f);
+    const bool live = m >= a.q_start[0] && m < a.q_start[a.n];
+    float top = mine.x;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) top = __builtin_elementwise_maximum(top, __shfl_xor(top, d, kWave));
+    const float f = mine.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mine.x - top);
+    float l = mine.y * f;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) l += __shfl_xor(l, d, kWave);
+    const int parts = live ? 64 - __clzll((long long)__ballot(!(f == 0.f))) : 0;   // those past hold nothing
+    float2 sum = make_float2(0.f, 0.f);
+    if (2 * lane < a.D) {
+        for (int s = wave % PER; s < parts; s += 4 * PER) {   // four loads in flight
+            float2 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[u] = *(const float2*)(o + all * min(s + u * PER, parts - 1) * a.D + 2 * lane);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool in = s + u * PER < parts;
+                const float g = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), min(s + u * PER, parts - 1)));
+                sum.x = fmaf(in ? v[u].x : 0.f, in ? g : 0.f, sum.x);
+                sum.y = fmaf(in ? v[u].y : 0.f, in ? g : 0.f, sum.y);
+            }
         }
     }
+    if constexpr (PER > 1) {
+        sums[wave][lane] = sum;
+        __syncthreads();
+#pragma unroll
+        for (int w = 1; w < PER; ++w) {
+            sum.x += sums[wave / PER * PER + w][lane].x;
+            sum.y += sums[wave / PER * PER + w][lane].y;
+        }
+    }
+    if (!live || wave % PER > 0 || 2 * lane >= a.D) return;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (2 * lane < a.D)
-        *(uint32_t*)((uint16_t*)a.out + m * a.out_stride + (int64_t)head * a.D + 2 * lane) = pack_bf16(x * inv, y * inv);
+    *(uint32_t*)((uint16_t*)a.out + m * a.out_stride + head * a.D + 2 * lane) = pack_bf16(sum.x * inv, sum.y * inv);
 }
 
 // The most tiles that any cut of Mq positions into n segments can need.
@@ -543,13 +602,20 @@ int64_t max_tiles(int64_t Mq, int rep, int n) {
     return std::min(Mq * ((rep + kRows - 1) / kRows), (Mq * rep + (int64_t)n * (kRows - 1)) / kRows);
 }
 
-// Parts of a tile's keys: enough for two workgroups a CU, each at least 4 tiles of keys of the longest
-// segment there may be.
-int split_count(int64_t Mq, int64_t Mk, int H, int G, int n) {
-    const int64_t items = max_tiles(Mq, H / G, n) * G;
-    if (items == 0) return 1;
-    const int64_t want = 2 * kCus / items, least = Mk / (4 * kKeys);
-    return (int)std::max<int64_t>(1, std::min(want, least));
+// The most parts of a row tile's keys, and the least tiles of a part: as many as give every CU a few
+// workgroups, none where there are two a CU without.  A part costs its rows' fp32 O to write and read
+// again, so tiles of few rows are cut finer (us: 32 rows, 2048 keys, 24 heads of 128, parts of 4 tiles
+// 13.1, of 8 16.2; 1024 rows and keys, 16 heads of 64, one part 15.6, two of 8 tiles 18.6; 8 single
+// rows over up to 8000 keys, 8 kv heads, three workgroups a CU at most 28.5, six 32).
+struct Split {
+    int most, part;
+};
+Split split_of(int64_t Mq, int64_t Mk, int H, int G, int n) {
+    const int64_t tiles = max_tiles(Mq, H / G, n), items = tiles * G;
+    if (items == 0 || items >= 2 * kCus) return Split{1, 1};
+    const bool few = Mq * (H / G) <= tiles * 32;
+    const int64_t want = (few ? 3 : 2) * kCus / items, part = few ? 4 : 12;
+    return Split{(int)std::max<int64_t>(1, std::min({want, Mk / (part * kKeys), (int64_t)kWave})), (int)part};
 }
 
 template <int NB>
@@ -568,21 +634,28 @@ bool attention_fits(int64_t Mq, int H, int G, int n) {
 }
 
 int64_t attention_workspace_bytes(int64_t Mq, int64_t Mk, int H, int G, int D, int n) {
-    const int splits = split_count(Mq, Mk, H, G, n);
+    const int splits = split_of(Mq, Mk, H, G, n).most;
     return splits <= 1 ? 0 : splits * Mq * H * (D + 2) * 4;
 }
 
 void launch_attention(const AttentionArgs& in, hipStream_t st) {
     AttentionArgs a = in;
     a.tiles = (int)max_tiles(a.Mq, a.H / a.G, a.n);
-    a.splits = split_count(a.Mq, a.Mk, a.H, a.G, a.n);
+    const Split split = split_of(a.Mq, a.Mk, a.H, a.G, a.n);
+    a.splits = split.most;
+    a.part = split.part;
     if (a.D <= 32) launch<1>(a, st);
     else if (a.D <= 64) launch<2>(a, st);
     else if (a.D <= 96) launch<3>(a, st);
     else launch<4>(a, st);
     if (a.splits > 1) {
+        // a row's waves read their parts side by side; with many rows there are waves enough (2048 rows of
+        // 8 heads, 2 parts: the call 33.6 us, with four waves a row 42)
         const int64_t rows = a.Mq * a.H;
-        hipLaunchKernelGGL(attention_join_kernel, dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a);
+        if (rows >= 4096)
+            hipLaunchKernelGGL(attention_join_kernel<1>, dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a);
+        else
+            hipLaunchKernelGGL(attention_join_kernel<kWaves>, dim3((unsigned)rows), dim3(kThreads), 0, st, a);
     }
 }
 

@@ -191,7 +191,8 @@ struct AttentionArgs {
     void* out;               // bf16 [Mq, H D]
     int64_t out_stride;
     void* work;
-    int splits, tiles;       // parts of a tile's keys, and the most row tiles (set by the launcher)
+    int tiles;               // the most row tiles (set by the launcher, as what follows)
+    int splits, part;        // the most parts of a row tile's keys, and the least key tiles of one
 };
 
 // Largest workspace the K split of svdq_gemm_w4a4_packed uses (its split count is capped so
