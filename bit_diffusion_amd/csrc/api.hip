@@ -951,7 +951,7 @@ svdq_status svdq_rotary(int64_t M, int32_t n_q_heads, int32_t n_k_heads, int32_t
     SVDQ_TRY(check_dtype(x_dtype, "x_dtype"));
     SVDQ_TRY(check_dtype(out_dtype, "out_dtype"));
     const int64_t xsz = x_dtype == SVDQ_DT_BF16 ? 2 : 4, osz = out_dtype == SVDQ_DT_BF16 ? 2 : 4;
-    bool vec = head_dim % (pairing == SVDQ_ROTARY_HALVES ? 16 : 8) == 0;
+    bool vec = head_dim % (pairing == SVDQ_ROTARY_HALVES ? 16 : 8) == 0, word = pairing == SVDQ_ROTARY_INTERLEAVED;
     const auto rows = [&](const void* in, int64_t stride, const void* to, int64_t to_stride, int64_t heads, const char* in_name,
                           const char* stride_name, const char* to_name, const char* to_stride_name) -> svdq_status {
         if (heads == 0) return SVDQ_OK;
@@ -961,6 +961,7 @@ svdq_status svdq_rotary(int64_t M, int32_t n_q_heads, int32_t n_k_heads, int32_t
         SVDQ_TRY(check_stride(to_stride, heads * head_dim, to_stride_name));
         if (in != nullptr && in == to && (x_dtype != out_dtype || stride != to_stride))
             return fail(SVDQ_ERR_INVALID_ARG, "%s is %s but their types or strides differ", to_name, in_name);
+        word = word && aligned(in, 2 * xsz) && aligned(to, 2 * osz) && stride % 2 == 0 && to_stride % 2 == 0;
         vec = vec && aligned(in, 16) && aligned(to, 16) && stride * xsz % 16 == 0 && to_stride * osz % 16 == 0;
         return SVDQ_OK;
     };
@@ -977,6 +978,7 @@ svdq_status svdq_rotary(int64_t M, int32_t n_q_heads, int32_t n_k_heads, int32_t
     a.out_bf16 = out_dtype == SVDQ_DT_BF16 ? 1 : 0;
     a.q_out = q_out; a.q_out_stride = q_out_stride; a.k_out = k_out; a.k_out_stride = k_out_stride;
     a.vec = vec;
+    a.word = word;
     svdq::launch_rotary(a, reinterpret_cast<hipStream_t>(stream));
     return after_launch("svdq_rotary");
 }

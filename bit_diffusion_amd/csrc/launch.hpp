@@ -170,7 +170,8 @@ struct RotaryArgs {
     int64_t q_out_stride;
     void* k_out;
     int64_t k_out_stride;
-    int vec;                 // rows take 16-byte accesses of 8 channels (pairs of 4)
+    int vec;                 // rows take accesses of 8 channels (halves: 8 pairs), 16-byte aligned
+    int word;                // pairs are side by side, rows aligned to a pair
 };
 
 struct AttentionArgs {

@@ -12,8 +12,7 @@
 // Bound: memory, q and k once in and once out.  Aligned heads: a lane holds 8 channels (16 bytes
 // of bf16) in adjacent pairs, or 8 from either half, and a head is a group of 8, 16 or 32 lanes of
 // one wave, so the norm's sum needs no LDS; the next head is loaded before this one is turned, the
-// first before the table is made.  Other head widths and alignments: a wave takes a head, a lane
-// single pairs.
+// first before the table is made.  Other head widths and alignments: a lane holds single pairs.
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -49,7 +48,7 @@ __device__ __forceinline__ void sync() {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// The sum over each LANES (8, 16, 32, 64) neighbouring lanes, in all of them.
+// The sum over each LANES (8, 16, 32) neighbouring lanes, in all of them.
 template <int LANES>
 __device__ __forceinline__ float group_sum(float v) {
     v += dpp<0xB1>(0.f, v);     // the neighbour
@@ -57,9 +56,25 @@ __device__ __forceinline__ float group_sum(float v) {
     v += dpp<0x141>(0.f, v);    // the other half of eight, mirrored
     if constexpr (LANES > 8) v += dpp<0x140>(0.f, v);
     if constexpr (LANES > 16) v += __shfl_xor(v, 16, kWave);
-    if constexpr (LANES > 32) v += __shfl_xor(v, 32, kWave);
     return v;
 }
+
+// A group of lanes' head: its row in the workgroup and its number there; `by` heads further each time.
+struct Item {
+    int r, h;
+};
+struct Step {
+    int heads, r, h;
+    __device__ __forceinline__ Step(int by, int heads_) : heads(heads_), r(by / heads_), h(by - by / heads_ * heads_) {}
+    __device__ __forceinline__ void next(Item& t) const {
+        t.r += r;
+        t.h += h;
+        if (t.h >= heads) {
+            t.h -= heads;
+            ++t.r;
+        }
+    }
+};
 
 // 8 channels as loaded.
 template <bool BF16>
@@ -115,19 +130,6 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int per)
                 if (a.k_weight != nullptr) wk[n][j] = bf16_to_f32(((const uint16_t*)a.k_weight)[ch[n] + j]);
             }
     }
-    // the lane's items: head and row, kHeads items further each time
-    const int step_r = kHeads / heads, step_h = kHeads - step_r * heads;
-    struct Item {
-        int r, h;
-    };
-    auto next = [&](Item& t) {
-        t.r += step_r;
-        t.h += step_h;
-        if (t.h >= heads) {
-            t.h -= heads;
-            ++t.r;
-        }
-    };
     Vec<XBF> v[NV];
     auto fetch = [&](const Item& t) {
         if (t.r >= rows || !on) return;
@@ -136,6 +138,7 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int per)
 #pragma unroll
         for (int n = 0; n < NV; ++n) v[n].load(q ? a.q : a.k, at + ch[n]);
     };
+    const Step step(kHeads, heads);
     Item t{first / heads, first % heads}, ahead = t;
     fetch(t);                   // on its way while the table is made
     fill_table(a, row0, rows, table);
@@ -149,7 +152,7 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int per)
             for (int j = 0; j < 8; ++j) x[n][j] = 0.f;
             if (mine) v[n].get(x[n]);
         }
-        next(ahead);
+        step.next(ahead);
         fetch(ahead);
         if (a.q_weight != nullptr || a.k_weight != nullptr) {
             float s = 0.f;
@@ -182,58 +185,102 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int per)
     }
 }
 
-// Any even D and any alignment: a wave takes a head, a lane the pairs lane and lane + 64.
-template <bool XBF, bool OBF>
+// The two channels of a pair: side by side and aligned as one (WORD), or anyhow.
+template <bool WORD, bool BF16>
+__device__ __forceinline__ float2 load_pair(const void* p, int64_t at, int a, int b) {
+    if constexpr (WORD && BF16) {
+        const uint32_t w = *(const uint32_t*)((const uint16_t*)p + at + a);
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    } else if constexpr (WORD) {
+        return *(const float2*)((const float*)p + at + a);
+    } else if constexpr (BF16) {
+        return make_float2(bf16_to_f32(((const uint16_t*)p)[at + a]), bf16_to_f32(((const uint16_t*)p)[at + b]));
+    } else {
+        return make_float2(((const float*)p)[at + a], ((const float*)p)[at + b]);
+    }
+}
+template <bool WORD, bool BF16>
+__device__ __forceinline__ void store_pair(void* p, int64_t at, int a, int b, float2 v) {
+    if constexpr (WORD && BF16) {
+        *(uint32_t*)((uint16_t*)p + at + a) = pack_bf16(v.x, v.y);
+    } else if constexpr (WORD) {
+        *(float2*)((float*)p + at + a) = v;
+    } else if constexpr (BF16) {
+        const uint32_t w = pack_bf16(v.x, v.y);
+        ((uint16_t*)p)[at + a] = (uint16_t)w;
+        ((uint16_t*)p)[at + b] = (uint16_t)(w >> 16);
+    } else {
+        ((float*)p)[at + a] = v.x;
+        ((float*)p)[at + b] = v.y;
+    }
+}
+
+// Any even D and any alignment: as above, a lane holding the pairs lane, lane + LANES, ...
+template <int LANES, int NP, bool WORD, bool XBF, bool OBF>
 __global__ __launch_bounds__(kThreads) void rotary_pairs_kernel(RotaryArgs a, int per) {
     __shared__ float2 table[kRows * kMaxPairs];
     const int64_t row0 = (int64_t)blockIdx.x * per;
-    const int rows = (int)min((int64_t)per, a.M - row0), P = a.D >> 1;
+    const int rows = (int)min((int64_t)per, a.M - row0), P = a.D >> 1, heads = a.q_heads + a.k_heads;
+    constexpr int kHeads = kThreads / LANES;
+    const int l = threadIdx.x % LANES, first = threadIdx.x / LANES;
+    const float inv_d = 1.f / (float)a.D;
+    int ca[NP], cb[NP];
+    float2 wq[NP], wk[NP];
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        const int p = l + n * LANES;
+        ca[n] = WORD || !a.halves ? 2 * p : p;
+        cb[n] = WORD || !a.halves ? 2 * p + 1 : p + P;
+        wq[n] = wk[n] = make_float2(1.f, 1.f);
+        if (p < P && a.q_weight != nullptr) wq[n] = load_pair<false, true>(a.q_weight, 0, ca[n], cb[n]);
+        if (p < P && a.k_weight != nullptr) wk[n] = load_pair<false, true>(a.k_weight, 0, ca[n], cb[n]);
+    }
+    float2 v[NP];
+    auto fetch = [&](const Item& t) {
+        if (t.r >= rows) return;
+        const bool q = t.h < a.q_heads;
+        const int64_t at = (row0 + t.r) * (q ? a.q_stride : a.k_stride) + (int64_t)(q ? t.h : t.h - a.q_heads) * a.D;
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+            if (l + n * LANES < P) v[n] = load_pair<WORD, XBF>(q ? a.q : a.k, at, ca[n], cb[n]);
+    };
+    const Step step(kHeads, heads);
+    Item t{first / heads, first % heads}, ahead = t;
+    fetch(t);
     fill_table(a, row0, rows, table);
     sync();
-    const int lane = threadIdx.x & 63, heads = a.q_heads + a.k_heads;
-    for (int i = threadIdx.x >> 6; i < rows * heads; i += kThreads / 64) {
-        const int r = i / heads, h = i - r * heads;
-        const bool q = h < a.q_heads;
-        const int hh = q ? h : h - a.q_heads;
-        const int64_t at = (row0 + r) * (q ? a.q_stride : a.k_stride) + (int64_t)hh * a.D;
-        const int64_t to = (row0 + r) * (q ? a.q_out_stride : a.k_out_stride) + (int64_t)hh * a.D;
-        const void* src = q ? a.q : a.k;
-        void* dst = q ? a.q_out : a.k_out;
-        const uint16_t* w = (const uint16_t*)(q ? a.q_weight : a.k_weight);
-        float x[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    for (; __any(t.r < rows); t = ahead) {
+        const bool q = t.h < a.q_heads, mine = t.r < rows;
+        float2 x[NP];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int n = 0; n < NP; ++n) x[n] = mine && l + n * LANES < P ? v[n] : make_float2(0.f, 0.f);
+        step.next(ahead);
+        fetch(ahead);
+        if (a.q_weight != nullptr || a.k_weight != nullptr) {
+            float s = 0.f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int p = lane + u * 64, c = a.halves ? p + j * P : 2 * p + j;
-                if (p < P) x[u][j] = XBF ? bf16_to_f32(((const uint16_t*)src)[at + c]) : ((const float*)src)[at + c];
+            for (int n = 0; n < NP; ++n) {
+                s = fmaf(x[n].x, x[n].x, s);
+                s = fmaf(x[n].y, x[n].y, s);
             }
-        if (w != nullptr) {
-            float s = x[0][0] * x[0][0];
-            s = fmaf(x[0][1], x[0][1], s);
-            s = fmaf(x[1][0], x[1][0], s);
-            s = fmaf(x[1][1], x[1][1], s);
-            s = __builtin_amdgcn_rsqf(fmaf(group_sum<64>(s), 1.f / (float)a.D, a.eps));
+            s = __builtin_amdgcn_rsqf(fmaf(group_sum<LANES>(s), inv_d, a.eps));
+            if ((q ? a.q_weight : a.k_weight) != nullptr) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int p = lane + u * 64, c = a.halves ? p + j * P : 2 * p + j;
-                    if (p < P) x[u][j] *= s * bf16_to_f32(w[c]);
+                for (int n = 0; n < NP; ++n) {
+                    x[n].x *= s * (q ? wq[n].x : wk[n].x);
+                    x[n].y *= s * (q ? wq[n].y : wk[n].y);
                 }
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int p = lane + u * 64;
-            if (p >= P) continue;
-            const float2 cs = table[r * P + p];
-            const float y[2] = {fmaf(x[u][0], cs.x, -x[u][1] * cs.y), fmaf(x[u][0], cs.y, x[u][1] * cs.x)};
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int c = a.halves ? p + j * P : 2 * p + j;
-                if (OBF) ((uint16_t*)dst)[to + c] = (uint16_t)f32_to_bf16(y[j]);
-                else ((float*)dst)[to + c] = y[j];
             }
+        }
+        if (!mine) continue;
+        const int64_t at = (row0 + t.r) * (q ? a.q_out_stride : a.k_out_stride) + (int64_t)(q ? t.h : t.h - a.q_heads) * a.D;
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const int p = l + n * LANES;
+            if (p >= P) continue;
+            const float2 cs = table[t.r * P + p];
+            store_pair<WORD, OBF>(q ? a.q_out : a.k_out, at, ca[n], cb[n],
+                                  make_float2(fmaf(x[n].x, cs.x, -x[n].y * cs.y), fmaf(x[n].x, cs.y, x[n].y * cs.x)));
         }
     }
 }
@@ -241,25 +288,31 @@ __global__ __launch_bounds__(kThreads) void rotary_pairs_kernel(RotaryArgs a, in
 template <bool XBF, bool OBF>
 void launch(const RotaryArgs& a, hipStream_t st) {
     const int heads = a.q_heads + a.k_heads, vecs = (a.halves ? a.D / 2 : a.D) / 8;
-    const int at_once = !a.vec ? kThreads / 64 : kThreads / (vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32);
+    const int lanes = a.vec ? (vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32) : a.D <= 128 ? 16 : 32, at_once = kThreads / lanes;
     const int64_t rows = std::min<int64_t>(a.M / kCus, (kPerGroup * at_once + heads - 1) / heads);
     const int per = (int)std::min<int64_t>(kRows, std::max<int64_t>(1, rows));
     const dim3 grid((unsigned)((a.M + per - 1) / per)), block(kThreads);
     if (!a.vec) {
-        hipLaunchKernelGGL((rotary_pairs_kernel<XBF, OBF>), grid, block, 0, st, a, per);
+        auto pairs = [&](auto n, auto np) {
+            if (a.word) hipLaunchKernelGGL((rotary_pairs_kernel<n.value, np.value, true, XBF, OBF>), grid, block, 0, st, a, per);
+            else hipLaunchKernelGGL((rotary_pairs_kernel<n.value, np.value, false, XBF, OBF>), grid, block, 0, st, a, per);
+        };
+        if (a.D <= 64) pairs(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
+        else if (a.D <= 128) pairs(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
+        else pairs(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{});
         return;
     }
-    auto go = [&](auto lanes) {
-        if constexpr (lanes.value < 32) {
+    auto go = [&](auto n) {
+        if constexpr (n.value < 32) {
             if (a.halves) {
-                hipLaunchKernelGGL((rotary_kernel<lanes.value, true, XBF, OBF>), grid, block, 0, st, a, per);
+                hipLaunchKernelGGL((rotary_kernel<n.value, true, XBF, OBF>), grid, block, 0, st, a, per);
                 return;
             }
         }
-        hipLaunchKernelGGL((rotary_kernel<lanes.value, false, XBF, OBF>), grid, block, 0, st, a, per);
+        hipLaunchKernelGGL((rotary_kernel<n.value, false, XBF, OBF>), grid, block, 0, st, a, per);
     };
-    if (vecs <= 8) go(std::integral_constant<int, 8>{});
-    else if (vecs <= 16) go(std::integral_constant<int, 16>{});
+    if (lanes == 8) go(std::integral_constant<int, 8>{});
+    else if (lanes == 16) go(std::integral_constant<int, 16>{});
     else go(std::integral_constant<int, 32>{});   // never pairs of halves, which have 16 vectors at most
 }
 
