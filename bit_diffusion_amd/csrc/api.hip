@@ -880,13 +880,16 @@ svdq_status svdq_layer_norm(int64_t M, int32_t C, int32_t n_segments, float eps,
         return fail(SVDQ_ERR_INVALID_ARG, "out is x but their types or strides differ");
     if (out != nullptr && out == y && (out_dtype != y_dtype || out_stride != y_stride))
         return fail(SVDQ_ERR_INVALID_ARG, "out is y but their types or strides differ");
-    const auto fours = [](const void* p, int64_t stride, size_t esz) {
-        return p == nullptr || (aligned(p, 4 * esz) && stride % 4 == 0);
+    const auto takes = [&](int n) {   // accesses of n elements
+        const auto rows = [&](const void* p, int64_t stride, size_t esz) {
+            return p == nullptr || (aligned(p, n * esz) && stride % n == 0);
+        };
+        return C % n == 0 && rows(x, x_stride, xsz) && rows(y, y_stride, ysz) && rows(weight, 0, 2) && rows(bias, 0, 2) &&
+               rows(mod_gate, mod_stride, msz) && rows(mod_scale, mod_stride, msz) && rows(mod_shift, mod_stride, msz) &&
+               rows(x_out, x_out_stride, xsz) && rows(out, out_stride, osz);
     };
-    const bool vec = C % 4 == 0 && fours(x, x_stride, xsz) && fours(y, y_stride, ysz) && fours(weight, 0, 2) &&
-                     fours(bias, 0, 2) && fours(mod_gate, mod_stride, msz) && fours(mod_scale, mod_stride, msz) &&
-                     fours(mod_shift, mod_stride, msz) && fours(x_out, x_out_stride, xsz) && fours(out, out_stride, osz);
-    if (!vec && C > 8192)
+    const int vec = takes(4) ? 4 : takes(2) ? 2 : 1;
+    if (vec < 4 && C > 8192)
         return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "C %d exceeds 8192, the maximum for rows that do not take accesses of "
                                                  "4 elements", C);
     SVDQ_TRY(check_current_device());

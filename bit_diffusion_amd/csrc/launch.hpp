@@ -145,7 +145,7 @@ struct LayerNormArgs {
     int out_bf16;
     void* out;
     int64_t out_stride;
-    int vec;                 // every row takes accesses of 4 elements
+    int vec;                 // elements of an access that every row takes: 4, 2 or 1
 };
 
 struct RotaryArgs {

@@ -26,7 +26,6 @@ namespace svdq {
 namespace {
 
 constexpr int kCus = 256;    // of the GPU
-constexpr int kVec = 4;      // columns of a thread's access where rows are aligned
 constexpr int kWaves = 16;   // of the widest workgroup
 constexpr int kWavesCu = 18; // a CU's share of the rows goes over workgroups of so many waves in all (4608
                              // rows of 6 waves: 28.7 us, with 12 waves 30.5, 24 29.4, 48 31.9)
@@ -51,7 +50,7 @@ __device__ __forceinline__ void sync() {
 // VEC columns at element `at`: as loaded, and as fp32.
 template <int VEC, bool BF16>
 struct Raw {
-    uint32_t u[VEC == 1 ? 1 : BF16 ? 2 : 4];
+    uint32_t u[BF16 ? (VEC + 1) / 2 : VEC];
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (uint32_t& w : u) w = 0;
@@ -59,8 +58,10 @@ struct Raw {
     __device__ __forceinline__ void load(const void* p, int64_t at) {
         if constexpr (VEC == 1) {
             u[0] = BF16 ? ((const uint16_t*)p)[at] : ((const uint32_t*)p)[at];
-        } else if constexpr (BF16) {
-            const uint2 w = *(const uint2*)((const uint16_t*)p + at);
+        } else if constexpr (BF16 && VEC == 2) {
+            u[0] = *(const uint32_t*)((const uint16_t*)p + at);
+        } else if constexpr (BF16 || VEC == 2) {
+            const uint2 w = *(const uint2*)((const char*)p + at * (BF16 ? 2 : 4));
             u[0] = w.x; u[1] = w.y;
         } else {
             const uint4 w = *(const uint4*)((const uint32_t*)p + at);
@@ -86,12 +87,14 @@ __device__ __forceinline__ void load(const void* p, int64_t at, bool bf16, float
 template <int VEC>
 __device__ __forceinline__ void store(void* p, int64_t at, bool bf16, const float (&v)[VEC]) {
     if constexpr (VEC == 1) {
-        if (bf16) ((uint16_t*)p)[at] = (uint16_t)f32_to_bf16(v[0]);
+        if (bf16) ((uint16_t*)p)[at] = (uint16_t)pack_bf16(v[0], 0.f);
         else ((float*)p)[at] = v[0];
-    } else if (bf16) {
-        *(uint2*)((uint16_t*)p + at) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    } else if constexpr (VEC == 2) {
+        if (bf16) *(uint32_t*)((uint16_t*)p + at) = pack_bf16(v[0], v[1]);
+        else *(float2*)((float*)p + at) = make_float2(v[0], v[1]);
     } else {
-        *(float4*)((float*)p + at) = make_float4(v[0], v[1], v[2], v[3]);
+        if (bf16) *(uint2*)((uint16_t*)p + at) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        else *(float4*)((float*)p + at) = make_float4(v[0], v[1], v[2], v[3]);
     }
 }
 
@@ -235,22 +238,20 @@ void launch(const LayerNormArgs& a, int threads, hipStream_t st) {
 }  // namespace
 
 void launch_layer_norm(const LayerNormArgs& a, hipStream_t st) {
-    const int n = a.vec ? (a.C + kVec - 1) / kVec : a.C;   // column vectors of a row
+    const int n = a.C / a.vec;   // column vectors of a row
     // two vectors a thread up to 1024 (4608 rows of 768 vectors: 28.7 us, with one 40, with four 31),
     // then as many as leave a row's threads in a workgroup their registers
     const int V = n <= 64 ? 1 : n <= 1024 ? 2 : n <= 2048 ? 4 : 8;
     const int threads = ((n + V - 1) / V + 63) / 64 * 64;
-    if (a.vec) {
-        if (V == 1) launch<kVec, 1, 64>(a, threads, st);
-        else if (V == 2) launch<kVec, 2, 512>(a, threads, st);
-        else if (V == 4) launch<kVec, 4, 512>(a, threads, st);
-        else launch<kVec, 8, 512>(a, threads, st);
-    } else {
-        if (V == 1) launch<1, 1, 64>(a, threads, st);
-        else if (V == 2) launch<1, 2, 512>(a, threads, st);
-        else if (V == 4) launch<1, 4, 512>(a, threads, st);
-        else launch<1, 8, 1024>(a, threads, st);
-    }
+    auto go = [&](auto vec) {
+        if (V == 1) launch<vec.value, 1, 64>(a, threads, st);
+        else if (V == 2) launch<vec.value, 2, 512>(a, threads, st);
+        else if (V == 4) launch<vec.value, 4, 512>(a, threads, st);
+        else launch<vec.value, 8, vec.value == 1 ? 1024 : 512>(a, threads, st);
+    };
+    if (a.vec == 4) go(std::integral_constant<int, 4>{});
+    else if (a.vec == 2) go(std::integral_constant<int, 2>{});
+    else go(std::integral_constant<int, 1>{});
 }
 
 }  // namespace svdq

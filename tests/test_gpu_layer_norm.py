@@ -34,8 +34,8 @@ class Case:
         self.wy = wide(rnd(M, C), self.ys, yd) if residual else None
         self.w = (1 + 0.3 * rnd(C)).to(BF).to(DEV) if affine else None
         self.b = (0.3 * rnd(C)).to(BF).to(DEV) if affine else None
-        # 3 C and C + 1 more: an odd stride where C is odd
-        self.ms = 3 * C + (4 if C % 4 == 0 else 1)
+        # a stride that takes what C takes
+        self.ms = 3 * C + (4 if C % 4 == 0 else 2 - C % 2)
         self.mod = (0.4 * rnd(n, self.ms)).to(md).to(DEV)
         self.gate = self.mod[:, :C] if gate and residual else None
         self.scale, self.mshift = (self.mod[:, C:2 * C], self.mod[:, 2 * C:3 * C]) if mod else (None, None)
@@ -105,6 +105,13 @@ CASES = {
     "up to four vectors": dict(starts=cut(9), C=4096, yd=F32, od=F32),
     "the first of eight": dict(starts=cut(9, 2), C=4100, xd=F32, md=BF),
     "widest": dict(starts=cut(2, 3), C=16384, affine=True),
+    "pairs, one": dict(starts=cut(6, 5), C=126),
+    "pairs, two": dict(starts=cut(6, 5), C=1170, tail=3, xd=F32, md=BF, affine=True),
+    "pairs, four": dict(starts=cut(6, 5), C=2050, od=F32),
+    "pairs, eight": dict(starts=cut(3, 5), C=4098, yd=F32),
+    "pairs, widest": dict(starts=cut(3, 2), C=8190, xd=F32, od=F32),
+    "pairs by a stride": dict(starts=cut(30, 20), C=320, xpad=2),
+    "pairs by an address": dict(starts=cut(30, 20), C=320, xpad=4, ypad=4, opad=4, shift=2),
     "single elements, one": dict(starts=cut(6, 6), C=63, yd=F32),
     "single elements, two": dict(starts=cut(6, 7), C=511, od=F32),
     "single elements, four": dict(starts=cut(6, 0, 0, 7), C=1023, xd=F32, md=BF, affine=True),
@@ -145,7 +152,7 @@ def test_matches_fp64(name):
 @pytest.mark.parametrize("xd", [BF, F32])
 @pytest.mark.parametrize("yd", [BF, F32])
 @pytest.mark.parametrize("od", [BF, F32])
-@pytest.mark.parametrize("C", [200, 1200, 3072, 5000, 63, 333, 777, 2001])
+@pytest.mark.parametrize("C", [200, 1200, 3072, 5000, 122, 1170, 2050, 4102, 63, 333, 2001, 3001])
 def test_types(xd, yd, od, C):
     c = Case(C, cut(11, 0, 6), C, tail=2, xd=xd, yd=yd, od=od, md=BF, affine=True)
     c.call()
