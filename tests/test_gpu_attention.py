@@ -122,6 +122,10 @@ CASES = {
     "single rows, causal": dict(qs=list(range(4)), ks=cut(5000, 64, 0), H=2, G=1, D=72, causal=True),
     "few rows, many keys": dict(qs=cut(40, 2), ks=cut(4000, 1000), H=2, G=1, D=128, cap=20.0),
     "few rows, many keys, 32": dict(qs=cut(40, 2), ks=cut(4000, 1000), H=2, G=1, D=32),
+    "many rows, split": dict(qs=cut(590, 10), ks=cut(2000, 900), H=8, G=8, D=64),
+    "many rows, split, causal": dict(qs=cut(590, 10), ks=cut(2000, 900), H=8, G=8, D=72, causal=True, prefix=[100, 3], tail=5),
+    "eight heads, several lengths": dict(qs=cut(140, 300, 20, 0, 10), ks=cut(500, 30, 0, 7, 129), H=16, G=8, D=64, cap=9.0),
+    "sixteen heads in step": dict(qs=cut(140, 300), H=16, G=16, D=32),
     "many segments": dict(qs=sorted([0] + [i * 37 % 900 for i in range(150)] + [900]), H=2, G=1, D=64),
     "more heads than a tile's rows": dict(qs=cut(3, 1), ks=cut(90, 200), H=300, G=2, D=64, causal=True),
     "sharp": dict(qs=cut(500), H=2, G=2, D=128, sharp=60.0),

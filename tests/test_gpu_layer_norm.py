@@ -152,7 +152,7 @@ def test_matches_fp64(name):
 @pytest.mark.parametrize("xd", [BF, F32])
 @pytest.mark.parametrize("yd", [BF, F32])
 @pytest.mark.parametrize("od", [BF, F32])
-@pytest.mark.parametrize("C", [200, 1200, 3072, 5000, 122, 1170, 2050, 4102, 63, 333, 2001, 3001])
+@pytest.mark.parametrize("C", [200, 1200, 3072, 5000, 9000, 122, 1170, 2050, 4102, 63, 333, 2001, 3001])
 def test_types(xd, yd, od, C):
     c = Case(C, cut(11, 0, 6), C, tail=2, xd=xd, yd=yd, od=od, md=BF, affine=True)
     c.call()

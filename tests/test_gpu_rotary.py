@@ -121,6 +121,20 @@ def test_matches_fp64(name):
     assert all(torch.equal(a, b) for a, b in zip(first, c.o)), "another run gives other bits"
 
 
+TYPES = [dict(M=37, H=4, G=2, pairs=pairs, halves=halves, xd=xd, od=od)
+         for pairs, halves in (([20, 8], False), ([32, 32], False), ([124], False), ([20, 12], True), ([80], True),
+                               ([5, 10], False), ([45], False), ([100, 27], False), ([15], True), ([30, 15], True), ([127], True))
+         for xd in (BF, F32) for od in (BF, F32)]
+
+
+@pytest.mark.parametrize("kw", TYPES)
+def test_types(kw):
+    c = Case(11, **kw)
+    c.call()
+    torch.cuda.synchronize()
+    c.check()
+
+
 @pytest.mark.parametrize("pairs,halves,xd", [([8, 28, 28], False, BF), ([16, 16], True, F32), ([5, 6], False, BF)])
 def test_in_place(pairs, halves, xd):
     c = Case(7, 300, 6, 2, pairs, halves=halves, xd=xd, od=xd)
