@@ -298,17 +298,19 @@ __device__ __forceinline__ void step(Rows<NB, MOD>& w, int key0, uint32_t kb, ui
         }
         return sum;
     };
-    // brings what is there to the maximum with this tile's, where a row's grew by more than `by`
-    auto grow = [&](float by) {
+    // brings rows that need it, or whose maximum grew by more than `by`, to the maximum with this tile's
+    // (the others stay as they are: a row's result does not depend on the rows beside it)
+    auto grow = [&](bool need, float by) {
         float top = s[0][0];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = __builtin_elementwise_maximum(top, s[u][i]);
         top = __builtin_elementwise_maximum(w.m, both_max(top));
-        if (!__any((top - w.m) * unit > by)) return;
-        const float keep = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((w.m - top) * unit);
-        w.m = top;
+        need = need || (top - w.m) * unit > by;
+        if (!__any(need)) return;
+        const float keep = !need || top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((w.m - top) * unit);
+        w.m = need ? top : w.m;
         w.l *= keep;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -317,12 +319,14 @@ __device__ __forceinline__ void step(Rows<NB, MOD>& w, int key0, uint32_t kb, ui
     };
     float sum;
     if constexpr ((MOD & kBias) != 0) {
-        grow(kGrow);
+        grow(false, kGrow);
         sum = weigh();
     } else {
         sum = weigh();
-        if (__any(!(sum < kMost) || w.m == -INFINITY)) {
-            grow(0.f);
+        const bool need = !(sum < kMost) || w.m == -INFINITY;
+        if (__any(need)) {
+            const int other = __shfl_xor((int)need, 32, kWave);   // the row's other half
+            grow(need || other != 0, INFINITY);
             sum = weigh();
         }
     }

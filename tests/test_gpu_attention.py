@@ -194,6 +194,21 @@ def test_what_is_not_seen_does_not_count(bad, causal):
         assert bool(torch.isnan(c.out[hit]).all())
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(cap=9.0), dict(bias=True), dict(causal=True), dict(causal=True, bias=True, cap=5.0)])
+def test_rows_do_not_depend_on_the_rows_beside_them(kw):
+    """The same bits whether the other rows of a segment hold numbers, huge ones or none."""
+    c = Case(12, cut(150, 90), 4, 2, 64, **kw)
+    c.call()
+    torch.cuda.synchronize()
+    ref = c.out.clone()
+    odd = torch.arange(240, device=DEV) % 3 == 1
+    for v in (float("nan"), 3e4, -float("inf")):
+        c.q[odd] = v
+        c.call()
+        torch.cuda.synchronize()
+        assert torch.equal(c.out[~odd], ref[~odd]), v
+
+
 @pytest.mark.parametrize("D", [32, 64, 96, 128])
 def test_infinite_values_where_seen(D):
     """An infinity of v gives its sign to the rows that see it, both signs or a NaN give NaN, in the
