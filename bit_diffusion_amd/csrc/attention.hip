@@ -21,9 +21,9 @@
 // rounded to bf16 (2^-8 of each weight at most, as V's own values were), and summed as rounded, which
 // takes their common error out again; O, maxima and sums are fp32.
 //
-// Maximum.  What the weights are taken against need not be the largest score so far: 2^40 above it
-// bf16 and fp32 hold a weight as well as 1.  So a row keeps the maximum of its first tile, and only
-// where the weights' sum of a tile passes 2^40 are maximum, O and sum brought up to date and the tile's
+// Maximum.  What the weights are taken against need not be the largest score so far: bf16 and fp32
+// hold a weight of 2^16 as well as 1.  So a row keeps the maximum of its first tile, and only
+// where the weights' sum of a tile passes 2^16 are maximum, O and sum brought up to date and the tile's
 // weights formed again (finding the largest score of every tile: 251 -> 260 us at 4608 rows and 24
 // heads of 128).  With a bias by distance scores grow from tile to tile as a rule, and the largest is
 // sought in each; O is rescaled only where it grew by more than 2^8.
@@ -55,7 +55,7 @@ constexpr int kKeys = 64;            // keys of a tile
 constexpr int kCus = 256;            // of the GPU
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;         // growth of a maximum, in powers of two, that O is rescaled for
-constexpr float kMost = 1.1e12f;     // sum of 32 weights past which a row gets a new maximum
+constexpr float kMost = 65536.f;     // sum of 32 weights past which a row gets a new maximum
 
 enum Mod { kPlain = 0, kCap = 1, kBias = 2, kBoth = 3 };
 
@@ -231,6 +231,9 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
     const s16x2 t = __builtin_bit_cast(s16x2, (w & 0x7F807F80u) + 0x00800080u);
     return __builtin_bit_cast(uint32_t, t >> 15);
 }
+__device__ __forceinline__ uint4 finite_only(uint4 v) {
+    return make_uint4(v.x & ~not_finite(v.x), v.y & ~not_finite(v.y), v.z & ~not_finite(v.z), v.w & ~not_finite(v.w));
+}
 // Of a bf16: 1 for infinity, 2^8 for minus infinity, 2^16 for a NaN, else 0, as bf16.
 __device__ __forceinline__ uint32_t kind16(uint32_t v) {
     const uint32_t bad = (v & 0x7F80u) == 0x7F80u;
@@ -331,7 +334,30 @@ __device__ __forceinline__ void step(Rows<NB, MOD>& w, int key0, uint32_t kb, ui
         }
     }
     w.l += sum;
-    uint32_t bad = 0;
+    // values that are not finite, found as what is not 0 after a product with 0: in a masked tile they
+    // are multiplied as 0, and who sees them is looked after below
+    bool bad = false;
+    if constexpr (MASK) {
+        const bf16x2 zeros{(__bf16)0.f, (__bf16)0.f};
+        float z = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const uint4 x = c < 2 ? v[c][b] : v_operand<NB>(vb, b, c);
+                z = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, x.x), zeros, z, false);
+                z = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, x.y), zeros, z, false);
+                z = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, x.z), zeros, z, false);
+                z = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, x.w), zeros, z, false);
+            }
+        bad = __any(z != z);
+        if (bad) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) v[c][b] = finite_only(v[c][b]);
+        }
+    }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         uint4 next[2][NB];
@@ -340,19 +366,17 @@ __device__ __forceinline__ void step(Rows<NB, MOD>& w, int key0, uint32_t kb, ui
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int b = 0; b < NB; ++b) next[c][b] = v_operand<NB>(vb, b, c + 2);
+            if (MASK && bad) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) next[c][b] = finite_only(next[c][b]);
+            }
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                uint4 x = v[c][b];
-                if constexpr (MASK) {
-                    const uint4 n = make_uint4(not_finite(x.x), not_finite(x.y), not_finite(x.z), not_finite(x.w));
-                    bad |= n.x | n.y | n.z | n.w;
-                    x = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
-                }
-                w.O[b] = mfma32(as_bf16x8(x), as_bf16x8(P[2 * half + c]), w.O[b]);
-            }
+            for (int b = 0; b < NB; ++b) w.O[b] = mfma32(as_bf16x8(v[c][b]), as_bf16x8(P[2 * half + c]), w.O[b]);
         if (half == 0) {
 #pragma unroll
             for (int c = 0; c < 2; ++c)
@@ -362,7 +386,7 @@ __device__ __forceinline__ void step(Rows<NB, MOD>& w, int key0, uint32_t kb, ui
     }
     if constexpr (MASK) {
         // who sees how many infinities, minus infinities and NaN (at most 64 of each: exact in fp32)
-        if (__any(bad != 0)) {
+        if (bad) {
             uint4 one[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
