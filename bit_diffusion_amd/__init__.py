@@ -46,17 +46,18 @@ def _dev_ptrs(names, tensors):
     """As _ptr for each of the buffers that a kernel reads or writes: a tensor elsewhere than on
     the current device is refused before its address reaches one."""
     ptrs, current = [], None
-    for i, t in enumerate(tensors):
+    for t in tensors:
         if t is not None and not isinstance(t, int):
             dev = t.get_device()
             if dev != current:
+                name = names[len(ptrs)]
                 if dev < 0:
-                    raise SvdqError(SVDQ_ERR_INVALID_ARG, f"{names[i]} is on {t.device}, not on a GPU")
+                    raise SvdqError(SVDQ_ERR_INVALID_ARG, f"{name} is on {t.device}, not on a GPU")
                 if current is None:
                     import torch
                     current = torch.cuda.current_device()
                 if dev != current:
-                    raise SvdqError(SVDQ_ERR_INVALID_ARG, f"{names[i]} is on {t.device}, not on the "
+                    raise SvdqError(SVDQ_ERR_INVALID_ARG, f"{name} is on {t.device}, not on the "
                                                           f"current device cuda:{current}")
             t = t.data_ptr()
         ptrs.append(t)
