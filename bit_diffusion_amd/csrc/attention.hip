@@ -69,6 +69,7 @@ struct Tile {
     int q0, len;       // the segment's first row of q and its positions,
     int k0, keys;      // its first key and its keys
     int row0;          // the tile's first packed row
+    int share;         // tiles of keys of a part that give every CU two, or 0 if not known
 };
 template <int CTRL, int ROWS = 0xf>
 __device__ __forceinline__ int max_dpp(int v) { return max(v, dpp<CTRL, ROWS>(v, v)); }
@@ -91,6 +92,15 @@ __device__ __forceinline__ int wave_scan(int v) {
     v += dpp<kBcast31, 0xc>(0, v);
     return v;
 }
+__device__ __forceinline__ float wave_sum(float v) {
+    v += dpp<kShr + 1>(0.f, v);
+    v += dpp<kShr + 2>(0.f, v);
+    v += dpp<kShr + 4>(0.f, v);
+    v += dpp<kShr + 8>(0.f, v);
+    v += dpp<kBcast15, 0xa>(0.f, v);
+    v += dpp<kBcast31, 0xc>(0.f, v);
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
 // Tile `want` of the segments' tiles of kRows rows (rep to a position).  Up to 64 segments: those
 // with the most keys first (by powers of two), so that no long tile starts when the others are done;
 // more: in order.  With a causal mask a segment's last rows first, which see the most.
@@ -111,6 +121,10 @@ __device__ __forceinline__ Tile find_tile(const AttentionArgs& a, int rep, int w
         const int keys = max(min(max(next[3], 0), Mk) - k0, 0);
         if (c + 64 < a.n) fetch(c + 64 + lane);
         const int nt = (len * rep + kRows - 1) / kRows;
+        // products of row and key tiles, dealt to two workgroups a CU
+        int share = 0;
+        if (a.splits > 1 && a.n <= 64)
+            share = (int)(wave_sum((float)nt * (float)((keys + kKeys - 1) / kKeys)) * ((float)a.G / (2 * kCus))) + 1;
         // a lane's turn: the number of its keys' bits, one turn for all of many segments; -1: no tile
         int turn = nt == 0 ? -1 : a.n > 64 ? 0 : 32 - __clz(keys);
         for (int now = a.n > 64 ? 0 : wave_max(turn); now >= 0; now = a.n > 64 ? -1 : wave_max(turn)) {
@@ -121,13 +135,13 @@ __device__ __forceinline__ Tile find_tile(const AttentionArgs& a, int rep, int w
                 const int off = want - __builtin_amdgcn_readlane(sum - mine, src);
                 const int tile = a.causal ? __builtin_amdgcn_readlane(nt, src) - 1 - off : off;
                 return Tile{c + src, __builtin_amdgcn_readlane(q0, src), __builtin_amdgcn_readlane(len, src),
-                            __builtin_amdgcn_readlane(k0, src), __builtin_amdgcn_readlane(keys, src), tile * kRows};
+                            __builtin_amdgcn_readlane(k0, src), __builtin_amdgcn_readlane(keys, src), tile * kRows, share};
             }
             want -= __builtin_amdgcn_readlane(sum, 63);
             if (turn == now) turn = -1;
         }
     }
-    return Tile{-1, 0, 0, 0, 0, 0};
+    return Tile{-1, 0, 0, 0, 0, 0, 0};
 }
 
 // The keys that packed row `row` of a segment sees: those below.
@@ -140,11 +154,6 @@ struct Limit {
         return causal ? min(max(max(prefix, row / rep + off + 1), 0), keys) : keys;
     }
 };
-
-// Tiles of keys that one of a row tile's workgroups takes, of `tiles` in all.
-__device__ __forceinline__ int part_tiles(const AttentionArgs& a, int tiles) {
-    return a.splits == 1 ? tiles : max(a.part, (tiles + a.splits - 1) / a.splits);
-}
 
 __device__ __forceinline__ f32x16 mfma32(bf16x8 x, bf16x8 y, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, c, 0, 0, 0);
@@ -423,6 +432,8 @@ __device__ __forceinline__ void step(Rows<NB, MOD>& w, int key0, uint32_t kb, ui
     }
 }
 
+constexpr float kDone = -1.f;   // in the place of a row's first sum: its result is written
+
 // Where a split's O, maximum and sum of row (position m, head h) stand in the workspace.
 __device__ __forceinline__ int64_t part_row(const AttentionArgs& a, int split, int64_t m, int h) {
     return ((int64_t)split * a.Mq + m) * a.H + h;
@@ -440,7 +451,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
     // the longest of all heads start first (1024 rows each over 77, 300, 0 and 128 keys, 16 heads: 16.0
     // -> 13.0 us); one segment's tiles are alike (4608 rows, 24 heads: 252 us, in step 254).
     const int xcd = blockIdx.x & 7;
-    int j = blockIdx.x >> 3, split, g, tile;
+    int j = blockIdx.x >> 3, split = 0, g, tile;
     if (a.n > 1 && a.G % 8 == 0) {
         const int heads = a.G / 8;
         split = j % a.splits;
@@ -460,8 +471,11 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
     const int klen = t.keys, rows = min(kRows, t.len * rep - t.row0);
     const Limit limit(a, t.seg, t.len, klen);
     // the workgroup's tiles: its part of those that its last row sees
-    const int tiles = (limit.of(t.row0 + rows - 1) + kKeys - 1) / kKeys, per = part_tiles(a, tiles);
+    const int tiles = (limit.of(t.row0 + rows - 1) + kKeys - 1) / kKeys;
+    const int per = max(max(a.part, t.share), (tiles + a.splits - 1) / a.splits);
     const int first = split * per, last = min(first + per, tiles);
+    const bool joined = per < tiles;             // else the first part has all keys and writes the result
+    if (split > 0 && !joined) return;
 
     // the lane's row, or the last one's again
     const bool active = wave * 32 < rows;
@@ -565,17 +579,19 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
         float* ml = (float*)a.work + all * D + at * 2;
         if (h == 0) {
             ml[0] = MOD == kPlain ? w.m * w.c0 : w.m;
-            ml[1] = w.l;
+            ml[1] = joined ? w.l : kDone;
         }
-        float* o = (float*)a.work + at * D;
+        if (joined && first < last) {
+            float* o = (float*)a.work + at * D;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const int ch = 32 * b + 2 * i + 4 * h;
-                if (ch < D) *(float4*)(o + ch) = make_float4(w.O[b][i], w.O[b][i + 1], w.O[b][i + 2], w.O[b][i + 3]);
-            }
-        return;
+                for (int i = 0; i < 16; i += 4) {
+                    const int ch = 32 * b + 2 * i + 4 * h;
+                    if (ch < D) *(float4*)(o + ch) = make_float4(w.O[b][i], w.O[b][i + 1], w.O[b][i + 2], w.O[b][i + 3]);
+                }
+        }
+        if (joined) return;
     }
     const float inv = w.l == 0.f ? 0.f : 1.f / w.l;   // a row that sees no key gives zeros
     uint16_t* op = (uint16_t*)a.out + (t.q0 + pos) * a.out_stride + (int64_t)head * D;
@@ -602,7 +618,8 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs 
     const float* o = (const float*)a.work + r * a.D;
     const float2* ml = (const float2*)((const float*)a.work + all * a.splits * a.D) + r;
     const float2 mine = lane < a.splits ? ml[all * lane] : make_float2(-INFINITY, 0.f);
-    const bool live = m >= a.q_start[0] && m < a.q_start[a.n];
+    const bool live = m >= a.q_start[0] && m < a.q_start[a.n] &&
+                      __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(mine.y))) != kDone;
     float top = mine.x;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) top = __builtin_elementwise_maximum(top, __shfl_xor(top, d, kWave));
@@ -645,20 +662,35 @@ int64_t max_tiles(int64_t Mq, int rep, int n) {
     return std::min(Mq * ((rep + kRows - 1) / kRows), (Mq * rep + (int64_t)n * (kRows - 1)) / kRows);
 }
 
-// The most parts of a row tile's keys, and the least tiles of a part: as many as give every CU a few
-// workgroups, none where there are two a CU without.  A part costs its rows' fp32 O to write and read
-// again, so tiles of few rows are cut finer (us: 32 rows, 2048 keys, 24 heads of 128, parts of 4 tiles
-// 13.1, of 8 16.2; 1024 rows and keys, 16 heads of 64, one part 15.6, two of 8 tiles 18.6; 8 single
-// rows over up to 8000 keys, 8 kv heads, three workgroups a CU at most 28.5, six 32).
+// The most parts of a row tile's keys, and the least tiles of a part.
 struct Split {
     int most, part;
 };
-Split split_of(int64_t Mq, int64_t Mk, int H, int G, int n) {
-    const int64_t tiles = max_tiles(Mq, H / G, n), items = tiles * G;
-    if (items == 0 || items >= 2 * kCus) return Split{1, 1};
-    const bool few = Mq * (H / G) <= tiles * 32;
-    const int64_t want = (few ? 3 : 2) * kCus / items, part = few ? 4 : 12;
-    return Split{(int)std::max<int64_t>(1, std::min({want, Mk / (part * kKeys), (int64_t)kWave})), (int)part};
+// Where row tiles leave CUs idle, as many parts as make the longest segment that there may be shortest:
+// a tile of keys takes a workgroup about 1.1 us, parts another launch and their rows' fp32 O written and
+// read once more.  What each part takes is settled on the GPU, where the lengths are known.  (us, one
+// part and several: 8 single rows over up to 8000 keys, 8 kv heads 82 and 26; one row over 8192 keys, 32
+// heads 32 and 13; 256 rows over 8192, 8 heads 140 and 26; 1300 causal rows of 4 heads 27.5 and 17.)
+Split split_of(int64_t Mq, int64_t Mk, int H, int G, int D, int n) {
+    const int64_t tiles = max_tiles(Mq, H / G, n), items = tiles * G, keys = (Mk + kKeys - 1) / kKeys;
+    if (items == 0 || items >= 2 * kCus || n == 0) return Split{1, 1};
+    const bool few = Mq * (H / G) <= tiles * 32;      // rows of a tile, on average
+    // of many rows a segment's share of the keys is known better than that
+    const int64_t longest = few ? keys : std::min(keys, (4 * keys + n - 1) / n);
+    const double part_us = (double)Mq * H * (D + 2) * 8 / 3e6;
+    double best = longest * 1.1;
+    int64_t parts = 1;
+    for (int64_t p = 2; p <= std::min({2 * kCus / items, (longest + 3) / 4, (int64_t)kWave}); ++p) {
+        const double us = (longest + p - 1) / p * 1.1 + 5 + p * part_us;
+        if (us < best) {
+            best = us;
+            parts = p;
+        }
+    }
+    if (parts == 1) return Split{1, 1};
+    const int64_t part = n > 1 && few ? 4 : std::max<int64_t>(4, (longest + parts - 1) / parts);
+    const int64_t most = std::min({(keys + part - 1) / part, std::max(parts, 3 * kCus / items), (int64_t)kWave});
+    return most <= 1 ? Split{1, 1} : Split{(int)most, (int)part};
 }
 
 template <int NB>
@@ -677,14 +709,14 @@ bool attention_fits(int64_t Mq, int H, int G, int n) {
 }
 
 int64_t attention_workspace_bytes(int64_t Mq, int64_t Mk, int H, int G, int D, int n) {
-    const int splits = split_of(Mq, Mk, H, G, n).most;
+    const int splits = split_of(Mq, Mk, H, G, D, n).most;
     return splits <= 1 ? 0 : splits * Mq * H * (D + 2) * 4;
 }
 
 void launch_attention(const AttentionArgs& in, hipStream_t st) {
     AttentionArgs a = in;
     a.tiles = (int)max_tiles(a.Mq, a.H / a.G, a.n);
-    const Split split = split_of(a.Mq, a.Mk, a.H, a.G, a.n);
+    const Split split = split_of(a.Mq, a.Mk, a.H, a.G, a.D, a.n);
     a.splits = split.most;
     a.part = split.part;
     if (a.D <= 32) launch<1>(a, st);

@@ -126,6 +126,10 @@ CASES = {
     "many rows, split, causal": dict(qs=cut(590, 10), ks=cut(2000, 900), H=8, G=8, D=72, causal=True, prefix=[100, 3], tail=5),
     "eight heads, several lengths": dict(qs=cut(140, 300, 20, 0, 10), ks=cut(500, 30, 0, 7, 129), H=16, G=8, D=64, cap=9.0),
     "sixteen heads in step": dict(qs=cut(140, 300), H=16, G=16, D=32),
+    "split, one long of many": dict(qs=list(range(9)), ks=cut(22, 11, 14, 529, 199, 14, 3630, 49), H=24, G=24, D=128, cap=50.0),
+    "split, short ones whole": dict(qs=cut(66, 315, 493, 20, 60, 91), H=2, G=2, D=80, cap=15.0, tail=13),
+    "split, causal": dict(qs=cut(1300), H=4, G=1, D=128, causal=True, tail=40),
+    "split, more segments than lanes": dict(qs=list(range(71)), ks=[60 * i if i < 70 else 60 * 69 + 3000 for i in range(71)], H=2, G=2, D=32),
     "many segments": dict(qs=sorted([0] + [i * 37 % 900 for i in range(150)] + [900]), H=2, G=1, D=64),
     "more heads than a tile's rows": dict(qs=cut(3, 1), ks=cut(90, 200), H=300, G=2, D=64, causal=True),
     "sharp": dict(qs=cut(500), H=2, G=2, D=128, sharp=60.0),

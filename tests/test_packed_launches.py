@@ -90,13 +90,16 @@ def test_every_kernel_is_launched_by_a_case(trace):
 
 
 def test_splits(trace):
-    """Few rows over many keys are split, and joined; two workgroups a CU without are not."""
-    _, launched, sizes = trace(["attn 1 600 1 1 64 1 0 0", "attn 1 400 1 1 64 1 0 0", "attn 512 100000 512 512 64 512 0 0",
-                                "attn 511 100000 1 1 64 511 0 0", "attn 4096 2000 8 8 64 1 0 0", "attn 1024 1535 4 4 64 1 0 0",
-                                "attn 1024 1536 4 4 64 1 0 0", "attn 1023 1536 4 4 64 1 0 0"])
-    assert [len(c) for c in launched] == [2, 1, 1, 1, 2, 1, 2, 2]
-    assert [b > 0 for _, b in sizes] == [len(c) == 2 for c in launched]
-    assert launched[6][1] == "attention_join_kernel<1>" and launched[7][1] == "attention_join_kernel<4>"
+    """Few rows over many keys are split, and joined, by four waves a row or one; short keys, and two
+    workgroups a CU without, are not."""
+    split = {"attn 1 512 1 1 64 1 0 0": 0, "attn 1 600 1 1 64 1 0 0": 4, "attn 512 100000 512 512 64 512 0 0": 0,
+             "attn 511 100000 1 1 64 511 0 0": 0, "attn 255 100000 1 1 64 255 0 0": 4,
+             "attn 4096 1500 8 8 64 1 0 0": 0, "attn 4096 9000 8 8 64 1 0 0": 1, "attn 1023 4000 4 4 64 1 0 0": 4,
+             "attn 1024 4000 4 4 64 1 0 0": 1, "attn 8 9000 8 8 128 8 0 0": 4, "attn 8 9000 64 64 128 8 0 0": 0}
+    _, launched, sizes = trace(list(split))
+    for c, ks, (_, b), per in zip(split, launched, sizes, split.values()):
+        assert (b > 0) == (per > 0) and len(ks) == 1 + (per > 0), (c, ks, b)
+        assert not per or ks[1] == f"attention_join_kernel<{per}>", (c, ks)
 
 
 def test_launch_choices_at_every_size(trace):
