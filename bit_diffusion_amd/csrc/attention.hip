@@ -38,8 +38,8 @@
 // must not meet a weight 0: they are multiplied as 0, and counted in a second product over who sees
 // them (poison below).
 //
-// Few rows: the keys of a tile are split over several workgroups, whose maxima, sums and O go to
-// the workspace and are joined by a second launch.
+// Few row tiles: the keys of each are split over several workgroups, whose maxima, sums and O go to the
+// workspace and are joined by a second launch.
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -450,19 +450,28 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
     // several segments, and kv heads in eights, an XCD goes through its heads' tiles in step, so that
     // the longest of all heads start first (1024 rows each over 77, 300, 0 and 128 keys, 16 heads: 16.0
     // -> 13.0 us); one segment's tiles are alike (4608 rows, 24 heads: 252 us, in step 254).
-    const int xcd = blockIdx.x & 7;
-    int j = blockIdx.x >> 3, split = 0, g, tile;
-    if (a.n > 1 && a.G % 8 == 0) {
-        const int heads = a.G / 8;
-        split = j % a.splits;
-        j /= a.splits;
-        tile = j / heads;
-        g = xcd * heads + j - tile * heads;
-    } else {
-        const int total = (int)gridDim.x, lo = total >> 3, more = total & 7;
+    // Parts of a tile are neighbours where there are few rows, else all first parts come before all second
+    // ones: those that a tile has no keys for end at once, and among the others every second place of a
+    // CU stayed empty (4 x 1024 rows of 4 heads with none cut in two: 55 us, so 28; 5 requests of 50 to 1400
+    // rows, 4 heads: 25.1 -> 22.1).
+    const int items = a.tiles * a.G;
+    int split = a.parts_last ? (int)blockIdx.x / items : 0, j = (int)blockIdx.x - split * items, g, tile;
+    const int xcd = j & 7;
+    j >>= 3;
+    const int runs = a.parts_last ? 1 : a.splits;
+    const bool in_step = a.n > 1 && a.G % 8 == 0;
+    if (!in_step) {
+        const int total = items * runs, lo = total >> 3, more = total & 7;
         j += xcd * lo + min(xcd, more);
-        split = j % a.splits;
-        j /= a.splits;
+    }
+    if (runs > 1) {
+        split = j % runs;
+        j /= runs;
+    }
+    if (in_step) {
+        tile = j / (a.G / 8);
+        g = (xcd - tile) * (a.G / 8) + j;
+    } else {
         g = j / a.tiles;
         tile = j - g * a.tiles;
     }
@@ -472,9 +481,16 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
     const Limit limit(a, t.seg, t.len, klen);
     // the workgroup's tiles: its part of those that its last row sees
     const int tiles = (limit.of(t.row0 + rows - 1) + kKeys - 1) / kKeys;
-    const int per = max(max(a.part, t.share), (tiles + a.splits - 1) / a.splits);
+    int per = tiles;
+    bool joined = false;         // else the first part has all keys and writes the result
+    if (a.splits > 1) {
+        const int least = max(max(a.part, t.share), (tiles + a.splits - 1) / a.splits);
+        const int parts = max((tiles + least - 1) / least, 1), alike = (tiles + parts - 1) / parts;
+        // where they save more than writing and reading them costs
+        joined = (float)(tiles - alike) > parts * a.part_tiles;
+        if (joined) per = alike;
+    }
     const int first = split * per, last = min(first + per, tiles);
-    const bool joined = per < tiles;             // else the first part has all keys and writes the result
     if (split > 0 && !joined) return;
 
     // the lane's row, or the last one's again
@@ -609,7 +625,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
 // Joins the parts of rows (position, head), PER waves a row: each takes every PER-th part in their
 // order, then the waves' sums are added in theirs.  Lane: part `lane`'s maximum and sum, and channels
 // 2 lane, 2 lane + 1.  Rows between the first offset and the last are the segments'.
-template <int PER>
+template <int PER>   // 1 or kWaves
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs a) {
     __shared__ float2 sums[kWaves][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -620,6 +636,7 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs 
     const float2 mine = lane < a.splits ? ml[all * lane] : make_float2(-INFINITY, 0.f);
     const bool live = m >= a.q_start[0] && m < a.q_start[a.n] &&
                       __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(mine.y))) != kDone;
+    if (!live) return;                     // all of a row's waves
     float top = mine.x;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) top = __builtin_elementwise_maximum(top, __shfl_xor(top, d, kWave));
@@ -627,7 +644,7 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs 
     float l = mine.y * f;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) l += __shfl_xor(l, d, kWave);
-    const int parts = live ? 64 - __clzll((long long)__ballot(!(f == 0.f))) : 0;   // those past hold nothing
+    const int parts = 64 - __clzll((long long)__ballot(!(f == 0.f)));   // those past hold nothing
     float2 sum = make_float2(0.f, 0.f);
     if (2 * lane < a.D) {
         for (int s = wave % PER; s < parts; s += 4 * PER) {   // four loads in flight
@@ -652,7 +669,7 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs 
             sum.y += sums[wave / PER * PER + w][lane].y;
         }
     }
-    if (!live || wave % PER > 0 || 2 * lane >= a.D) return;
+    if (wave % PER > 0 || 2 * lane >= a.D) return;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     *(uint32_t*)((uint16_t*)a.out + m * a.out_stride + head * a.D + 2 * lane) = pack_bf16(sum.x * inv, sum.y * inv);
 }
@@ -662,35 +679,41 @@ int64_t max_tiles(int64_t Mq, int rep, int n) {
     return std::min(Mq * ((rep + kRows - 1) / kRows), (Mq * rep + (int64_t)n * (kRows - 1)) / kRows);
 }
 
-// The most parts of a row tile's keys, and the least tiles of a part.
+// How a row tile's keys are cut: into `most` parts, of `part` key tiles or more.
 struct Split {
     int most, part;
+    float cost;   // of a part's O, in the time of a tile of keys
+    int last;     // parts_last
 };
-// Where row tiles leave CUs idle, as many parts as make the longest segment that there may be shortest:
-// a tile of keys takes a workgroup about 1.1 us, parts another launch and their rows' fp32 O written and
-// read once more.  What each part takes is settled on the GPU, where the lengths are known.  (us, one
-// part and several: 8 single rows over up to 8000 keys, 8 kv heads 82 and 26; one row over 8192 keys, 32
-// heads 32 and 13; 256 rows over 8192, 8 heads 140 and 26; 1300 causal rows of 4 heads 27.5 and 17.)
+// Where row tiles leave CUs idle, as many parts as make the longest segment that there may be shortest: a
+// tile of keys takes a workgroup about as long as below, parts another launch and their rows' fp32 O
+// written and read once more.  Which are cut, and how, is settled on the GPU, where the lengths are known.
+// Us, one part and several: 8 single rows over up to 8000 keys, 8 kv heads 167 and 29; one row over 8192
+// keys, 8 kv heads 133 and 13; 256 rows over 8192, 8 heads 143 and 26; 1300 causal rows of 4 heads 27.8
+// and 19.5; 2048 rows of 8 heads 40.3 and 35.5; 5 requests of 50 to 1400 rows, 4 heads 30.2 and 22.0; lost
+// where all are as long, which only the GPU knows: 4 x 512 rows of 4 heads 15.0 and 17.9.
 Split split_of(int64_t Mq, int64_t Mk, int H, int G, int D, int n) {
+    const Split whole{1, 1, 0.f, 0};
     const int64_t tiles = max_tiles(Mq, H / G, n), items = tiles * G, keys = (Mk + kKeys - 1) / kKeys;
-    if (items == 0 || items >= 2 * kCus || n == 0) return Split{1, 1};
+    if (items == 0 || items >= 2 * kCus || n == 0) return whole;
     const bool few = Mq * (H / G) <= tiles * 32;      // rows of a tile, on average
     // of many rows a segment's share of the keys is known better than that
     const int64_t longest = few ? keys : std::min(keys, (4 * keys + n - 1) / n);
+    const double tile_us = few ? 1.1 : 0.2 + 0.225 * ((D + 31) / 32), join_us = few ? 5 : 6;
     const double part_us = (double)Mq * H * (D + 2) * 8 / 3e6;
-    double best = longest * 1.1;
+    double best = longest * tile_us;
     int64_t parts = 1;
     for (int64_t p = 2; p <= std::min({2 * kCus / items, (longest + 3) / 4, (int64_t)kWave}); ++p) {
-        const double us = (longest + p - 1) / p * 1.1 + 5 + p * part_us;
+        const double us = (longest + p - 1) / p * tile_us + join_us + p * part_us;
         if (us < best) {
             best = us;
             parts = p;
         }
     }
-    if (parts == 1) return Split{1, 1};
+    if (parts == 1) return whole;
     const int64_t part = n > 1 && few ? 4 : std::max<int64_t>(4, (longest + parts - 1) / parts);
     const int64_t most = std::min({(keys + part - 1) / part, std::max(parts, 3 * kCus / items), (int64_t)kWave});
-    return most <= 1 ? Split{1, 1} : Split{(int)most, (int)part};
+    return most <= 1 ? whole : Split{(int)most, (int)part, (float)(part_us / tile_us), n > 1 && !few};
 }
 
 template <int NB>
@@ -719,6 +742,8 @@ void launch_attention(const AttentionArgs& in, hipStream_t st) {
     const Split split = split_of(a.Mq, a.Mk, a.H, a.G, a.D, a.n);
     a.splits = split.most;
     a.part = split.part;
+    a.part_tiles = split.cost;
+    a.parts_last = split.last;
     if (a.D <= 32) launch<1>(a, st);
     else if (a.D <= 64) launch<2>(a, st);
     else if (a.D <= 96) launch<3>(a, st);

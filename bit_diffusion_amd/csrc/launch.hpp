@@ -194,6 +194,8 @@ struct AttentionArgs {
     void* work;
     int tiles;               // the most row tiles (set by the launcher, as what follows)
     int splits, part;        // the most parts of a row tile's keys, and the least key tiles of one
+    int parts_last;          // all first parts in front of all second ones
+    float part_tiles;        // cost of writing and reading a part, in key tiles
 };
 
 // Largest workspace the K split of svdq_gemm_w4a4_packed uses (its split count is capped so

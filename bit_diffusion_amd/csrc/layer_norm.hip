@@ -14,7 +14,7 @@
 // change (as fp32 rows they are three times a bf16 row's bytes, which the caches would else have to
 // deliver with every row).  A row at a time, the next one's loads in flight, and several workgroups a
 // CU that wait at different barriers: four rows at a time, with one pair of barriers for all, held
-// four times the registers and took 85 us where this takes 29 (4608 x 3072 bf16 with residual).
+// four times the registers and took 85 us where this takes 27 (4608 x 3072 bf16 with residual).
 #include "common.hpp"
 #include "launch.hpp"
 #include "segments.hpp"
@@ -28,7 +28,8 @@ namespace {
 constexpr int kCus = 256;    // of the GPU
 constexpr int kWaves = 16;   // of the widest workgroup
 constexpr int kWavesCu = 18; // a CU's share of the rows goes over workgroups of so many waves in all (4608
-                             // rows of 6 waves: 28.7 us, with 12 waves 30.5, 24 29.4, 48 31.9)
+                             // rows of 6 waves: 26.9 us, with 12 waves 28.7, 24 27.4, 48 26.3; 1238 of 5
+                             // waves: 9.5, 10.9, 9.6, 8.6)
 
 // The sum over the wave, in every lane.
 __device__ __forceinline__ float wave_sum(float v) {
@@ -251,7 +252,7 @@ void launch(const LayerNormArgs& a, int threads, hipStream_t st) {
 
 void launch_layer_norm(const LayerNormArgs& a, hipStream_t st) {
     const int n = a.C / a.vec;   // column vectors of a row
-    // two vectors a thread up to 1024 (4608 rows of 768 vectors: 28.7 us, with one 40, with four 31),
+    // two vectors a thread up to 1024 (4608 rows of 768 vectors: 26.9 us, with one 40, with four 30),
     // then as many as leave a row's threads in a workgroup their registers
     const int V = n <= 64 ? 1 : n <= 1024 ? 2 : n <= 2048 ? 4 : 8;
     const int threads = ((n + V - 1) / V + 63) / 64 * 64;

@@ -27,8 +27,8 @@ constexpr int kCus = 256;    // of the GPU
 constexpr int kMaxPairs = 128;
 constexpr int kRows = 16;    // rows of a workgroup, at most
 // Heads that a group of lanes takes: so many pay for the angle table and its start (4608 rows of 48
-// heads of 128: 27.5 us, with 4 heads 32.4; 6001 rows of 20 heads of 96, fp32: 17.8, with one row a
-// workgroup, 1 head, 39).
+// heads of 128: 30.5 us, with 4 heads 36, with one 39; 6001 rows of 20 heads of 96, fp32: 16.6, 16.5 and
+// 24.3).
 constexpr int kPerGroup = 16;
 
 // cos and sin of `rows` rows' angles: table[row][pair].
