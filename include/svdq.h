@@ -524,8 +524,9 @@ svdq_status svdq_rotary(int64_t M, int32_t n_q_heads, int32_t n_k_heads, int32_t
  *   out[i, h] = sum_j exp(t_ij) v[j, h'] / sum_j exp(t_ij),
  *
  * d = keys of s - rows of s, which puts the last row at the last key.  A row that sees no key gives
- * zeros.  q, k and v are bf16; scores, the running maximum, sum and result are fp32, the weights
- * exp(t_ij - max) rounded to bf16 for their product with v.
+ * zeros.  q, k and v are bf16; scores, the sums and the result before its rounding are fp32, the
+ * weights rounded to bf16.  They are taken against a score that may be 16 powers of two below the
+ * largest (sums of |v| over a row's keys must stay 2^-16 below fp32's range).
  *   scale      finite and positive.  cap finite, 0: none.
  *   mask       svdq_mask: SVDQ_MASK_NONE all keys of the segment (rows of an image see one another);
  *              SVDQ_MASK_CAUSAL keys j <= i + d, and all j < prefix[s] (a prompt in front of it, or
@@ -542,8 +543,8 @@ svdq_status svdq_rotary(int64_t M, int32_t n_q_heads, int32_t n_k_heads, int32_t
  *              [Mkv, n_kv_heads head_dim] bf16: column ranges of wider matrices.  No input may
  *              overlap out.
  *   workspace  svdq_attention_workspace_bytes(Mq, Mkv, n_heads, n_kv_heads, head_dim, n_segments)
- *              bytes at least (0 unless the rows are few), 16-byte aligned, overwritten; calls that
- *              may overlap in time need one each.
+ *              bytes at least (0 where the rows keep the GPU busy without it), 16-byte aligned,
+ *              overwritten; calls that may overlap in time need one each.
  * What a row does not see does not change its result, infinities and NaN among it.  A NaN score
  * that a row sees makes the row NaN.
  * head_dim a multiple of 8 up to 128; n_heads a positive multiple of n_kv_heads; Mq up to 2^24 and
