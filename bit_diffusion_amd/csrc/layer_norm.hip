@@ -27,9 +27,11 @@ namespace {
 
 constexpr int kCus = 256;    // of the GPU
 constexpr int kWaves = 16;   // of the widest workgroup
-constexpr int kWavesCu = 18; // a CU's share of the rows goes over workgroups of so many waves in all (4608
-                             // rows of 6 waves: 26.9 us, with 12 waves 28.7, 24 27.4, 48 26.3; 1238 of 5
-                             // waves: 9.5, 10.9, 9.6, 8.6)
+// A CU's share of the rows goes over as many workgroups as read kFlight bytes at a time, up to kWavesCu waves
+// of them, three quarters of that where x is fp32 (us, waves 18, 24 and 30; bf16: 4096 x 1152 12.1, 11.5, 11.4;
+// 4608 x 3072 27.1, 27.5, 26.4; 9216 x 3072 52.7, 51.5, 53.5, without y 36.2, 32.6, 41.3; fp32 4608 x 3072 without
+// y 20.9, 25.0, 25.4).
+constexpr int kFlight = 57344, kWavesCu = 24;
 
 // The sum over the wave, in every lane.
 __device__ __forceinline__ float wave_sum(float v) {
@@ -237,8 +239,12 @@ __global__ __launch_bounds__(kThreads) void layer_norm_kernel(LayerNormArgs a, i
 
 template <int VEC, int V, int kThreads>
 void launch(const LayerNormArgs& a, int threads, hipStream_t st) {
-    const int64_t most = kCus * std::max(1, kWavesCu * 64 / threads);
-    const int per = (int)((a.M + most - 1) / most);
+    const int waves = threads / 64, row = a.C * ((a.x_bf16 ? 2 : 4) + (a.y == nullptr ? 0 : a.y_bf16 ? 2 : 4));
+    const int64_t most = kCus * std::max(1, std::min((kFlight + row / 2) / row, (a.x_bf16 ? kWavesCu : kWavesCu * 3 / 4) / waves));
+    // narrow rows have a workgroup each where the GPU holds them all (1238 x 1170, fp32 x: 9.7 -> 8.6 us; of 9 KB
+    // and more not: 1300 x 3072 11.4 -> 12.7; nor element by element: 1238 x 1171 10.0 -> 11.2)
+    const bool at_once = VEC > 1 && row <= 8192 && a.M * waves <= kCus * 32;
+    const int per = at_once ? 1 : (int)((a.M + most - 1) / most);
     const dim3 grid((unsigned)((a.M + per - 1) / per)), block(threads);
     auto go = [&](auto xb, auto yb, auto ob) {
         hipLaunchKernelGGL((layer_norm_kernel<VEC, V, kThreads, xb.value, yb.value, ob.value>), grid, block, 0, st, a, per);
