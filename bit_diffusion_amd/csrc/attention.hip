@@ -203,11 +203,12 @@ struct Lds {
     static __device__ __forceinline__ int v_slot(int r, int s) { return s ^ (kSlots == 16 ? (r & 3) << 2 : ((r >> 1) & 1) << 2); }
 };
 
-// One wave's rows.
-template <int NB, int MOD>
+// One wave's rows.  NC: steps of 16 channels that Q K^T has (D <= 16 NC, NC <= 8).
+template <int NC, int MOD>
 struct Rows {
+    static constexpr int NB = (NC + 1) / 2;
     f32x16 O[NB];      // O^T: lane (h, row) has channels 32 b + 8 (i / 4) + 4 h + i % 4
-    bf16x8 Q[2 * NB];  // channels 16 c + 8 h to + 7 of the lane's row
+    bf16x8 Q[NC];      // channels 16 c + 8 h to + 7 of the lane's row
     float m, l;        // maximum of the row's scores (MOD = kPlain: unscaled; else times log2 e), this half's sum
     int limit;         // keys that the row sees
     int at;            // the key at distance 0
@@ -261,22 +262,23 @@ __device__ __forceinline__ uint4 v_operand(uint32_t vbase, int b, int kc) {
 }
 
 // A tile of 64 keys from key0 on: kb, vb the lane's read addresses in this tile's buffers.
-template <int NB, int MOD, bool MASK>
-__device__ __forceinline__ void step(Rows<NB, MOD>& w, int key0, uint32_t kb, uint32_t vb) {
+template <int NC, int MOD, bool MASK>
+__device__ __forceinline__ void step(Rows<NC, MOD>& w, int key0, uint32_t kb, uint32_t vb) {
+    constexpr int NB = Rows<NC, MOD>::NB;
     using L = Lds<NB>;
     const int lane = threadIdx.x & 63, h = lane >> 5;
     f32x16 s[2];
     __builtin_amdgcn_s_setprio(1);   // the other wave's weights wait for these products, not these for them
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        bf16x8 k[2 * NB];
+        bf16x8 k[NC];
 #pragma unroll
-        for (int c = 0; c < 2 * NB; ++c)
+        for (int c = 0; c < NC; ++c)
             k[c] = *(lds_bf16x8*)(lds_u8*)(uintptr_t)((kb ^ (uint32_t)(c * 32)) + u * 32 * L::kRow);
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[u][i] = 0.f;
 #pragma unroll
-        for (int c = 0; c < 2 * NB; ++c) s[u] = mfma32(k[c], w.Q[c], s[u]);
+        for (int c = 0; c < NC; ++c) s[u] = mfma32(k[c], w.Q[c], s[u]);
     }
     // the first half of V is on its way while the weights are formed
     uint4 v[2][NB];
@@ -439,8 +441,9 @@ __device__ __forceinline__ int64_t part_row(const AttentionArgs& a, int split, i
     return ((int64_t)split * a.Mq + m) * a.H + h;
 }
 
-template <int NB, int MOD>
+template <int NC, int MOD>
 __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a) {
+    constexpr int NB = Rows<NC, MOD>::NB;
     using L = Lds<NB>;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * L::kTile];   // K, V, K, V
     const int lane = threadIdx.x & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -497,7 +500,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
     const bool active = wave * 32 < rows;
     const int row = t.row0 + min(wave * 32 + (lane & 31), rows - 1);
     const int pos = row / rep, head = g * rep + row - pos * rep;
-    Rows<NB, MOD> w;
+    Rows<NC, MOD> w;
     w.m = -INFINITY;
     w.l = 0.f;
     w.limit = limit.of(row);
@@ -509,7 +512,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
     if ((MOD & kCap) != 0) w.c0 *= 2.f / a.cap;
     const uint16_t* qp = (const uint16_t*)a.q + (t.q0 + pos) * a.q_stride + (int64_t)head * D;
 #pragma unroll
-    for (int c = 0; c < 2 * NB; ++c) {
+    for (int c = 0; c < NC; ++c) {
         const int ch = 16 * c + 8 * h;
         w.Q[c] = as_bf16x8(ch < D ? *(const uint4*)(qp + ch) : make_uint4(0u, 0u, 0u, 0u));
     }
@@ -578,14 +581,14 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
         wait_copies();
         barrier();   // this tile is there, and the other buffer has been read
         if (tile + 1 < last) copy_tile(tile + 1, (tile + 1 - first) & 1);
-        if (active) step<NB, MOD, false>(w, tile * kKeys, at + kr, at + vr);
+        if (active) step<NC, MOD, false>(w, tile * kKeys, at + kr, at + vr);
         at = smem0 + (((tile + 1 - first) & 1) * 2) * L::kTile;
     }
     for (int tile = whole; tile < last; ++tile) {
         wait_copies();
         barrier();
         if (tile + 1 < last) copy_tile(tile + 1, (tile + 1 - first) & 1);
-        if (tile * kKeys < most) step<NB, MOD, true>(w, tile * kKeys, at + kr, at + vr);
+        if (tile * kKeys < most) step<NC, MOD, true>(w, tile * kKeys, at + kr, at + vr);
         at = smem0 + (((tile + 1 - first) & 1) * 2) * L::kTile;
     }
     if (!active || wave * 32 + (lane & 31) >= rows) return;
@@ -716,13 +719,13 @@ Split split_of(int64_t Mq, int64_t Mk, int H, int G, int D, int n) {
     return most <= 1 ? whole : Split{(int)most, (int)part, (float)(part_us / tile_us), n > 1 && !few};
 }
 
-template <int NB>
+template <int NC>
 void launch(const AttentionArgs& a, hipStream_t st) {
     const dim3 grid((unsigned)(a.tiles * (int64_t)a.G * a.splits)), block(kThreads);
-    if (a.cap != 0.f && a.slopes != nullptr) hipLaunchKernelGGL((attention_kernel<NB, kBoth>), grid, block, 0, st, a);
-    else if (a.cap != 0.f) hipLaunchKernelGGL((attention_kernel<NB, kCap>), grid, block, 0, st, a);
-    else if (a.slopes != nullptr) hipLaunchKernelGGL((attention_kernel<NB, kBias>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((attention_kernel<NB, kPlain>), grid, block, 0, st, a);
+    if (a.cap != 0.f && a.slopes != nullptr) hipLaunchKernelGGL((attention_kernel<NC, kBoth>), grid, block, 0, st, a);
+    else if (a.cap != 0.f) hipLaunchKernelGGL((attention_kernel<NC, kCap>), grid, block, 0, st, a);
+    else if (a.slopes != nullptr) hipLaunchKernelGGL((attention_kernel<NC, kBias>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((attention_kernel<NC, kPlain>), grid, block, 0, st, a);
 }
 
 }  // namespace
@@ -744,10 +747,16 @@ void launch_attention(const AttentionArgs& in, hipStream_t st) {
     a.part = split.part;
     a.part_tiles = split.cost;
     a.parts_last = split.last;
-    if (a.D <= 32) launch<1>(a, st);
-    else if (a.D <= 64) launch<2>(a, st);
-    else if (a.D <= 96) launch<3>(a, st);
-    else launch<4>(a, st);
+    // no step of Q K^T without channels (16 heads of 72, 6 requests, 4916 rows: 66 us with six steps, with five 63)
+    switch (std::max(2, (a.D + 15) / 16)) {
+        case 2: launch<2>(a, st); break;
+        case 3: launch<3>(a, st); break;
+        case 4: launch<4>(a, st); break;
+        case 5: launch<5>(a, st); break;
+        case 6: launch<6>(a, st); break;
+        case 7: launch<7>(a, st); break;
+        default: launch<8>(a, st); break;
+    }
     if (a.splits > 1) {
         // a row's waves read their parts side by side; with many rows there are waves enough (2048 rows of
         // 8 heads, 2 parts: the call 33.6 us, with four waves a row 42)

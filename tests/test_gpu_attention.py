@@ -143,6 +143,11 @@ CASES = {
 }
 
 
+# every number of 16-channel steps, each with and without a cap and a bias
+CASES.update({f"width {D}, cap {cap}, bias {bias}": dict(qs=cut(130, 20), ks=cut(200, 70), H=2, G=1, D=D, cap=cap, bias=bias)
+              for D in (16, 32, 40, 48, 64, 72, 80, 96, 104, 112, 128) for cap in (0.0, 6.0) for bias in (False, True)})
+
+
 @pytest.mark.parametrize("name", list(CASES))
 def test_matches_fp64(name):
     print("attention", name, flush=True)
