@@ -28,6 +28,9 @@
 // heads of 128).  With a bias by distance scores grow from tile to tile as a rule, and the largest is
 // sought in each; O is rescaled only where it grew by more than 2^8.
 //
+// Few rows and keys: a wave's time is a tile's latency, so two waves share rows, each takes every other
+// tile of keys (SHARE), and their maxima, sums and O meet in LDS.
+//
 // LDS.  K and V tiles, rows of 64 or 128 channels, twice each: the next tile's copies (LDS DMA,
 // 16 bytes a lane) fly while this one is multiplied, one barrier a tile.  The 16-byte slots of a
 // row are exclusive-ored with the row (K: for 16 rows of one channel slot; V: for 4 rows of 32
@@ -50,7 +53,7 @@ namespace svdq {
 namespace {
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
-constexpr int kRows = 32 * kWaves;   // rows of a workgroup
+constexpr int kRows = 32 * kWaves;   // rows of a workgroup, or half as many where two waves share them
 constexpr int kKeys = 64;            // keys of a tile
 constexpr int kCus = 256;            // of the GPU
 constexpr float kLog2e = 1.4426950408889634f;
@@ -101,9 +104,10 @@ __device__ __forceinline__ float wave_sum(float v) {
     v += dpp<kBcast31, 0xc>(0.f, v);
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
-// Tile `want` of the segments' tiles of kRows rows (rep to a position).  Up to 64 segments: those
+// Tile `want` of the segments' tiles of ROWS rows (rep to a position).  Up to 64 segments: those
 // with the most keys first (by powers of two), so that no long tile starts when the others are done;
 // more: in order.  With a causal mask a segment's last rows first, which see the most.
+template <int ROWS>
 __device__ __forceinline__ Tile find_tile(const AttentionArgs& a, int rep, int want) {
     const int lane = threadIdx.x & 63, M = (int)a.Mq, Mk = (int)a.Mk;
     int next[4];
@@ -120,7 +124,7 @@ __device__ __forceinline__ Tile find_tile(const AttentionArgs& a, int rep, int w
         const int len = c + lane < a.n ? max(min(max(next[1], 0), M) - q0, 0) : 0;
         const int keys = max(min(max(next[3], 0), Mk) - k0, 0);
         if (c + 64 < a.n) fetch(c + 64 + lane);
-        const int nt = (len * rep + kRows - 1) / kRows;
+        const int nt = (len * rep + ROWS - 1) / ROWS;
         // products of row and key tiles, dealt to two workgroups a CU
         int share = 0;
         if (a.splits > 1 && a.n <= 64)
@@ -135,7 +139,7 @@ __device__ __forceinline__ Tile find_tile(const AttentionArgs& a, int rep, int w
                 const int off = want - __builtin_amdgcn_readlane(sum - mine, src);
                 const int tile = a.causal ? __builtin_amdgcn_readlane(nt, src) - 1 - off : off;
                 return Tile{c + src, __builtin_amdgcn_readlane(q0, src), __builtin_amdgcn_readlane(len, src),
-                            __builtin_amdgcn_readlane(k0, src), __builtin_amdgcn_readlane(keys, src), tile * kRows, share};
+                            __builtin_amdgcn_readlane(k0, src), __builtin_amdgcn_readlane(keys, src), tile * ROWS, share};
             }
             want -= __builtin_amdgcn_readlane(sum, 63);
             if (turn == now) turn = -1;
@@ -441,11 +445,13 @@ __device__ __forceinline__ int64_t part_row(const AttentionArgs& a, int split, i
     return ((int64_t)split * a.Mq + m) * a.H + h;
 }
 
-template <int NC, int MOD>
-__global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a) {
-    constexpr int NB = Rows<NC, MOD>::NB;
+// SHARE: waves that share rows, each taking every SHARE-th tile of keys.
+template <int NC, int MOD, int SHARE>
+__global__ __launch_bounds__(kThreads, 2 / SHARE) void attention_kernel(AttentionArgs a) {
+    constexpr int NB = Rows<NC, MOD>::NB, ROWS = kRows / SHARE;
     using L = Lds<NB>;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * L::kTile];   // K, V, K, V
+    constexpr int kBuf = SHARE * 2 * L::kTile;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kBuf];   // K, V of a tile, and of the next
     const int lane = threadIdx.x & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rep = a.H / a.G, D = a.D;
 
@@ -478,9 +484,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
         g = j / a.tiles;
         tile = j - g * a.tiles;
     }
-    const Tile t = find_tile(a, rep, tile);
+    const Tile t = find_tile<ROWS>(a, rep, tile);
     if (t.seg < 0) return;
-    const int klen = t.keys, rows = min(kRows, t.len * rep - t.row0);
+    const int klen = t.keys, rows = min(ROWS, t.len * rep - t.row0);
     const Limit limit(a, t.seg, t.len, klen);
     // the workgroup's tiles: its part of those that its last row sees
     const int tiles = (limit.of(t.row0 + rows - 1) + kKeys - 1) / kKeys;
@@ -497,8 +503,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
     if (split > 0 && !joined) return;
 
     // the lane's row, or the last one's again
-    const bool active = wave * 32 < rows;
-    const int row = t.row0 + min(wave * 32 + (lane & 31), rows - 1);
+    const int mine = wave / SHARE * 32, turn = wave % SHARE;   // the wave's first row in the tile, its first tile of keys
+    const bool active = mine < rows;
+    const int row = t.row0 + min(mine + (lane & 31), rows - 1);
     const int pos = row / rep, head = g * rep + row - pos * rep;
     Rows<NC, MOD> w;
     w.m = -INFINITY;
@@ -523,7 +530,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
 
     // of them those that all its rows see whole; and the keys that the wave's last row sees
     const int whole = min(max(limit.of(t.row0) / kKeys, first), last);
-    const int most = active ? limit.of(t.row0 + min(wave * 32 + 31, rows - 1)) : 0;
+    const int most = active ? limit.of(t.row0 + min(mine + 31, rows - 1)) : 0;
 
     // copies: an instruction fills 1 KB, kLanes lanes a row, kStep rows
     constexpr int kLanes = L::kSlots, kStep = 64 / kLanes;
@@ -548,7 +555,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
     static_assert(kStep % 4 == 0, "v_slot goes by the row modulo 4");
     auto copy_tile = [&](int tile, int buf) {
         const uint64_t kt = uniform_ptr(kp + (int64_t)tile * kKeys * kbytes), vt = uniform_ptr(vp + (int64_t)tile * kKeys * vbytes);
-        const uint32_t to = lds0 + buf * 2 * L::kTile;
+        const uint32_t to = lds0 + buf;
         const int past = tile * kKeys + kKeys - klen;        // keys past the segment's: its last again
         if (past <= 0) {
 #pragma unroll
@@ -567,7 +574,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
     };
     // channels past D: zeros, which no copy overwrites
     if (D < L::kRow / 2) {
-        for (int i = threadIdx.x; i < 4 * L::kTile / 16; i += kThreads) *(uint4*)(smem + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = threadIdx.x; i < 2 * kBuf / 16; i += kThreads) *(uint4*)(smem + i * 16) = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
     }
     // the lane's reads of K (row lane % 32, slot h of every 2) and of V (4 lanes to a row of 16 channels)
@@ -575,23 +582,55 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
     const int vrow = 4 * h + ((lane >> 2) & 3);
     const uint32_t vr = vrow * L::kRow + L::v_slot(vrow, ((lane >> 4) & 1) * 2 + ((lane >> 1) & 1)) * 16 + (lane & 1) * 8 + L::kTile;
 
-    if (first < last) copy_tile(first, 0);
-    uint32_t at = smem0;
-    for (int tile = first; tile < whole; ++tile) {
+    // tiles tile to tile + SHARE - 1 to buffer `buf`
+    auto copy_tiles = [&](int tile, int buf) {
+#pragma unroll
+        for (int i = 0; i < SHARE; ++i)
+            if (tile + i < last) copy_tile(tile + i, (buf * SHARE + i) * 2 * L::kTile);
+    };
+    copy_tiles(first, 0);
+    const uint32_t own = turn * 2 * L::kTile;
+    uint32_t at = smem0 + own;
+    int now = first, buf = 1;
+    for (; now + SHARE <= whole; now += SHARE, buf ^= 1) {
         wait_copies();
-        barrier();   // this tile is there, and the other buffer has been read
-        if (tile + 1 < last) copy_tile(tile + 1, (tile + 1 - first) & 1);
-        if (active) step<NC, MOD, false>(w, tile * kKeys, at + kr, at + vr);
-        at = smem0 + (((tile + 1 - first) & 1) * 2) * L::kTile;
+        barrier();   // these tiles are there, and the other buffer has been read
+        copy_tiles(now + SHARE, buf);
+        if (active) step<NC, MOD, false>(w, (now + turn) * kKeys, at + kr, at + vr);
+        at = smem0 + own + buf * kBuf;
     }
-    for (int tile = whole; tile < last; ++tile) {
+    for (; now < last; now += SHARE, buf ^= 1) {
         wait_copies();
         barrier();
-        if (tile + 1 < last) copy_tile(tile + 1, (tile + 1 - first) & 1);
-        if (tile * kKeys < most) step<NC, MOD, true>(w, tile * kKeys, at + kr, at + vr);
-        at = smem0 + (((tile + 1 - first) & 1) * 2) * L::kTile;
+        copy_tiles(now + SHARE, buf);
+        if (now + turn < last && (now + turn) * kKeys < most) step<NC, MOD, true>(w, (now + turn) * kKeys, at + kr, at + vr);
+        at = smem0 + own + buf * kBuf;
     }
-    if (!active || wave * 32 + (lane & 31) >= rows) return;
+    if constexpr (SHARE > 1) {
+        // the second wave's maximum, sum and O through LDS, as it holds them
+        float* there = (float*)smem + wave / SHARE * (NB * 16 + 2) * kWave + lane;
+        __syncthreads();
+        if (turn == 1) {
+            there[0] = w.m;
+            there[kWave] = w.l;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) there[(2 + b * 16 + i) * kWave] = w.O[b][i];
+        }
+        __syncthreads();
+        if (turn == 1) return;
+        const float unit = MOD == kPlain ? w.c0 : 1.f, other = there[0], top = __builtin_elementwise_maximum(w.m, other);
+        const float f0 = w.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((w.m - top) * unit);
+        const float f1 = other == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((other - top) * unit);
+        w.m = top;
+        w.l = fmaf(there[kWave], f1, w.l * f0);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w.O[b][i] = fmaf(there[(2 + b * 16 + i) * kWave], f1, w.O[b][i] * f0);
+    }
+    if (!active || mine + (lane & 31) >= rows) return;
     w.l = both_sum(w.l);
     if (a.splits > 1) {
         const int64_t at = part_row(a, split, t.q0 + pos, head), all = (int64_t)a.splits * a.Mq * a.H;
@@ -678,8 +717,8 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs 
 }
 
 // The most tiles that any cut of Mq positions into n segments can need.
-int64_t max_tiles(int64_t Mq, int rep, int n) {
-    return std::min(Mq * ((rep + kRows - 1) / kRows), (Mq * rep + (int64_t)n * (kRows - 1)) / kRows);
+int64_t max_tiles(int64_t Mq, int rep, int n, int rows = kRows) {
+    return std::min(Mq * ((rep + rows - 1) / rows), (Mq * rep + (int64_t)n * (rows - 1)) / rows);
 }
 
 // How a row tile's keys are cut: into `most` parts, of `part` key tiles or more.
@@ -704,9 +743,11 @@ Split split_of(int64_t Mq, int64_t Mk, int H, int G, int D, int n) {
     const int64_t longest = few ? keys : std::min(keys, (4 * keys + n - 1) / n);
     const double tile_us = few ? 1.1 : 0.2 + 0.225 * ((D + 31) / 32), join_us = few ? 5 : 6;
     const double part_us = (double)Mq * H * (D + 2) * 8 / 3e6;
-    double best = longest * tile_us;
+    const bool shared = max_tiles(Mq, H / G, n, kRows / 2) * G <= kCus;    // two waves to a row (launch_attention)
+    double best = (shared ? (longest + 1) / 2 : longest) * tile_us;
     int64_t parts = 1;
-    for (int64_t p = 2; p <= std::min({2 * kCus / items, (longest + 3) / 4, (int64_t)kWave}); ++p) {
+    const int64_t places = few && n > 1 ? 3 * kCus : 2 * kCus;   // short segments leave theirs to the longest
+    for (int64_t p = 2; p <= std::min({places / items, (longest + 3) / 4, (int64_t)kWave}); ++p) {
         const double us = (longest + p - 1) / p * tile_us + join_us + p * part_us;
         if (us < best) {
             best = us;
@@ -719,13 +760,13 @@ Split split_of(int64_t Mq, int64_t Mk, int H, int G, int D, int n) {
     return most <= 1 ? whole : Split{(int)most, (int)part, (float)(part_us / tile_us), n > 1 && !few};
 }
 
-template <int NC>
+template <int NC, int SHARE>
 void launch(const AttentionArgs& a, hipStream_t st) {
     const dim3 grid((unsigned)(a.tiles * (int64_t)a.G * a.splits)), block(kThreads);
-    if (a.cap != 0.f && a.slopes != nullptr) hipLaunchKernelGGL((attention_kernel<NC, kBoth>), grid, block, 0, st, a);
-    else if (a.cap != 0.f) hipLaunchKernelGGL((attention_kernel<NC, kCap>), grid, block, 0, st, a);
-    else if (a.slopes != nullptr) hipLaunchKernelGGL((attention_kernel<NC, kBias>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((attention_kernel<NC, kPlain>), grid, block, 0, st, a);
+    if (a.cap != 0.f && a.slopes != nullptr) hipLaunchKernelGGL((attention_kernel<NC, kBoth, SHARE>), grid, block, 0, st, a);
+    else if (a.cap != 0.f) hipLaunchKernelGGL((attention_kernel<NC, kCap, SHARE>), grid, block, 0, st, a);
+    else if (a.slopes != nullptr) hipLaunchKernelGGL((attention_kernel<NC, kBias, SHARE>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((attention_kernel<NC, kPlain, SHARE>), grid, block, 0, st, a);
 }
 
 }  // namespace
@@ -747,15 +788,27 @@ void launch_attention(const AttentionArgs& in, hipStream_t st) {
     a.part = split.part;
     a.part_tiles = split.cost;
     a.parts_last = split.last;
+    // two waves to 32 rows, each with every other tile of keys, where every CU has a workgroup at most also
+    // then (us, before and so: 662 rows of 8 heads of 128 18.6 and 14.4; 1024 rows of 4 heads of 64 15.4 and 10.9;
+    // 500 and 200 causal rows of 4 heads over 2 14.8 and 11.7)
+    const int64_t halves = max_tiles(a.Mq, a.H / a.G, a.n, kRows / 2);
+    if (a.splits == 1 && halves * a.G <= kCus) {
+        a.tiles = (int)halves;
+        if (a.D <= 32) launch<2, 2>(a, st);
+        else if (a.D <= 64) launch<4, 2>(a, st);
+        else if (a.D <= 96) launch<6, 2>(a, st);
+        else launch<8, 2>(a, st);
+        return;
+    }
     // no step of Q K^T without channels (16 heads of 72, 6 requests, 4916 rows: 66 us with six steps, with five 63)
     switch (std::max(2, (a.D + 15) / 16)) {
-        case 2: launch<2>(a, st); break;
-        case 3: launch<3>(a, st); break;
-        case 4: launch<4>(a, st); break;
-        case 5: launch<5>(a, st); break;
-        case 6: launch<6>(a, st); break;
-        case 7: launch<7>(a, st); break;
-        default: launch<8>(a, st); break;
+        case 2: launch<2, 1>(a, st); break;
+        case 3: launch<3, 1>(a, st); break;
+        case 4: launch<4, 1>(a, st); break;
+        case 5: launch<5, 1>(a, st); break;
+        case 6: launch<6, 1>(a, st); break;
+        case 7: launch<7, 1>(a, st); break;
+        default: launch<8, 1>(a, st); break;
     }
     if (a.splits > 1) {
         // a row's waves read their parts side by side; with many rows there are waves enough (2048 rows of

@@ -143,9 +143,11 @@ CASES = {
 }
 
 
-# every number of 16-channel steps, each with and without a cap and a bias
-CASES.update({f"width {D}, cap {cap}, bias {bias}": dict(qs=cut(130, 20), ks=cut(200, 70), H=2, G=1, D=D, cap=cap, bias=bias)
-              for D in (16, 32, 40, 48, 64, 72, 80, 96, 104, 112, 128) for cap in (0.0, 6.0) for bias in (False, True)})
+# every number of 16-channel steps, each with and without a cap and a bias, for few heads (two waves share
+# rows) and for many
+CASES.update({f"width {D}, cap {cap}, bias {bias}, {G} kv heads": dict(qs=cut(130, 20), ks=cut(200, 70), H=H, G=G, D=D, cap=cap, bias=bias)
+              for D in (16, 32, 40, 48, 64, 72, 80, 96, 104, 112, 128) for cap in (0.0, 6.0) for bias in (False, True)
+              for H, G in ((2, 1), (80, 80))})
 
 
 @pytest.mark.parametrize("name", list(CASES))
@@ -188,9 +190,10 @@ def test_every_key_counts_once(qlen, klen, H, G, D, causal):
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("causal", [False, True])
-def test_what_is_not_seen_does_not_count(bad, causal):
+@pytest.mark.parametrize("G", [2, 80])
+def test_what_is_not_seen_does_not_count(bad, causal, G):
     """Rows of k and v of other segments, behind the last and, with a causal mask, of later positions."""
-    c, ref = (Case(6, cut(70, 90, 133), 4, 2, 72, causal=causal, prefix=[0, 3, 0] if causal else None, tail=40) for _ in range(2))
+    c, ref = (Case(6, cut(70, 90, 133), 2 * G, G, 72, causal=causal, prefix=[0, 3, 0] if causal else None, tail=40) for _ in range(2))
     ref.call()
     hit = torch.zeros(c.Mq, dtype=torch.bool, device=DEV)     # rows that see a bad key
     rows = {20: 70, 100: 160, 165: 293, 292: 293}             # bad row -> end of its segment
@@ -208,9 +211,10 @@ def test_what_is_not_seen_does_not_count(bad, causal):
 
 
 @pytest.mark.parametrize("kw", [dict(), dict(cap=9.0), dict(bias=True), dict(causal=True), dict(causal=True, bias=True, cap=5.0)])
-def test_rows_do_not_depend_on_the_rows_beside_them(kw):
+@pytest.mark.parametrize("G", [2, 80])
+def test_rows_do_not_depend_on_the_rows_beside_them(kw, G):
     """The same bits whether the other rows of a segment hold numbers, huge ones or none."""
-    c = Case(12, cut(150, 90), 4, 2, 64, **kw)
+    c = Case(12, cut(150, 90), 2 * G, G, 64, **kw)
     c.call()
     torch.cuda.synchronize()
     ref = c.out.clone()
@@ -223,10 +227,11 @@ def test_rows_do_not_depend_on_the_rows_beside_them(kw):
 
 
 @pytest.mark.parametrize("D", [32, 64, 96, 128])
-def test_infinite_values_where_seen(D):
+@pytest.mark.parametrize("G", [1, 80])
+def test_infinite_values_where_seen(D, G):
     """An infinity of v gives its sign to the rows that see it, both signs or a NaN give NaN, in the
     columns that hold them and nowhere else."""
-    c, ref = (Case(8, cut(100), 2, 1, D, causal=True) for _ in range(2))
+    c, ref = (Case(8, cut(100), 2 * G, G, D, causal=True) for _ in range(2))
     ref.call()
     c.v[50, 3], c.v[60, 4], c.v[70, 5] = float("inf"), -float("inf"), float("nan")
     c.v[52, 7], c.v[80, 7] = float("inf"), -float("inf")
@@ -254,6 +259,7 @@ def test_scores_that_are_infinite():
 
 
 @pytest.mark.parametrize("kw", [dict(qs=cut(90, 60, 31), H=4, G=2, D=72, causal=True, prefix=[9, 0, 31]),
+                                dict(qs=cut(90, 60, 31), H=160, G=80, D=72, causal=True, prefix=[9, 0, 31]),
                                 dict(qs=[0, 1, 2, 3], ks=cut(2000, 100, 900), H=4, G=2, D=128)])
 def test_graph_replays_with_other_offsets(kw):
     c = Case(10, **kw)

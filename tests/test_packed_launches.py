@@ -92,7 +92,7 @@ def test_every_kernel_is_launched_by_a_case(trace):
 def test_splits(trace):
     """Few rows over many keys are split, and joined, by four waves a row or one; short keys, and two
     workgroups a CU without, are not."""
-    split = {"attn 1 512 1 1 64 1 0 0": 0, "attn 1 600 1 1 64 1 0 0": 4, "attn 512 100000 512 512 64 512 0 0": 0,
+    split = {"attn 1 1024 1 1 64 1 0 0": 0, "attn 1 1025 1 1 64 1 0 0": 4, "attn 512 100000 512 512 64 512 0 0": 0,
              "attn 511 100000 1 1 64 511 0 0": 0, "attn 255 100000 1 1 64 255 0 0": 4,
              "attn 4096 1500 8 8 64 1 0 0": 0, "attn 4096 9000 8 8 64 1 0 0": 1, "attn 1023 4000 4 4 64 1 0 0": 4,
              "attn 1024 4000 4 4 64 1 0 0": 1, "attn 8 9000 8 8 128 8 0 0": 4, "attn 8 9000 64 64 128 8 0 0": 0}
