@@ -731,9 +731,8 @@ struct Split {
 // tile of keys takes a workgroup about as long as below, parts another launch and their rows' fp32 O
 // written and read once more.  Which are cut, and how, is settled on the GPU, where the lengths are known.
 // Us, one part and several: 8 single rows over up to 8000 keys, 8 kv heads 167 and 29; one row over 8192
-// keys, 8 kv heads 133 and 13; 256 rows over 8192, 8 heads 143 and 26; 1300 causal rows of 4 heads 27.8
-// and 19.5; 2048 rows of 8 heads 40.3 and 35.5; 5 requests of 50 to 1400 rows, 4 heads 30.2 and 22.0; lost
-// where all are as long, which only the GPU knows: 4 x 512 rows of 4 heads 15.0 and 17.9.
+// keys, 8 kv heads 133 and 13; 256 rows over 8192, 8 heads 143 and 26; 5 requests of 50 to 1400 rows, 4 heads
+// 30.2 and 22.0; lost where all are as long, which only the GPU knows: 4 x 1024 rows of 4 heads 23.7 and 27.8.
 Split split_of(int64_t Mq, int64_t Mk, int H, int G, int D, int n) {
     const Split whole{1, 1, 0.f, 0};
     const int64_t tiles = max_tiles(Mq, H / G, n), items = tiles * G, keys = (Mk + kKeys - 1) / kKeys;
@@ -790,7 +789,7 @@ void launch_attention(const AttentionArgs& in, hipStream_t st) {
     a.parts_last = split.last;
     // two waves to 32 rows, each with every other tile of keys, where every CU has a workgroup at most also
     // then (us, before and so: 662 rows of 8 heads of 128 18.6 and 14.4; 1024 rows of 4 heads of 64 15.4 and 10.9;
-    // 500 and 200 causal rows of 4 heads over 2 14.8 and 11.7)
+    // 500 and 200 causal rows of 4 heads over 2 14.8 and 11.7; 1500 rows of 4 heads of 128, in parts 20.8, 23.1)
     const int64_t halves = max_tiles(a.Mq, a.H / a.G, a.n, kRows / 2);
     if (a.splits == 1 && halves * a.G <= kCus) {
         a.tiles = (int)halves;

@@ -134,6 +134,7 @@ CASES = {
     "parts last, causal": dict(qs=cut(0, 700, 30, 64, 0, 200), ks=cut(100, 2500, 3000, 64, 700, 500), H=6, G=3, D=104, causal=True,
                                prefix=[5, 2000, 0, 7, 1, 100]),
     "parts last, none cut": dict(qs=cut(512, 512, 500, 512), H=4, G=4, D=128, tail=9),
+    "parts last, none cut, more rows": dict(qs=cut(1024, 1024, 1000, 1024), H=4, G=4, D=128, tail=9),
     "many segments": dict(qs=sorted([0] + [i * 37 % 900 for i in range(150)] + [900]), H=2, G=1, D=64),
     "more heads than a tile's rows": dict(qs=cut(3, 1), ks=cut(90, 200), H=300, G=2, D=64, causal=True),
     "sharp": dict(qs=cut(500), H=2, G=2, D=128, sharp=60.0),
