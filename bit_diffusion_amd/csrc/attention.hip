@@ -59,6 +59,9 @@ constexpr int kCus = 256;            // of the GPU
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;         // growth of a maximum, in powers of two, that O is rescaled for
 constexpr float kMost = 65536.f;     // sum of 32 weights past which a row gets a new maximum
+constexpr float kFine = 64.f;        // cap up to which, and |z| up to which above it, a capped score takes the
+constexpr float kBend = 1.5f;        // first form and the second (Rows::capped)
+constexpr float kLargest = 3.402823466e38f;
 
 enum Mod { kPlain = 0, kCap = 1, kBias = 2, kBoth = 3 };
 
@@ -217,20 +220,55 @@ struct Rows {
     int limit;         // keys that the row sees
     int at;            // the key at distance 0
     float slope;       // times log2 e
-    float c0, c1, c2;  // kPlain, kBias: c0 = scale log2 e; with cap: 2 scale log2 e / cap, cap log2 e, 2 cap log2 e
+    float c0, c1, cz;  // scale log2 e; with cap: cap log2 e, 2 scale log2 e / cap
+    bool fine;         // cap <= kFine
+
+    // cap log2 e tanh(y) of 16 products x, y = x scale / cap, z = 2 y log2 e.
+    // Caps up to kFine: cap - 2 cap / (2^z + 1), whose error, 2^-23 of the cap, is 2^-17 of a weight at most where
+    // weights are rounded by 2^-9.  Larger caps, whose error would grow past that: up to |z| = kBend as c0 x
+    // (tanh(y) / y), a polynomial in z^2 (off by 2^-25.4 of it at most), so that what is far below the cap keeps its
+    // relative precision; above as 1 - 2 / (2^|z| + 1), which cancels no more than half.  Which form a score takes
+    // depends on it and the cap alone; where no lane needs the last, it is passed over.  (2 x 2048 rows of 8 heads of
+    // 128, cap 50: 55.1 us, with the choice of a form 57.0; cap 65: the first form 55.3, the second 62.5; scores of
+    // up to twice the cap 66.6 and, where most waves need the last, 89.6.)
+    __device__ __forceinline__ void capped(f32x16& s) const {
+        const auto each = [&](auto form) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = form(s[i], s[i] * cz);
+        };
+        if (fine) {
+            const float c2 = 2.f * c1;
+            each([&](float, float z) { return c1 - c2 * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(z) + 1.f); });
+            return;
+        }
+        const auto small = [&](float x, float z) {
+            const float w = z * z;
+            const float p = fmaf(fmaf(fmaf(fmaf(3.5228786e-06f, w, -9.168231e-05f), w, 0.0019222912f), w, -0.040037446f), w, 1.f);
+            return x * c0 * p;
+        };
+        const auto any = [&](float x, float z) {
+            const float t = c1 * fmaf(-2.f, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(fabsf(z)) + 1.f), 1.f);
+            const float below = small(x, z), above = copysignf(t, z);
+            return fabsf(z) > kBend ? above : below;
+        };
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(s[i]));
+        if (__any(most * cz > kBend)) each(any);
+        else each(small);
+    }
 
     // scores of 32 keys from key0 on to the exponent's domain
     template <bool MASK>
     __device__ __forceinline__ void score(f32x16& s, int key0, int h) const {
         const float far = (float)(key0 + 4 * h - at);
         const int seen = limit - key0 - 4 * h;
+        if constexpr ((MOD & kCap) != 0) capped(s);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int key = 8 * (i >> 2) + (i & 3);   // from the lane's first one on
             float x = s[i];
-            if constexpr ((MOD & kCap) != 0)
-                x = c1 - c2 * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * c0) + 1.f);
-            else if constexpr (MOD == kBias) x *= c0;
+            if constexpr (MOD == kBias) x *= c0;
             if constexpr ((MOD & kBias) != 0) x = fmaf(-slope, fabsf(far + (float)key), x);
             if constexpr (MASK) x = key < seen ? x : -INFINITY;
             s[i] = x;
@@ -514,9 +552,13 @@ __global__ __launch_bounds__(kThreads, 2 / SHARE) void attention_kernel(Attentio
     w.at = pos + limit.off;
     w.slope = (MOD & kBias) != 0 ? a.slopes[head] * kLog2e : 0.f;
     w.c0 = a.scale * kLog2e;
-    w.c1 = a.cap * kLog2e;
-    w.c2 = 2.f * w.c1;
-    if ((MOD & kCap) != 0) w.c0 *= 2.f / a.cap;
+    w.c1 = w.cz = 0.f;
+    w.fine = __float_as_int(a.cap) <= __float_as_int(kFine);   // of positive floats, on the scalar unit
+    if ((MOD & kCap) != 0) {
+        w.c1 = fminf(a.cap * kLog2e, kLargest);
+        // a tiny cap: 0 stays 0, what is not gives the cap
+        w.cz = fminf(w.fine ? w.c0 * (2.f / a.cap) : 2.f * (w.c0 / a.cap), kLargest);
+    }
     const uint16_t* qp = (const uint16_t*)a.q + (t.q0 + pos) * a.q_stride + (int64_t)head * D;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {

@@ -527,7 +527,8 @@ svdq_status svdq_rotary(int64_t M, int32_t n_q_heads, int32_t n_k_heads, int32_t
  * zeros.  q, k and v are bf16; scores, the sums and the result before its rounding are fp32, the
  * weights rounded to bf16.  They are taken against a score that may be 16 powers of two below the
  * largest (sums of |v| over a row's keys must stay 2^-16 below fp32's range).
- *   scale      finite and positive.  cap finite, 0: none.
+ *   scale      finite and positive.  cap finite, 0: none; a capped score is off by 2^-23 of the cap where
+ *              that is 64 or less, else by a few roundings of its own.
  *   mask       svdq_mask: SVDQ_MASK_NONE all keys of the segment (rows of an image see one another);
  *              SVDQ_MASK_CAUSAL keys j <= i + d, and all j < prefix[s] (a prompt in front of it, or
  *              the rows of an image that see one another).
