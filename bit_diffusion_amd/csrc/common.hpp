@@ -41,6 +41,13 @@ __device__ __forceinline__ float wave_max_xor(float v, int mask) {
     return fmaxf(v, __shfl_xor(v, mask, kWave));
 }
 
+// 1 / sqrt(x), x >= 0, by the hardware's rsq (about 1 ulp), which takes subnormal numbers for 0.
+__device__ __forceinline__ float rsqrt_hw(float x) {
+    const bool tiny = x < 0x1p-126f;
+    const float r = __builtin_amdgcn_rsqf(tiny ? x * 0x1p64f : x);
+    return tiny ? r * 0x1p32f : r;
+}
+
 // Lane moves by DPP (a few cycles where a shuffle through LDS takes a hundred): lane i gets
 // `src` of lane i - N of its row of 16 (kShr + N), of the row before's last lane (kBcast15, rows 1
 // and 3) or of lane 31 (kBcast31, rows 2 and 3), and `old` where there is no such lane.  Joining

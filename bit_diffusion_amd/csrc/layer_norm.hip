@@ -224,7 +224,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_kernel(LayerNormArgs a, i
             sync();
             const float off = total(1) / c_count;
             const float var = fmaxf(fmaf(-off, off, total(2) / c_count), 0.f);
-            const float rstd = __builtin_amdgcn_rsqf(var + a.eps);
+            const float rstd = rsqrt_hw(var + a.eps);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = (v * T + tid) * VEC;

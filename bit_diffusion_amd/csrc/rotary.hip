@@ -160,7 +160,7 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int per)
             for (int n = 0; n < NV; ++n)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) s = fmaf(x[n][j], x[n][j], s);
-            s = __builtin_amdgcn_rsqf(fmaf(group_sum<LANES>(s), inv_d, a.eps));
+            s = rsqrt_hw(fmaf(group_sum<LANES>(s), inv_d, a.eps));
             if ((q ? a.q_weight : a.k_weight) != nullptr) {
 #pragma unroll
                 for (int n = 0; n < NV; ++n)
@@ -263,7 +263,7 @@ __global__ __launch_bounds__(kThreads) void rotary_pairs_kernel(RotaryArgs a, in
                 s = fmaf(x[n].x, x[n].x, s);
                 s = fmaf(x[n].y, x[n].y, s);
             }
-            s = __builtin_amdgcn_rsqf(fmaf(group_sum<LANES>(s), inv_d, a.eps));
+            s = rsqrt_hw(fmaf(group_sum<LANES>(s), inv_d, a.eps));
             if ((q ? a.q_weight : a.k_weight) != nullptr) {
 #pragma unroll
                 for (int n = 0; n < NP; ++n) {
