@@ -290,7 +290,8 @@ void launch(const RotaryArgs& a, hipStream_t st) {
     const int heads = a.q_heads + a.k_heads, vecs = (a.halves ? a.D / 2 : a.D) / 8;
     const int lanes = a.vec ? (vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32) : a.D <= 128 ? 16 : 32, at_once = kThreads / lanes;
     const int64_t rows = std::min<int64_t>(a.M / kCus, (kPerGroup * at_once + heads - 1) / heads);
-    const int per = (int)std::min<int64_t>(kRows, std::max<int64_t>(1, rows));
+    // two at least where one each would be 2^24 workgroups: a launch has fewer than 2^32 threads
+    const int per = (int)std::min<int64_t>(kRows, std::max<int64_t>(a.M > (int64_t)1 << 23 ? 2 : 1, rows));
     const dim3 grid((unsigned)((a.M + per - 1) / per)), block(kThreads);
     if (!a.vec) {
         auto pairs = [&](auto n, auto np) {
