@@ -476,7 +476,8 @@ __device__ __forceinline__ void step(Rows<NC, MOD>& w, int key0, uint32_t kb, ui
     }
 }
 
-constexpr float kDone = -1.f;   // in the place of a row's first sum: its result is written
+// in the place of a row's sum: of the first part, its result is written; this part has no keys and no O
+constexpr float kDone = -1.f, kNone = -2.f;
 
 // Where a split's O, maximum and sum of row (position m, head h) stand in the workspace.
 __device__ __forceinline__ int64_t part_row(const AttentionArgs& a, int split, int64_t m, int h) {
@@ -679,7 +680,7 @@ __global__ __launch_bounds__(kThreads, 2 / SHARE) void attention_kernel(Attentio
         float* ml = (float*)a.work + all * D + at * 2;
         if (h == 0) {
             ml[0] = MOD == kPlain ? w.m * w.c0 : w.m;
-            ml[1] = joined ? w.l : kDone;
+            ml[1] = !joined ? kDone : first < last ? w.l : kNone;
         }
         if (joined && first < last) {
             float* o = (float*)a.work + at * D;
@@ -717,7 +718,7 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs 
     const int64_t m = r / a.H, head = r - m * a.H;
     const float* o = (const float*)a.work + r * a.D;
     const float2* ml = (const float2*)((const float*)a.work + all * a.splits * a.D) + r;
-    const float2 mine = lane < a.splits ? ml[all * lane] : make_float2(-INFINITY, 0.f);
+    const float2 mine = lane < a.splits ? ml[all * lane] : make_float2(-INFINITY, kNone);
     const bool live = m >= a.q_start[0] && m < a.q_start[a.n] &&
                       __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(mine.y))) != kDone;
     if (!live) return;                     // all of a row's waves
@@ -728,7 +729,9 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs 
     float l = mine.y * f;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) l += __shfl_xor(l, d, kWave);
-    const int parts = 64 - __clzll((long long)__ballot(!(f == 0.f)));   // those past hold nothing
+    // those with keys, the first ones; also where a part's weights are 0 against the others', for its O may
+    // be no number
+    const int parts = __popcll(__ballot(mine.y != kNone));
     float2 sum = make_float2(0.f, 0.f);
     if (2 * lane < a.D) {
         for (int s = wave % PER; s < parts; s += 4 * PER) {   // four loads in flight
