@@ -1003,6 +1003,8 @@ svdq_status svdq_attention(int64_t Mq, int64_t Mkv, int32_t n_heads, int32_t n_k
     SVDQ_TRY(check_attention(Mq, Mkv, n_heads, n_kv_heads, head_dim, n_segments));
     if (!(std::isfinite(scale) && scale > 0.0f))
         return fail(SVDQ_ERR_INVALID_ARG, "scale = %g must be finite and positive", (double)scale);
+    if (scale > 0x1p127f)
+        return fail(SVDQ_ERR_UNSUPPORTED_CONFIG, "scale = %g exceeds the supported maximum 2^127", (double)scale);
     if (!(std::isfinite(cap) && cap >= 0.0f))
         return fail(SVDQ_ERR_INVALID_ARG, "cap = %g must be finite and not negative", (double)cap);
     if (mask != SVDQ_MASK_NONE && mask != SVDQ_MASK_CAUSAL)

@@ -479,6 +479,10 @@ __device__ __forceinline__ void step(Rows<NC, MOD>& w, int key0, uint32_t kb, ui
 // in the place of a row's sum: of the first part, its result is written; this part has no keys and no O
 constexpr float kDone = -1.f, kNone = -2.f;
 
+// 1 / l for a row's sum l and maximum m.  A row that sees no key, or only scores of minus infinity, gives zeros; one
+// whose maximum left the range when multiplied by scale log2 e has lost its weights, and is no number.
+__device__ __forceinline__ float inverse(float l, float m) { return l == 0.f && m == -INFINITY ? 0.f : 1.f / l; }
+
 // Where a split's O, maximum and sum of row (position m, head h) stand in the workspace.
 __device__ __forceinline__ int64_t part_row(const AttentionArgs& a, int split, int64_t m, int h) {
     return ((int64_t)split * a.Mq + m) * a.H + h;
@@ -694,7 +698,7 @@ __global__ __launch_bounds__(kThreads, 2 / SHARE) void attention_kernel(Attentio
         }
         if (joined) return;
     }
-    const float inv = w.l == 0.f ? 0.f : 1.f / w.l;   // a row that sees no key gives zeros
+    const float inv = inverse(w.l, w.m);
     uint16_t* op = (uint16_t*)a.out + (t.q0 + pos) * a.out_stride + (int64_t)head * D;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -757,7 +761,7 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs 
         }
     }
     if (wave % PER > 0 || 2 * lane >= a.D) return;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = inverse(l, top);
     *(uint32_t*)((uint16_t*)a.out + m * a.out_stride + head * a.D + 2 * lane) = pack_bf16(sum.x * inv, sum.y * inv);
 }
 

@@ -526,8 +526,9 @@ svdq_status svdq_rotary(int64_t M, int32_t n_q_heads, int32_t n_k_heads, int32_t
  * d = keys of s - rows of s, which puts the last row at the last key.  A row that sees no key gives
  * zeros.  q, k and v are bf16; scores, the sums and the result before its rounding are fp32, the
  * weights rounded to bf16.  They are taken against a score that may be 16 powers of two below the
- * largest (sums of |v| over a row's keys must stay 2^-16 below fp32's range).
- *   scale      finite and positive.  cap finite, 0: none; a capped score is off by 2^-23 of the cap where
+ * largest (sums of |v| over a row's keys must stay 2^-16 below fp32's range).  q . k and t_ij must
+ * stay within 2^127 in size (a row with scores above that is NaN).
+ *   scale      positive, up to 2^127.  cap finite, 0: none; a capped score is off by 2^-23 of the cap where
  *              that is 64 or less, else by a few roundings of its own.
  *   mask       svdq_mask: SVDQ_MASK_NONE all keys of the segment (rows of an image see one another);
  *              SVDQ_MASK_CAUSAL keys j <= i + d, and all j < prefix[s] (a prompt in front of it, or
@@ -547,7 +548,9 @@ svdq_status svdq_rotary(int64_t M, int32_t n_q_heads, int32_t n_k_heads, int32_t
  *              bytes at least (0 where the rows keep the GPU busy without it), 16-byte aligned,
  *              overwritten; calls that may overlap in time need one each.
  * What a row does not see does not change its result, infinities and NaN among it.  A NaN score
- * that a row sees makes the row NaN.
+ * that a row sees makes the row NaN, and a value that is not finite the column that holds it, also
+ * where its weight is 0 in fp32.  Scores of minus infinity weigh nothing; a row that sees no others
+ * gives zeros.
  * head_dim a multiple of 8 up to 128; n_heads a positive multiple of n_kv_heads; Mq up to 2^24 and
  * Mq n_heads below 2^25, Mkv up to 2^30, n_segments up to 2^16 (Mq = 0 or n_segments = 0 enqueues
  * nothing; a buffer without elements may be NULL).  q, k, v and out must be 16-byte aligned, their

@@ -1,5 +1,5 @@
 """svdq_attention: what a row sees reaches it.  Values that are not numbers under weights of 0, scores of
-minus infinity; in calls whose keys are cut in parts and in others."""
+minus infinity, scores past fp32's range; in calls whose keys are cut in parts and in others."""
 import pytest
 import torch
 
@@ -98,6 +98,37 @@ def test_all_scores_minus_infinity(shape):
     c.call()
     torch.cuda.synchronize()
     assert bool((c.out[:c.qs[-1]] == 0.0).all())
+
+
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_scores_at_the_end_of_the_range(shape):
+    """The largest score takes all of the weight up to 2^127; a row with scores past that is no number.  The
+    largest scale, and scores of 2^7."""
+    c = case(shape)
+    c.q.zero_()
+    c.k.zero_()
+    c.q[:, ::c.D] = 2.0 ** 63
+    for i in range(c.n):
+        c.k[c.ks[i], ::c.D] = 2.0 ** 63
+    c.scale = 1.0
+    c.call()
+    torch.cuda.synchronize()
+    for i in range(c.n):
+        out = c.out[c.qs[i]:c.qs[i + 1]].reshape(-1, c.H, c.D)
+        want = c.v[c.ks[i]].reshape(1, c.G, c.D).repeat_interleave(c.H // c.G, 1).expand_as(out)
+        assert torch.equal(out, want)
+    whole = c.out.clone()
+    c.scale = 3.0
+    c.call()
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(c.out[:c.qs[-1]]).all())
+    c.q[:, ::c.D] = 2.0 ** -60
+    for i in range(c.n):
+        c.k[c.ks[i], ::c.D] = 2.0 ** -60
+    c.scale = 2.0 ** 127
+    c.call()
+    torch.cuda.synchronize()
+    assert torch.equal(c.out, whole)
 
 
 @pytest.mark.parametrize("D", [32, 64, 96, 128])
