@@ -184,8 +184,9 @@ __global__ __launch_bounds__(kThreads) void layer_norm_kernel(LayerNormArgs a, i
                 }
             if (kAhead && row + 1 < end) fetch(row + 1);
             // the stream is read again only behind the next linears: kept out of the caches, it leaves them
-            // to what the next one reads (4608 x 3072 bf16: 27.6 -> 22.7 us, with svdq_quantize_act_packed
-            // behind it 50.8 -> 50.7, at 9216 rows 81.0 -> 78.2)
+            // to what the next one reads (bf16 rows of 3072, through the caches and so, us; alone: 4608 rows 27.4
+            // and 26.6, 9216 rows 50.0 and 49.9; with svdq_quantize_act_packed behind: 1024 rows 21.9 and 20.4, 4608
+            // rows 51.1 and 51.4, 9216 rows 79.6 and 77.7)
             if (a.x_out != nullptr) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {

@@ -548,9 +548,9 @@ svdq_status svdq_rotary(int64_t M, int32_t n_q_heads, int32_t n_k_heads, int32_t
  *              bytes at least (0 where the rows keep the GPU busy without it), 16-byte aligned,
  *              overwritten; calls that may overlap in time need one each.
  * What a row does not see does not change its result, infinities and NaN among it.  A NaN score
- * that a row sees makes the row NaN, and a value that is not finite the column that holds it, also
- * where its weight is 0 in fp32.  Scores of minus infinity weigh nothing; a row that sees no others
- * gives zeros.
+ * that a row sees makes the row NaN; a value that is not finite leaves its column of the row not
+ * finite, also where its weight is 0 in fp32.  Scores of minus infinity weigh nothing; a row that sees
+ * no others gives zeros.
  * head_dim a multiple of 8 up to 128; n_heads a positive multiple of n_kv_heads; Mq up to 2^24 and
  * Mq n_heads below 2^25, Mkv up to 2^30, n_segments up to 2^16 (Mq = 0 or n_segments = 0 enqueues
  * nothing; a buffer without elements may be NULL).  q, k, v and out must be 16-byte aligned, their
